@@ -53,6 +53,8 @@ extern "C" {
 #define HS_DEVERR_EMPTY 0x4u      /* decode of a request with no positions: output set to 0 */
 #define HS_DEVERR_TIMEOUT 0x8u    /* a bounded wait inside a kernel gave up */
 #define HS_DEVERR_METADATA 0x10u  /* page table / reverse map found inconsistent */
+#define HS_DEVERR_PAGE 0x40u      /* paged cache: a page id outside [0, n_pages) where a position is held */
+#define HS_DEVERR_OFFSETS 0x80u   /* paged cache: token offsets that decrease or leave [0, n_tok] */
 #define HS_DEVERR_NO_LEAD 0x20u   /* a follower layer of a shared selection was decoded without
                                      its group lead's selection of the same step: output 0 */
 
@@ -391,8 +393,199 @@ int hs_indexer_topk_static(int32_t n_req, int32_t n_max, int32_t d_idx, int32_t 
  */
 int hs_indexer_topk_static_error(int32_t device, uint32_t* out);
 
+/* ==========================================================================
+ * Rotary positions, and a paged cache that stays in HBM.
+ *
+ * The two-tier cache above takes queries and rows whose positions are already
+ * rotated in: hs_rotary_apply rotates them.  Layers that attend to every
+ * position, and requests short enough to stay in HBM, use the paged cache:
+ * hs_paged_append rotates and stores new keys and values, hs_paged_decode
+ * attends one new token per request over them.  None of these calls keeps
+ * anything from one call for the next but what it writes to the caller's
+ * buffers.  Messages of failed
+ * calls: hs_last_error(NULL), of the calling thread.
+ * ======================================================================== */
+#define HS_BF16 0
+#define HS_FP16 1
+#define HS_FP32 2   /* hs_rotary_apply only */
+#define HS_E4M3 3 /* 8-bit e4m3 pages, with one scale per kv head */
+
+/* A [tokens][heads][d] view of 16- or 32-bit elements: element (t, h, i) is at
+ * data + t * token_stride + h * head_stride + i (strides in elements, >= 0). */
+typedef struct hs_heads {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t heads;
+  int32_t _pad;
+} hs_heads_t;
+
+/* Frequencies of a rotation over the first rot_dim elements of a head, pair i of
+ * rot_dim / 2:  f_i = base^(-2 i / rot_dim) radians per position, then by `scaling`:
+ *   HS_ROTARY_PLAIN    f_i
+ *   HS_ROTARY_LINEAR   f_i / factor                         (position interpolation)
+ *   HS_ROTARY_NTK      base * factor^(rot_dim / (rot_dim - 2)) in place of base
+ *   HS_ROTARY_BY_PARTS w_i f_i + (1 - w_i) f_i / factor, where the turns within the
+ *                      original context, t_i = original_context * f_i / (2 pi), give
+ *                      w_i = clamp((t_i - low) / (high - low), 0, 1)  (YaRN)
+ * magnitude multiplies every rotated value; 0 takes the kind's own: 0.1 ln(factor) + 1
+ * for HS_ROTARY_BY_PARTS with factor > 1, else 1. */
+#define HS_ROTARY_PLAIN 0
+#define HS_ROTARY_LINEAR 1
+#define HS_ROTARY_NTK 2
+#define HS_ROTARY_BY_PARTS 3
+typedef struct hs_rotary_config {
+  double base;             /* > 1 */
+  double factor;           /* >= 1; not read by HS_ROTARY_PLAIN */
+  double original_context; /* HS_ROTARY_BY_PARTS: > 0 */
+  double low;              /* HS_ROTARY_BY_PARTS: turns at and below which f_i / factor is taken */
+  double high;             /* HS_ROTARY_BY_PARTS: turns at and above which f_i stays; > low */
+  double magnitude;        /* >= 0 */
+  int32_t rot_dim;         /* even, in [2, 1024] */
+  int32_t scaling;         /* HS_ROTARY_* */
+} hs_rotary_config_t;
+
+/*
+ * hs_rotary_table — on the host, the table a rotation is applied with.
+ *   inv_freq : NULL, or host double [rot_dim / 2]: frequencies in radians per position,
+ *              finite and >= 0, in place of the formulas (of cfg then only rot_dim and
+ *              magnitude are read)
+ *   turns    : host uint64 [rot_dim / 2]: f_i / (2 pi) as a fraction of 2^64.  A position
+ *              times an entry, modulo 2^64, is the angle as a fraction of a turn: exact in
+ *              integers for every int32 position (the error is that of the entry itself,
+ *              about 2^-55 turns per position)
+ *   magnitude: host float, the factor on rotated values
+ */
+int hs_rotary_table(const hs_rotary_config_t* cfg, const double* inv_freq, uint64_t* turns, float* magnitude);
+
+typedef struct hs_rotary {
+  const uint64_t* turns; /* dev [rot_dim / 2], a copy of hs_rotary_table's */
+  int32_t rot_dim;       /* even, in [2, d] */
+  int32_t interleaved;   /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2 i, 2 i + 1) */
+  int32_t transpose;     /* 1: the transposed rotation (angles negated): the gradient's, and, where
+                            magnitude is 1, the inverse */
+  float magnitude;
+} hs_rotary_t;
+
+/*
+ * hs_rotary_apply — out = magnitude * R(position * f) in, for one or two tensors of
+ * the same tokens (a step's queries and keys) in one launch; elements from rot_dim
+ * to d are copied.  Stream-ordered, capturable.
+ *   type     : HS_BF16, HS_FP16 or HS_FP32; arithmetic in 32 bits, rounded once
+ *   d        : elements of a head, in [2, 1024]
+ *   n_tok    : tokens (0: a no-op);  positions: dev int32 [n_tok]
+ *   in, out  : n_views (1 or 2) views each; out[i] is in[i] itself (same data and
+ *              strides: in place) or memory apart from it.  Output elements must be
+ *              distinct.  Any alignment of the element type; 16-byte aligned views
+ *              and strides take the faster loads
+ *   device   : CUDA device of the buffers (the current device is left as it was)
+ */
+int hs_rotary_apply(const hs_rotary_t* rot, int32_t type, int32_t d, int32_t n_tok, const int32_t* positions,
+                    int32_t n_views, const hs_heads_t* in, const hs_heads_t* out, int32_t device, void* stream);
+
+/*
+ * The paged cache.  Per layer: pages [n_pages][2][h_kv][page_size][d], a page's keys
+ * then its values, each kv head's rows of consecutive positions together.  Position
+ * n of request r is row n % page_size of page page_table[r][n / page_size].
+ * The page size must be 16, 32, 64, 128 or 256; d 64, 128 or 256 (keys and values
+ * alike); h_q % h_kv == 0.  Queries, new keys and values and outputs are `type`
+ * (HS_BF16 or HS_FP16); pages are the same type or HS_E4M3: then they hold
+ * value / kv_scale[layer][0 key, 1 value][kv head], saturated to +-448.
+ */
+typedef struct hs_paged_config {
+  int32_t n_layers;
+  int32_t n_pages;       /* pages per layer */
+  int32_t page_size;
+  int32_t max_requests;  /* rows of page_table and of lengths, 1 .. 4096 */
+  int32_t max_pages;     /* columns of page_table; max_pages * page_size <= 2^22 positions */
+  int32_t h_q;
+  int32_t h_kv;
+  int32_t d;
+  int32_t type;
+  int32_t page_type;
+  int32_t window;        /* 0: all positions; else the last `window` of them are attended */
+  int32_t device;
+  float softmax_scale;   /* 0: 1 / sqrt(d) */
+  int32_t _pad;
+} hs_paged_config_t;
+
+typedef struct hs_paged hs_paged_t;
+
+/*
+ * hs_paged_create — check `cfg` and describe the caller's pool.  Allocates nothing on
+ * the device: every buffer is the caller's until hs_paged_destroy (NULL is a no-op).
+ *   pages     : dev [n_layers][n_pages][2][h_kv][page_size][d], 16-byte aligned; what it
+ *               holds is not read here
+ *   kv_scale  : dev float [n_layers][2][h_kv], positive; HS_E4M3 pages only (else NULL)
+ *   error_word: dev uint32, zeroed by the caller: the calls set HS_DEVERR_* bits in it
+ */
+int hs_paged_create(const hs_paged_config_t* cfg, void* pages, const float* kv_scale, uint32_t* error_word,
+                    hs_paged_t** out);
+void hs_paged_destroy(hs_paged_t* h);
+
+/*
+ * hs_paged_append — store new tokens of each request (stream-ordered, capturable).
+ *   req_ids     : dev int32 [n_req] distinct request ids, or NULL for 0 .. n_req-1
+ *   n_tok       : rows of q, q_out, k and v
+ *   tok_offsets : dev int32 [n_req + 1], or NULL.  Request i of the call takes rows
+ *                 tok_offsets[i] .. tok_offsets[i+1]-1 (none where they are equal); rows
+ *                 before the first and from the last offset on belong to no request and
+ *                 are neither read nor written.  NULL: n_tok / n_req rows each (n_tok must
+ *                 be a multiple of n_req)
+ *   page_table  : dev int32 [max_requests][max_pages]
+ *   lengths     : dev int32 [max_requests]: positions held before the call
+ *   next_lengths: dev int32 [max_requests] or NULL, apart from lengths: receives
+ *                 lengths + new tokens for the requests of the call
+ *   rot         : rotation of k (and q) at the token's position, or NULL for none
+ *                 (its transpose field must be 0)
+ *   q, q_out    : views of the step's queries and of their rotated values, or both
+ *                 NULL; in place or apart as for hs_rotary_apply; needs rot
+ *   k, v        : views of the new keys and values (h_kv heads)
+ * The row of token j of request r takes position lengths[r] + j.  `lengths` itself is
+ * not changed, so every layer of a step is given the same one, and a call that is
+ * repeated rewrites the same rows.  A request with a bad id (HS_DEVERR_REQ_RANGE), a
+ * length below 0 or tokens past max_pages * page_size (HS_DEVERR_CAPACITY) is skipped
+ * whole (its next length is its length); a position whose page id is out of range is
+ * not stored (HS_DEVERR_PAGE).  Offsets that decrease or leave [0, n_tok]
+ * (HS_DEVERR_OFFSETS) give their request no tokens.
+ */
+int hs_paged_append(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* req_ids, int32_t n_tok,
+                    const int32_t* tok_offsets, const int32_t* page_table, const int32_t* lengths,
+                    int32_t* next_lengths, const hs_rotary_t* rot, const hs_heads_t* q, const hs_heads_t* q_out,
+                    const hs_heads_t* k, const hs_heads_t* v, void* stream);
+
+/*
+ * hs_paged_decode — attention of one token per request over its cached positions
+ * (stream-ordered, capturable): with N = lengths[r] and the last min(N, window) positions,
+ *   o_h = sum_n softmax_n(softmax_scale * q_h . K_n) V_n,   kv head floor(h * h_kv / h_q).
+ *   lengths  : dev int32 [max_requests], the new token's own position counted
+ *   q        : view of [n_req][h_q][d], 16-byte aligned rows
+ *   out      : dev [n_req][h_q][d] (type), 16-byte aligned
+ *   lse      : dev float [n_req][h_q] or NULL: ln sum_n exp(softmax_scale * q_h . K_n)
+ *   workspace: dev, hs_paged_workspace_bytes(h) bytes, 256-byte aligned; its contents
+ *              matter only within the call: calls that may overlap need one each
+ * A length of 0 (a padded row of a batch) gives out = 0, lse = -inf.  So does a request
+ * with a bad id (HS_DEVERR_REQ_RANGE) or a length outside [0, max_pages * page_size]
+ * (HS_DEVERR_CAPACITY).  Positions on a page whose id is out of range are left out
+ * (HS_DEVERR_PAGE).  Rows of a page at and behind the length are never used, whatever
+ * they hold.  Scores, the softmax and the sums are in 32 bits; the weights that multiply
+ * 16-bit (8-bit) values are rounded to the page type (to 16 bits).
+ * The result does not depend on which page ids hold a request, and is the same bits
+ * from call to call.
+ */
+int64_t hs_paged_workspace_bytes(const hs_paged_t* h);
+int hs_paged_decode(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* req_ids, const int32_t* page_table,
+                    const int32_t* lengths, const hs_heads_t* q, void* out, float* lse, void* workspace,
+                    void* stream);
+
+/* hs_paged_error — synchronise the device and read the handle's error word
+ * (HS_DEVERR_* bits since the caller zeroed it).  HS_ERR_DEVICE (with *out set)
+ * when it is non-zero. */
+int hs_paged_error(hs_paged_t* h, uint32_t* out);
+
 /* hs_last_error — message of the handle's last failed call ("" if none); with
- * h == NULL, the message of the last failed hs_create in this thread. */
+ * h == NULL, the message of the last failed hs_create, hs_rotary_* or hs_paged_* call
+ * in this thread. */
 const char* hs_last_error(const hs_handle_t* h);
 
 /* hs_status_string — static name of a status code. */

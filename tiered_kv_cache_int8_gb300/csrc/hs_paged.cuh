@@ -1,0 +1,92 @@
+// Shared between the rotary / append kernels (hs_rotary.cu), the paged
+// attention kernels (hs_paged_attention.cu) and their host side (hs_paged.cu).
+#ifndef HS_PAGED_CUH_
+#define HS_PAGED_CUH_
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <vector>
+
+#include "hs_internal.cuh"
+
+namespace hs {
+
+constexpr int PG_MAX_REQUESTS = 4096;
+constexpr int PG_MAX_POSITIONS = 1 << 22;
+
+inline size_t type_bytes(int t) { return t == HS_FP32 ? 4 : t == HS_E4M3 ? 1 : 2; }
+
+// One tensor of a rotation or append: rows of `heads` heads per token.
+enum ViewKind { VIEW_ROTATE = 0, VIEW_KEYS = 1, VIEW_VALUES = 2 };
+struct RowView {
+  const void* in;
+  void* out;          // VIEW_ROTATE only
+  int64_t in_ts, in_hs, out_ts, out_hs;
+  int32_t heads;
+  int32_t kind;
+};
+
+struct RotateParams {
+  RowView v[3];
+  int32_t n_views;
+  int32_t rows;          // heads of all views together
+  int32_t d;
+  int32_t n_tok;
+  int32_t tok_per_cta;
+  int32_t rot_dim;       // 0: no rotation
+  int32_t items;         // work items of a row
+  float magnitude;
+  float sign;            // -1: the transposed rotation
+  const uint64_t* turns;
+  const int32_t* positions;   // hs_rotary_apply
+  // append
+  const int32_t* req_ids;
+  const int32_t* tok_offsets;
+  const int32_t* page_table;
+  const int32_t* lengths;
+  int32_t* next_lengths;
+  int32_t n_req, tok_per_req, max_requests, max_pages, n_pages, page_size, page_shift, h_kv;
+  unsigned char* pages;       // of the layer
+  const float* kv_scale;      // of the layer
+  unsigned int* dev_error;
+};
+
+struct PagedDecodeParams {
+  const int32_t* req_ids;
+  const int32_t* page_table;
+  const int32_t* lengths;
+  const void* q;
+  int64_t q_ts, q_hs;
+  void* out;
+  float* lse;
+  float* ws;
+  const unsigned char* pages;  // of the layer
+  const float* kv_scale;       // of the layer, or null
+  unsigned int* dev_error;
+  int32_t n_req, max_requests, max_pages, n_pages, page_size, page_shift;
+  int32_t h_q, h_kv, group, d, window, type, page_type;
+  int32_t grid;
+  float scale_log2;
+};
+
+cudaError_t launch_rotate(const RotateParams& p, int type, int page_type, bool append, bool interleaved,
+                          bool wide, cudaStream_t st);
+cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t st);
+int64_t paged_workspace_bytes(int h_q, int h_kv, int d, int num_sms);
+
+}  // namespace hs
+
+struct hs_paged {
+  hs_paged_config_t cfg;
+  void* pages = nullptr;
+  const float* kv_scale = nullptr;
+  unsigned int* dev_error = nullptr;
+  int num_sms = 0;
+  int page_shift = 0;
+  float scale_log2 = 0.f;
+};
+
+#endif  // HS_PAGED_CUH_

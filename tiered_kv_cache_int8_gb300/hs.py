@@ -27,6 +27,11 @@ HS_DEVERR_EMPTY = 0x4
 HS_DEVERR_TIMEOUT = 0x8
 HS_DEVERR_METADATA = 0x10
 HS_DEVERR_NO_LEAD = 0x20
+HS_DEVERR_PAGE = 0x40
+HS_DEVERR_OFFSETS = 0x80
+
+HS_BF16, HS_FP16, HS_FP32, HS_E4M3 = 0, 1, 2, 3
+HS_ROTARY_PLAIN, HS_ROTARY_LINEAR, HS_ROTARY_NTK, HS_ROTARY_BY_PARTS = 0, 1, 2, 3
 
 HS_K_APPEND, HS_K_SELECT, HS_K_ATTENTION, HS_K_COUNT = 0, 1, 2, 3
 
@@ -40,7 +45,9 @@ KERNEL_NAMES = ("append", "select", "attention")
 EXPORTED = ("hs_create", "hs_destroy", "hs_append", "hs_decode_layer", "hs_stats", "hs_snapshot",
             "hs_reset_request", "hs_set_timing", "hs_kernel_times", "hs_last_error",
             "hs_status_string", "hs_row_elems", "hs_indexer_topk_static",
-            "hs_indexer_topk_static_error")
+            "hs_indexer_topk_static_error", "hs_rotary_table", "hs_rotary_apply", "hs_paged_create",
+            "hs_paged_destroy", "hs_paged_append", "hs_paged_workspace_bytes", "hs_paged_decode",
+            "hs_paged_error")
 
 
 class HsConfig(ctypes.Structure):
@@ -65,6 +72,27 @@ class HsStats(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {n: int(getattr(self, n)) for n, _ in self._fields_ if n != "_pad"}
+
+
+class HsHeads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("_pad", ctypes.c_int32)]
+
+
+class HsRotaryConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("base", "factor", "original_context", "low", "high", "magnitude")] + [
+        ("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32)]
+
+
+class HsRotary(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("transpose", ctypes.c_int32), ("magnitude", ctypes.c_float)]
+
+
+class HsPagedConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "n_layers", "n_pages", "page_size", "max_requests", "max_pages", "h_q", "h_kv", "d", "type", "page_type",
+        "window", "device")] + [("softmax_scale", ctypes.c_float), ("_pad", ctypes.c_int32)]
 
 
 class HsError(RuntimeError):
@@ -112,6 +140,23 @@ def lib():
         L.hs_indexer_topk_static.restype = ctypes.c_int
         L.hs_indexer_topk_static_error.argtypes = [I32, P(ctypes.c_uint32)]
         L.hs_indexer_topk_static_error.restype = ctypes.c_int
+        L.hs_rotary_table.argtypes = [P(HsRotaryConfig), P(ctypes.c_double), P(ctypes.c_uint64), P(ctypes.c_float)]
+        L.hs_rotary_table.restype = ctypes.c_int
+        L.hs_rotary_apply.argtypes = [P(HsRotary), I32, I32, I32, VP, I32, P(HsHeads), P(HsHeads), I32, VP]
+        L.hs_rotary_apply.restype = ctypes.c_int
+        L.hs_paged_create.argtypes = [P(HsPagedConfig), VP, VP, VP, P(VP)]
+        L.hs_paged_create.restype = ctypes.c_int
+        L.hs_paged_destroy.argtypes = [VP]
+        L.hs_paged_destroy.restype = None
+        L.hs_paged_append.argtypes = [VP, I32, I32, VP, I32, VP, VP, VP, VP, P(HsRotary), P(HsHeads), P(HsHeads),
+                                      P(HsHeads), P(HsHeads), VP]
+        L.hs_paged_append.restype = ctypes.c_int
+        L.hs_paged_workspace_bytes.argtypes = [VP]
+        L.hs_paged_workspace_bytes.restype = ctypes.c_int64
+        L.hs_paged_decode.argtypes = [VP, I32, I32, VP, VP, VP, P(HsHeads), VP, VP, VP, VP]
+        L.hs_paged_decode.restype = ctypes.c_int
+        L.hs_paged_error.argtypes = [VP, P(ctypes.c_uint32)]
+        L.hs_paged_error.restype = ctypes.c_int
         _LIB = L
     return _LIB
 

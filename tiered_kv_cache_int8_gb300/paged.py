@@ -1,0 +1,331 @@
+"""Rotary positions and the paged cache: the binding of hs_rotary_* and hs_paged_*
+(include/hs.h states what they compute).
+
+Every step runs in the library's CUDA kernels.  Calls run on the current stream
+of their device, or on ``stream``; a call's own outputs and workspace are
+allocated on that stream.  ``ValueError`` for tensors of a wrong shape, type or
+device, ``HsError`` for what the library refuses.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from .hs import (HS_BF16, HS_E4M3, HS_ERR_DEVICE, HS_FP16, HS_FP32, HS_OK, HS_ROTARY_BY_PARTS, HS_ROTARY_LINEAR,
+                 HS_ROTARY_NTK, HS_ROTARY_PLAIN, HsError, HsHeads, HsPagedConfig, HsRotary, HsRotaryConfig, lib)
+
+TYPES = {torch.bfloat16: HS_BF16, torch.float16: HS_FP16, torch.float32: HS_FP32, torch.float8_e4m3fn: HS_E4M3}
+SCALINGS = {"linear": HS_ROTARY_LINEAR, "ntk": HS_ROTARY_NTK, "by_parts": HS_ROTARY_BY_PARTS}
+
+
+def _check(rc: int):
+    if rc != HS_OK:
+        raise HsError(rc, lib().hs_last_error(None).decode())
+
+
+def _need(ok: bool, why: str):
+    if not ok:
+        raise ValueError(why)
+
+
+def _heads(name: str, x, device, dtype, d: int | None = None, heads: int | None = None) -> HsHeads:
+    """The [tokens, heads, d] view of a tensor whose last dimension is dense."""
+    if x.dim() != 3 or x.device != device or x.dtype != dtype:
+        raise ValueError(f"{name} must be [tokens, heads, d] {dtype} on {device}, not {list(x.shape)} {x.dtype} on {x.device}")
+    _, h, e = x.shape
+    if (d is not None and e != d) or (heads is not None and h != heads):
+        raise ValueError(f"{name} must be [tokens, {heads}, {d}], not {list(x.shape)}")
+    ts, hs, es = x.stride()
+    if es != 1 and e > 1:
+        raise ValueError(f"{name}'s last dimension must be dense")
+    return HsHeads(x.data_ptr(), ts, hs, h, 0)
+
+
+def _ints(name: str, x, device, shape):
+    if x.dtype != torch.int32 or x.device != device or tuple(x.shape) != tuple(shape) or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device}, "
+                         f"not {list(x.shape)} {x.dtype} on {x.device}")
+    return x.data_ptr()
+
+
+class _On:
+    """The stream of a call: the current one, or a given one, on which the call's
+    own tensors are then allocated and the given tensors are marked as used."""
+
+    def __init__(self, stream, device, tensors):
+        self.ctx = None
+        if stream is None:
+            self.raw = torch.cuda.current_stream(device).cuda_stream
+            return
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        self.raw = stream.cuda_stream
+        if self.raw != torch.cuda.current_stream(device).cuda_stream:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+            self.ctx = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.raw
+
+    def __exit__(self, *a):
+        if self.ctx is not None:
+            self.ctx.__exit__(*a)
+
+
+class Rotary:
+    """A rotation of the first ``rot_dim`` elements of a head by position * frequency.
+
+    interleaved : pairs (2i, 2i+1) instead of (i, i + rot_dim / 2)
+    scaling     : None, or {"kind": "linear" | "ntk" | "by_parts", "factor": f} and, for
+                  "by_parts", "original_context", "low" (default 1) and "high" (default 32)
+    inv_freq    : frequencies (radians per position, rot_dim / 2 of them) in place of the formulas
+    magnitude   : the factor on rotated values; None takes the kind's own
+    """
+
+    def __init__(self, rot_dim: int, *, base: float = 10000.0, interleaved: bool = False, scaling: dict | None = None,
+                 inv_freq=None, magnitude: float | None = None, device: int = 0):
+        kind, sc = HS_ROTARY_PLAIN, dict(scaling or {})
+        if sc:
+            name = sc.pop("kind", None)
+            _need(name in SCALINGS, f"scaling's kind must be one of {sorted(SCALINGS)}")
+            kind = SCALINGS[name]
+            known = {"factor"} | ({"original_context", "low", "high"} if kind == HS_ROTARY_BY_PARTS else set())
+            _need(set(sc) <= known and "factor" in sc and (kind != HS_ROTARY_BY_PARTS or "original_context" in sc),
+                  f"scaling of kind {name} takes {sorted(known)}")
+        _need(magnitude is None or magnitude > 0, "magnitude must be > 0")
+        cfg = HsRotaryConfig(base, sc.get("factor", 1.0), sc.get("original_context", 0.0), sc.get("low", 1.0),
+                             sc.get("high", 32.0), magnitude or 0.0, rot_dim, kind)
+        n = max(1, rot_dim // 2)
+        freqs = None
+        if inv_freq is not None:
+            values = [float(f) for f in inv_freq]
+            _need(len(values) == n, f"inv_freq must have rot_dim / 2 = {n} entries")
+            freqs = (ctypes.c_double * n)(*values)
+        turns = (ctypes.c_uint64 * n)()
+        mag = ctypes.c_float(0.0)
+        _check(lib().hs_rotary_table(ctypes.byref(cfg), freqs, turns, ctypes.byref(mag)))
+        self.rot_dim, self.interleaved, self.magnitude = rot_dim, bool(interleaved), float(mag.value)
+        self.turns = list(turns)     # as fractions of 2^64 of a turn per position
+        self.device = torch.device("cuda", device)
+        as_signed = [t - (1 << 64) if t >> 63 else t for t in self.turns]
+        self._table = torch.tensor(as_signed, dtype=torch.int64, device=self.device)
+        self.plan = tuple(HsRotary(self._table.data_ptr(), rot_dim, int(interleaved), t, mag.value) for t in (0, 1))
+        # the table's copy is on the stream of the creation; calls may be on any
+        torch.cuda.current_stream(self.device).synchronize()
+
+    def apply(self, positions, *xs, out=None, transpose: bool = False, stream=None):
+        """Rotates one or two tensors [tokens, heads, d] (a step's queries and keys) of
+        the tokens at ``positions`` (int32 [tokens]); returns the rotated tensor(s).
+
+        out       : the tensor(s) to write: the inputs themselves (in place) or others
+        transpose : the transposed rotation (angles negated): what takes a gradient of
+                    the rotated values back; the inverse where magnitude is 1
+        """
+        _need(len(xs) in (1, 2), "apply takes one or two tensors")
+        dev, x0 = self.device, xs[0]
+        dtype = x0.dtype
+        _need(dtype in (torch.bfloat16, torch.float16, torch.float32), f"no rotation of {dtype}")
+        views = [_heads("x", x, dev, dtype) for x in xs]
+        n, d = int(x0.shape[0]), int(x0.shape[2])
+        _need(all(x.shape[0] == n and x.shape[2] == d for x in xs), "the tensors have different tokens or widths")
+        pos = _ints("positions", positions, dev, (n,))
+        if out is not None:
+            outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
+            _need(len(outs) == len(xs) and all(o.shape == x.shape for o, x in zip(outs, xs)),
+                  "out must have the shapes of the inputs")
+        with _On(stream, dev, (positions, *xs, *(outs if out is not None else ()))) as raw:
+            if out is None:
+                outs = tuple(torch.empty(x.shape, dtype=dtype, device=dev) for x in xs)
+            k = len(xs)
+            _check(lib().hs_rotary_apply(ctypes.byref(self.plan[1 if transpose else 0]), TYPES[dtype], d, n, pos, k,
+                                         (HsHeads * k)(*views),
+                                         (HsHeads * k)(*[_heads("out", o, dev, dtype) for o in outs]),
+                                         dev.index, raw))
+        return outs[0] if k == 1 else outs
+
+
+class PagedKVCache:
+    """A paged cache of keys and values in HBM, its append and its one-token attention.
+
+    pages      : [n_layers, n_pages, 2, h_kv, page_size, d] (given, or allocated here)
+    page_table : int32 [max_requests, max_pages], page ids of each request (-1: none);
+                 written by ``reserve`` / ``release``, or by the caller, who then hands
+                 out the pages
+    lengths    : int32 [max_requests], positions held before the step
+    next_lengths : with the tokens that ``append`` stored; ``decode`` attends to these,
+                 and ``commit`` makes them the lengths once every layer is through
+
+    Calls that write nothing in common may run at once on different streams.
+    """
+
+    def __init__(self, *, n_layers: int, n_pages: int, page_size: int, max_requests: int, max_pages: int, h_q: int,
+                 h_kv: int, d: int, dtype=torch.bfloat16, kv_dtype=None, softmax_scale: float = 0.0, window: int = 0,
+                 rotary: Rotary | None = None, kv_scale=None, pages=None, device: int = 0):
+        kv_dtype = kv_dtype or dtype
+        _need(dtype in TYPES and kv_dtype in TYPES, f"no cache of {kv_dtype} for {dtype}")
+        self._h = ctypes.c_void_p()
+        self.device = torch.device("cuda", device)
+        self.cfg = HsPagedConfig(n_layers, n_pages, page_size, max_requests, max_pages, h_q, h_kv, d, TYPES[dtype],
+                                 TYPES[kv_dtype], window, device, softmax_scale, 0)
+        self.dtype, self.kv_dtype, self.rotary = dtype, kv_dtype, rotary
+        self.n_layers, self.n_pages, self.page_size, self.max_pages = n_layers, n_pages, page_size, max_pages
+        self.max_requests, self.h_q, self.h_kv, self.d = max_requests, h_q, h_kv, d
+        _need(rotary is None or rotary.device == self.device, "the rotation is on another device")
+        shape = (n_layers, n_pages, 2, h_kv, page_size, d)
+        if kv_scale is not None:
+            _need(tuple(kv_scale.shape) == (n_layers, 2, h_kv) and kv_scale.dtype == torch.float32
+                  and kv_scale.device == self.device, f"kv_scale must be float32 [n_layers, 2, h_kv] on {self.device}")
+            kv_scale = kv_scale.contiguous()
+        if pages is not None:
+            _need(tuple(pages.shape) == shape and pages.dtype == kv_dtype and pages.device == self.device
+                  and pages.is_contiguous(), f"pages must be a contiguous {kv_dtype} tensor {list(shape)} on {self.device}")
+        else:   # what a bad configuration makes of this is refused by the library below
+            pages = torch.empty([max(0, s) for s in shape], dtype=kv_dtype, device=self.device)
+        self._error = torch.zeros(4, dtype=torch.int32, device=self.device)
+        _check(lib().hs_paged_create(ctypes.byref(self.cfg), pages.data_ptr(),
+                                     None if kv_scale is None else kv_scale.data_ptr(), self._error.data_ptr(),
+                                     ctypes.byref(self._h)))
+        self.pages, self.kv_scale = pages, kv_scale
+        self.page_table = torch.full((max_requests, max_pages), -1, dtype=torch.int32, device=self.device)
+        self.lengths = torch.zeros(max_requests, dtype=torch.int32, device=self.device)
+        self.next_lengths = torch.zeros(max_requests, dtype=torch.int32, device=self.device)
+        self._ws_bytes = int(lib().hs_paged_workspace_bytes(self._h))
+        self._free = list(range(n_pages - 1, -1, -1))
+        self._held: dict[int, list[int]] = {}
+        torch.cuda.current_stream(self.device).synchronize()
+
+    # -- lifetime --------------------------------------------------------------
+    def close(self):
+        if self._h:
+            lib().hs_paged_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *a):
+        self.close()
+
+    # -- pages and lengths -------------------------------------------------------
+    def reserve(self, req: int, n_positions: int):
+        """Gives request ``req`` pages for ``n_positions`` positions in all (on the current stream)."""
+        _need(0 <= req < self.max_requests, "request out of range")
+        have = self._held.setdefault(req, [])
+        need = -(-n_positions // self.page_size)
+        _need(need <= self.max_pages, f"{n_positions} positions are more than max_pages * page_size")
+        n = need - len(have)
+        if n <= 0:
+            return
+        if n > len(self._free):
+            raise MemoryError(f"{n} pages wanted, {len(self._free)} free")
+        new = [self._free.pop() for _ in range(n)]
+        self.page_table[req, len(have):need] = torch.tensor(new, dtype=torch.int32, device=self.device)
+        have.extend(new)
+
+    def release(self, req: int):
+        """Takes back the pages of ``req``: its table row is cleared and its lengths are 0."""
+        _need(0 <= req < self.max_requests, "request out of range")
+        self._free.extend(reversed(self._held.pop(req, [])))
+        self.page_table[req] = -1
+        self.lengths[req] = 0
+        self.next_lengths[req] = 0
+
+    def free_pages(self) -> int:
+        return len(self._free)
+
+    def set_lengths(self, lengths):
+        """Positions held by every request (int32 [max_requests])."""
+        self.lengths.copy_(lengths)
+        self.next_lengths.copy_(lengths)
+
+    def commit(self):
+        """The step is through every layer: its tokens count as held."""
+        self.lengths.copy_(self.next_lengths)
+
+    # -- the path ------------------------------------------------------------------
+    def append(self, layer: int, k, v, q=None, q_out=None, req_ids=None, tok_offsets=None, stream=None):
+        """Stores new keys and values (k, v: [tokens, h_kv, d]), rotated by the cache's
+        ``rotary`` at positions lengths[r], lengths[r] + 1, ...; sets next_lengths.
+
+        q           : the step's queries [tokens, h_q, d]; their rotated values are returned
+        q_out       : where to write them (q itself: in place)
+        tok_offsets : int32 [requests + 1]: request i takes rows tok_offsets[i] .. tok_offsets[i+1]-1;
+                      rows outside belong to nobody (their rows of a new q_out are undefined).
+                      None: one row per request (with req_ids: the same number for each)
+        req_ids     : int32 [requests] distinct ids; None: requests 0, 1, ...
+        """
+        dev, n = self.device, int(k.shape[0])
+        hk = _heads("k", k, dev, self.dtype, self.d, self.h_kv)
+        hv = _heads("v", v, dev, self.dtype, self.d, self.h_kv)
+        _need(v.shape[0] == n, "k and v have different numbers of rows")
+        if req_ids is not None:
+            n_req = int(req_ids.shape[0])
+        elif tok_offsets is not None:
+            n_req = int(tok_offsets.shape[0]) - 1
+        else:
+            n_req = n
+        ids = None if req_ids is None else _ints("req_ids", req_ids, dev, (n_req,))
+        offs = None if tok_offsets is None else _ints("tok_offsets", tok_offsets, dev, (n_req + 1,))
+        hq = ho = None
+        if q is not None:
+            _need(self.rotary is not None, "q needs a cache with a rotation")
+            hq = _heads("q", q, dev, self.dtype, self.d, self.h_q)
+            _need(q.shape[0] == n and (q_out is None or q_out.shape == q.shape), "q, q_out and k have different rows")
+        else:
+            _need(q_out is None, "q_out without q")
+        with _On(stream, dev, (k, v, q, q_out, req_ids, tok_offsets)) as raw:
+            if q is not None:
+                if q_out is None:
+                    q_out = torch.empty(q.shape, dtype=self.dtype, device=dev)
+                ho = ctypes.byref(_heads("q_out", q_out, dev, self.dtype, self.d, self.h_q))
+                hq = ctypes.byref(hq)
+            rot = None if self.rotary is None else ctypes.byref(self.rotary.plan[0])
+            _check(lib().hs_paged_append(self._h, layer, n_req, ids, n, offs, self.page_table.data_ptr(),
+                                         self.lengths.data_ptr(), self.next_lengths.data_ptr(), rot, hq, ho,
+                                         ctypes.byref(hk), ctypes.byref(hv), raw))
+        return q_out
+
+    def decode(self, layer: int, q, req_ids=None, lengths=None, out=None, return_lse: bool = False, stream=None):
+        """Attention of one token per request: q [requests, h_q, d] -> out of its shape
+        (and, with return_lse, the float32 [requests, h_q] logarithms of the softmax sums).
+
+        lengths : int32 [max_requests], positions attended to; None: next_lengths
+        """
+        dev, n = self.device, int(q.shape[0])
+        hq = _heads("q", q, dev, self.dtype, self.d, self.h_q)
+        ids = None if req_ids is None else _ints("req_ids", req_ids, dev, (n,))
+        if lengths is None:
+            lens = self.next_lengths.data_ptr()
+        else:
+            lens = _ints("lengths", lengths, dev, (self.max_requests,))
+        if out is not None:
+            _need(out.shape == q.shape and out.dtype == self.dtype and out.device == dev and out.is_contiguous(),
+                  "out must be contiguous, of q's shape, type and device")
+        with _On(stream, dev, (q, req_ids, lengths, out)) as raw:
+            if out is None:
+                out = torch.empty((n, self.h_q, self.d), dtype=self.dtype, device=dev)
+            lse = torch.empty((n, self.h_q), dtype=torch.float32, device=dev) if return_lse else None
+            ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
+            _check(lib().hs_paged_decode(self._h, layer, n, ids, self.page_table.data_ptr(), lens, ctypes.byref(hq),
+                                         out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), raw))
+        return (out, lse) if return_lse else out
+
+    # -- errors ----------------------------------------------------------------------
+    def device_error(self) -> int:
+        """HS_DEVERR_* bits that the calls have set so far (synchronises the device)."""
+        w = ctypes.c_uint32(0)
+        rc = lib().hs_paged_error(self._h, ctypes.byref(w))
+        if rc not in (HS_OK, HS_ERR_DEVICE):
+            _check(rc)
+        return int(w.value)
