@@ -19,7 +19,8 @@ LIB = os.path.join(HERE, "libhs.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["hs_api.cu", "hs_append.cu", "hs_score.cu", "hs_select.cu", "hs_attention.cu", "hs_attention_mla.cu",
-           "hs_static.cu", "hs_rotary.cu", "hs_paged.cu", "hs_paged_attention.cu"]
+           "hs_static.cu", "hs_rotary.cu", "hs_paged.cu", "hs_paged_attention.cu",
+           "hs_paged_attention_d64.cu", "hs_paged_attention_d128.cu", "hs_paged_attention_d256.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 

@@ -356,7 +356,7 @@ int hs_paged_append(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
 }
 
 int64_t hs_paged_workspace_bytes(const hs_paged_t* h) {
-  return h ? hs::paged_workspace_bytes(h->cfg.h_q, h->cfg.h_kv, h->cfg.d, h->num_sms) : 0;
+  return h ? hs::paged_workspace_bytes(h->cfg.d, h->cfg.h_q / h->cfg.h_kv, h->cfg.page_type, h->num_sms) : 0;
 }
 
 int hs_paged_decode(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* req_ids, const int32_t* page_table,
@@ -408,6 +408,7 @@ int hs_paged_decode(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
   p.scale_log2 = h->scale_log2;
   DeviceScope dev(c.device);
   if (dev.err != cudaSuccess) return fail_cuda(dev.err, "hs_paged_decode: device");
+  if (h->num_sms < 1) return named(HS_ERR_CUDA, me, "the handle was created without its device");
   const cudaError_t e = hs::launch_paged_decode(p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? HS_OK : fail_cuda(e, "hs_paged_decode: launch");
 }

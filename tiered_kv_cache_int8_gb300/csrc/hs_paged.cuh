@@ -75,7 +75,7 @@ struct PagedDecodeParams {
 cudaError_t launch_rotate(const RotateParams& p, int type, int page_type, bool append, bool interleaved,
                           bool wide, cudaStream_t st);
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t st);
-int64_t paged_workspace_bytes(int h_q, int h_kv, int d, int num_sms);
+int64_t paged_workspace_bytes(int d, int group, int page_type, int num_sms);
 
 }  // namespace hs
 

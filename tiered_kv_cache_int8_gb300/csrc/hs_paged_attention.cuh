@@ -1,0 +1,765 @@
+// Attention of one new token per request over its paged cache:
+//
+//   o_h = sum_n softmax_n(scale * q_h . K_n) V_n,  lse_h = ln sum_n exp(scale * q_h . K_n)
+//
+// over n in [max(0, N - window), N), in one pass with a running maximum m and sum l
+// (of two pieces: m = max, l and o weighted by 2^(m_i - m)).
+//
+// Bound: HBM.  A row of keys and values serves the h_q / h_kv query heads of its
+// kv head, a few flops per byte, so the time is the cache's bytes; what the design
+// is after is an even share of them for every SM and enough of them in flight.
+//
+// Work.  The positions of every (request, kv head) are cut into units of 16; all
+// units of the call, request by request and head by head, form one sequence, and
+// every CTA (one per SM) takes an equal contiguous share of it, every warp an equal
+// share of its CTA's.  So one request of 200 K positions and a batch of short ones
+// are spread the same way, with no table of splits: a CTA finds its place by a
+// prefix sum over the lengths.
+//
+// A warp runs alone: it has its own ring of stages in shared memory, starts the
+// TMA copies of its next units itself (one copy of 16 rows of keys and of values: a
+// unit never crosses a page), waits for its own mbarriers, and keeps its own m, l
+// and output.  No barrier joins warps before the end of the share.
+//
+// Products on mma.sync m16n8k16 with 32-bit sums, transposed so that the wide side
+// is the cache's: S^T = K Q^T (16 rows x 8 heads per tile), O^T += V^T P^T (16
+// output elements x 8 heads); the tensor pipe is far from the bound.  P^T becomes
+// the second product's operand by movmatrix.
+//
+// Pieces.  A (request, head) wholly inside a warp's share is written out by the
+// warp.  What crosses warps is joined by the CTA at its end, what crosses CTAs goes
+// to the workspace and is joined by the second kernel (a programmatic dependent):
+// at most one such chain starts in a CTA, so that kernel has one small block per
+// CTA and head.
+#ifndef HS_PAGED_ATTENTION_CUH_
+#define HS_PAGED_ATTENTION_CUH_
+
+#include "hs_paged.cuh"
+
+namespace hs {
+namespace pa {
+
+constexpr int UNIT = 16;                 // positions
+constexpr float P_SHIFT = 15.f;          // see weight()
+constexpr int RING_BYTES = 192 * 1024;
+
+template <int D, int NT, int QTYPE, bool E4M3>
+struct Cfg {
+  static constexpr int ES = E4M3 ? 1 : 2;
+  static constexpr int HEADS = 8 * NT;                       // query heads of a pass
+  static constexpr int ROW = D * ES < 128 ? D * ES : 128;    // bytes of a row in one swizzled block
+  static constexpr int BLOCKS = D * ES / ROW;                // blocks side by side in a row
+  static constexpr int HALF = UNIT * D * ES;                 // bytes of a unit's keys (or values)
+  static constexpr int STAGE = 2 * HALF;
+  // as many warps as keep three stages of the ring each; six at least are there in any case
+  static constexpr int WARPS = STAGE >= 16384 ? 4 : STAGE <= 2048 ? 16 : 8;
+  static constexpr int STAGES = RING_BYTES / (WARPS * STAGE) < 12 ? RING_BYTES / (WARPS * STAGE) : 12;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int PROW = D + 4;                         // floats of a piece's head row (bank spread)
+  static constexpr int PIECE = HEADS * PROW + 2 * HEADS;     // o rows, then m, then l
+  static_assert(PIECE * 4 <= STAGES * STAGE, "a piece fits a warp's ring");
+  static constexpr int SM_RING = 0;
+  static constexpr int SM_BARS = WARPS * STAGES * STAGE;
+  static constexpr int SM_META = SM_BARS + WARPS * STAGES * 8;
+  static constexpr int SM_SCAN = SM_META + 2 * WARPS * 32;
+  static constexpr int SM_PRE = SM_SCAN + (WARPS + 2) * 4 * 2;
+  static size_t smem(int n_req) { return 1024 + SM_PRE + (size_t)(n_req + 1) * 4; }
+};
+
+// where the second kernel finds a chain of pieces that starts in a CTA
+struct Chain {
+  int32_t ri, hc;      // request of the call, kv head and chunk of its query heads
+  int32_t last;        // the chain's last CTA; -1: none starts here
+  int32_t _pad;
+};
+
+// workspace: two pieces per CTA (0: of the segment that came in, 1: of the one that
+// goes on), one per warp, then a Chain per CTA
+__host__ __device__ inline size_t ws_cta(int piece, int cta, int slot) { return (size_t)(cta * 2 + slot) * piece; }
+__host__ __device__ inline size_t ws_warp(int piece, int grid, int warps, int cta, int warp) {
+  return ((size_t)grid * 2 + (size_t)cta * warps + warp) * piece;
+}
+__host__ __device__ inline size_t ws_chain(int piece, int grid, int warps) { return (size_t)grid * (2 + warps) * piece; }
+
+struct Meta {          // a piece that does not cover its segment
+  float* at;           // null: none
+  int32_t ri, hc, from, to, n, _pad;
+};
+
+template <int QTYPE>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (QTYPE == HS_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+template <int QTYPE>
+__device__ __forceinline__ float2 unpack2(uint32_t u) {
+  if constexpr (QTYPE == HS_BF16) return make_float2(bf16lo(u), bf16hi(u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// two e4m3 values (low byte first) as two fp16: exact
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
+  uint32_t y;
+  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(y) : "r"(two));
+  return y;
+}
+
+__device__ __forceinline__ void tma_unit(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+      ::"r"(dst), "l"(map), "r"(bar), "r"(0), "r"(row), "r"(0), "r"(0)
+      : "memory");
+}
+
+// softmax weight 2^x.  Weights that go to fp16 are taken 2^15 times as large (and
+// so is their sum): with the largest at 2^15, a weight keeps fp16's full precision
+// down to 2^-29 of the largest, where unscaled ones would lose it below 2^-14.
+template <bool BF16>
+__device__ __forceinline__ float weight(float x) {
+  return BF16 ? exp2f(x) : exp2f(x + P_SHIFT);
+}
+
+// Units of request i of the call (0 with an error bit for a bad one).
+__device__ __forceinline__ int request_units(const PagedDecodeParams& p, int i, int* first_unit, int* first, int* len,
+                                             int* req, unsigned* err) {
+  *req = p.req_ids ? p.req_ids[i] : i;
+  *len = *first = *first_unit = 0;
+  if (*req < 0 || *req >= p.max_requests) {
+    *err |= HS_DEVERR_REQ_RANGE;
+    return 0;
+  }
+  const int n = p.lengths[*req];
+  if (n < 0 || n > p.max_pages << p.page_shift) {
+    *err |= HS_DEVERR_CAPACITY;
+    return 0;
+  }
+  *len = n;
+  *first = p.window > 0 ? max(0, n - p.window) : 0;
+  *first_unit = *first / UNIT;
+  return (n + UNIT - 1) / UNIT - *first_unit;
+}
+
+template <int QTYPE>
+__device__ __forceinline__ void store_out4(void* out, long long at, float4 v) {
+  uint2 w;
+  w.x = pack2<QTYPE>(v.x, v.y);
+  w.y = pack2<QTYPE>(v.z, v.w);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = w;
+}
+
+// 1 / l of a finished row: 0 where nothing was attended, NaN where a score was one
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
+template <bool BF16>
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l) - (BF16 ? 0.f : P_SHIFT)) * 0.693147180559945f;
+}
+
+struct Place {   // a unit of the sequence
+  int ri, hc, u, n;
+};
+
+template <int D, int NT, int QTYPE, bool E4M3>
+__global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
+    paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ CUtensorMap map) {
+  using C = Cfg<D, NT, QTYPE, E4M3>;
+  constexpr bool BF16 = QTYPE == HS_BF16 && !E4M3;   // type of the products
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::SM_BARS);
+  Meta* meta = reinterpret_cast<Meta*>(smem + C::SM_META);
+  int* scan = reinterpret_cast<int*>(smem + C::SM_SCAN);
+  int* pre = reinterpret_cast<int*>(smem + C::SM_PRE);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+
+  uint64_t* bar = bars + warp * C::STAGES;
+  if (lane == 0) {
+    for (int s = 0; s < C::STAGES; ++s) mbar_init(&bar[s], 1);
+    fence_mbar_init();
+  }
+  if (lane < 2) meta[warp * 2 + lane].at = nullptr;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // ---- the sequence: units before each request, for one head
+  {
+    const int per = (p.n_req + C::THREADS - 1) / C::THREADS;
+    const int i0 = min(p.n_req, tid * per), i1 = min(p.n_req, i0 + per);
+    int sum = 0, a, b, c, r;
+    unsigned err = 0;
+    for (int i = i0; i < i1; ++i) sum += request_units(p, i, &a, &b, &c, &r, &err);
+    int at = block_exclusive_scan<C::THREADS>(sum, scan, nullptr);
+    for (int i = i0; i < i1; ++i) {
+      pre[i] = at;
+      at += request_units(p, i, &a, &b, &c, &r, &err);
+    }
+    if (i1 == p.n_req && i0 < i1) pre[p.n_req] = at;
+    if (err && blockIdx.x == 0) set_error(p.dev_error, err);
+    __syncthreads();
+  }
+  const int chunks = (p.group + C::HEADS - 1) / C::HEADS;
+  const int hcn = p.h_kv * chunks;
+  const long long total = (long long)pre[p.n_req] * hcn;
+  long long share = (total + gridDim.x - 1) / gridDim.x;
+  if (share < C::WARPS) share = C::WARPS;
+  const long long wshare = (share + C::WARPS - 1) / C::WARPS;
+  const long long cta0 = blockIdx.x * share;
+  const long long cta1 = min(total, cta0 + share);
+  const long long w0 = cta0 + warp * wshare;
+  const long long w1 = min(cta1, w0 + wshare);
+
+  const unsigned char* ring = smem + C::SM_RING + (size_t)warp * C::STAGES * C::STAGE;
+  const uint32_t ring_s = smem_addr(ring);
+
+  if (w0 < w1) {
+    Place at;                       // the unit to be consumed next
+    {
+      int lo = 0, hi = p.n_req;     // pre[lo] * hcn <= w0 < pre[hi] * hcn
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((long long)pre[mid] * hcn <= w0) lo = mid; else hi = mid;
+      }
+      at.ri = lo;
+      at.n = pre[lo + 1] - pre[lo];
+      const int rem = (int)(w0 - (long long)pre[lo] * hcn);
+      at.hc = rem / at.n;
+      at.u = rem - at.hc * at.n;
+    }
+    Place is = at;                  // the unit whose copy starts next
+    long long to_issue = w1 - w0, to_do = w1 - w0;
+    auto step = [&](Place& x) {
+      if (++x.u == x.n) {
+        x.u = 0;
+        if (++x.hc == hcn) {
+          x.hc = 0;
+          do ++x.ri; while (x.ri < p.n_req && pre[x.ri + 1] == pre[x.ri]);
+          x.n = x.ri < p.n_req ? pre[x.ri + 1] - pre[x.ri] : 1;
+        }
+      }
+    };
+
+    // ---- copies
+    int i_ri = -1, i_unit0 = 0, i_pages = 0;        // the request whose copies are being started
+    const int32_t* i_table = nullptr;
+    int win = 0, win_page = -1;                     // its page ids win .. win + 31, one per lane
+    bool win_ok = false;
+    unsigned bad = 0;                               // stages whose page id was out of range
+    const int upp = p.page_shift - 4;               // units of a page: 2^upp
+    auto issue = [&](int stage) {
+      if (is.ri != i_ri) {
+        int first, len, req;
+        unsigned err = 0;
+        request_units(p, is.ri, &i_unit0, &first, &len, &req, &err);
+        i_ri = is.ri;
+        i_pages = (len + p.page_size - 1) >> p.page_shift;
+        i_table = p.page_table + (long long)req * p.max_pages;
+        win_ok = false;
+      }
+      const int ua = i_unit0 + is.u;
+      const int pg = ua >> upp;
+      if (!win_ok || pg < win || pg >= win + 32) {
+        win = pg;
+        win_page = win + lane < i_pages ? i_table[win + lane] : -1;
+        win_ok = true;
+      }
+      int page = __shfl_sync(FULL_MASK, win_page, pg - win);
+      if (page < 0 || page >= p.n_pages) {
+        page = 0;                   // some page: its rows are not used
+        bad |= 1u << stage;
+        if (lane == 0) set_error(p.dev_error, HS_DEVERR_PAGE);
+      } else {
+        bad &= ~(1u << stage);
+      }
+      if (lane == 0) {
+        const int row = ((page * 2 * p.h_kv + is.hc / chunks) << p.page_shift) + ((ua << 4) & (p.page_size - 1));
+        mbar_arrive_expect_tx(&bar[stage], C::STAGE);
+        tma_unit(ring_s + stage * C::STAGE, &map, row, smem_addr(&bar[stage]));
+      }
+      step(is);
+    };
+    for (int s = 0; s < C::STAGES && to_issue > 0; ++s, --to_issue) issue(s);
+
+    // ---- lane's places in a stage: ldmatrix rows and the swizzle of their 16-byte pieces
+    auto place = [&](int row, int piece) {
+      const int sw = C::ROW == 128 ? (row & 7) : ((row >> 1) & 3);
+      return (uint32_t)(row * C::ROW + ((piece ^ sw) << 4));
+    };
+    const uint32_t k_at = place(lane & 15, lane >> 4);
+    const uint32_t v_at = C::HALF + (E4M3 ? k_at : place((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1));
+    // piece 2 i + b of a row: b is in the lane's place, 2 i changes bits that the place's xor keeps apart
+    auto piece2 = [&](uint32_t base, int i) {
+      constexpr int PER = C::ROW / 32;              // pairs of pieces in a block
+      return (base ^ ((i % PER) << 5)) + (i / PER) * (UNIT * C::ROW);
+    };
+
+    uint32_t qf[NT][D / 16][2];
+    float fac[NT][2];                               // scores to powers of two, by head
+    float o[NT][D / 16][4], m[NT][2], l[NT][2];
+    int first = 0, len = 0, unit0 = 0, from = 0;
+    bool fresh = true, alive = true;
+    int stage = 0;
+    uint32_t phase = 0;
+
+    for (; to_do > 0; --to_do) {
+      if (fresh) {                                  // a segment begins (or the share does)
+        int req;
+        unsigned err = 0;
+        request_units(p, at.ri, &unit0, &first, &len, &req, &err);
+        from = at.u;
+        const int kvh = at.hc / chunks, chunk = at.hc - kvh * chunks;
+        const float ks = E4M3 ? p.kv_scale[kvh] : 1.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int hg = chunk * C::HEADS + nt * 8 + g;        // head within the group
+          const bool have = hg < p.group;
+          const uint16_t* qrow = static_cast<const uint16_t*>(p.q) + at.ri * p.q_ts + (kvh * p.group + (have ? hg : 0)) * p.q_hs;
+          if constexpr (E4M3) {
+            // columns 4t .. 4t+3 of each 16: the order in which the key bytes come
+            float x[D / 16][4], mx = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              const uint2 w = *reinterpret_cast<const uint2*>(qrow + c * 16 + t * 4);
+              const float2 a = unpack2<QTYPE>(w.x), b = unpack2<QTYPE>(w.y);
+              x[c][0] = a.x; x[c][1] = a.y; x[c][2] = b.x; x[c][3] = b.y;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(x[c][e]));
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 2));
+            // the row under a power of two, its largest in [1, 2): fp16 holds it as well as its own type
+            const int e2 = mx > 0.f && mx < INFINITY ? ilogbf(mx) : 0;
+            const float down = exp2f((float)(-e2 / 2)), down2 = exp2f((float)(-e2 - (-e2 / 2)));
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              qf[nt][c][0] = have ? pack2<HS_FP16>(x[c][0] * down * down2, x[c][1] * down * down2) : 0u;
+              qf[nt][c][1] = have ? pack2<HS_FP16>(x[c][2] * down * down2, x[c][3] * down * down2) : 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int ee = __shfl_sync(FULL_MASK, e2, (2 * t + e) << 2);
+              fac[nt][e] = p.scale_log2 * ks * exp2f((float)(ee / 2)) * exp2f((float)(ee - ee / 2));
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(qrow + c * 16 + e * 8 + t * 2);
+                qf[nt][c][e] = have ? w : 0u;
+              }
+            fac[nt][0] = fac[nt][1] = p.scale_log2;
+          }
+          m[nt][0] = m[nt][1] = -INFINITY;
+          l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) o[nt][c][0] = o[nt][c][1] = o[nt][c][2] = o[nt][c][3] = 0.f;
+        }
+        fresh = false;
+      }
+
+      if (alive) {
+        alive = __all_sync(FULL_MASK, mbar_wait_bounded(&bar[stage], phase));
+        if (!alive) {                               // a copy did not come: none is started any more
+          if (lane == 0) set_error(p.dev_error, HS_DEVERR_TIMEOUT);
+          // those in flight get their time before the shared memory goes on to something else
+          const int flying = (int)min(to_do, (long long)C::STAGES);
+          for (int j = 0; j < flying; ++j) {
+            const int s = stage + j;
+            mbar_wait_bounded(&bar[s < C::STAGES ? s : s - C::STAGES], s < C::STAGES ? phase : phase ^ 1u);
+          }
+        }
+      }
+      if (alive) {
+        const uint32_t st = ring_s + stage * C::STAGE;
+        // ---- S^T = K Q^T
+        float s[NT][4], s2[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t r[4];
+            ldsm4(r, st + piece2(k_at, i));
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t a[4] = {e4m3x2_to_half2(r[2 * c]), e4m3x2_to_half2(r[2 * c + 1]),
+                                     e4m3x2_to_half2(r[2 * c] >> 16), e4m3x2_to_half2(r[2 * c + 1] >> 16)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816<false>(c ? s2[nt] : s[nt], a, qf[nt][2 * i + c][0], qf[nt][2 * i + c][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t a[4];
+            ldsm4(a, st + piece2(k_at, c));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<BF16>(c & 1 ? s2[nt] : s[nt], a, qf[nt][c][0], qf[nt][c][1]);
+          }
+        }
+        // ---- rows of the unit that are attended: [lo, hi)
+        const int pos = (unit0 + at.u) * UNIT;
+        const int lo = max(0, first - pos), hi = (bad >> stage) & 1 ? 0 : min(UNIT, len - pos);
+        const bool part = lo > 0 || hi < UNIT;
+        const bool in0 = !part || (g >= lo && g < hi), in1 = !part || (g + 8 >= lo && g + 8 < hi);
+        float mx[NT][2];
+        bool grows = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            s[nt][e] = in0 ? (s[nt][e] + s2[nt][e]) * fac[nt][e] : -INFINITY;
+            s[nt][e + 2] = in1 ? (s[nt][e + 2] + s2[nt][e + 2]) * fac[nt][e] : -INFINITY;
+            float x = fmaxf(s[nt][e], s[nt][e + 2]);
+            x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, 16));
+            mx[nt][e] = x;
+            grows = grows || x > m[nt][e];
+          }
+        if (__any_sync(FULL_MASK, grows)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float n = fmaxf(m[nt][e], mx[nt][e]);
+              const float keep = exp2f(m[nt][e] - (n == -INFINITY ? 0.f : n));
+              m[nt][e] = n;
+              l[nt][e] *= keep;
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) {
+                o[nt][c][e] *= keep;
+                o[nt][c][e + 2] *= keep;
+              }
+            }
+        }
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float base = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+            w[e] = weight<BF16>(s[nt][e] - base);
+            w[e + 2] = weight<BF16>(s[nt][e + 2] - base);
+            l[nt][e] += w[e] + w[e + 2];
+          }
+          pf[nt][0] = transpose8(pack2<BF16 ? HS_BF16 : HS_FP16>(w[0], w[1]));
+          pf[nt][1] = transpose8(pack2<BF16 ? HS_BF16 : HS_FP16>(w[2], w[3]));
+        }
+        // ---- O^T += V^T P^T.  Rows that are not attended may hold anything: their values become 0
+        uint32_t keep01 = 0xffffffffu, keep23 = 0xffffffffu;
+        if (part) {
+          auto halves = [&](int r) {
+            return (r >= lo && r < hi ? 0xffffu : 0u) | (r + 1 >= lo && r + 1 < hi ? 0xffff0000u : 0u);
+          };
+          keep01 = halves(2 * t);
+          keep23 = halves(2 * t + 8);
+        }
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t r[4];
+            ldsm4_trans(r, st + piece2(v_at, i));
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t x = r[2 * c] & keep01, y = r[2 * c + 1] & keep23;
+              // a row pair of the tile is elements 2g and 2g+1 of the 16
+              const uint32_t a[4] = {e4m3x2_to_half2(__byte_perm(x, 0, 0x4420)), e4m3x2_to_half2(__byte_perm(x, 0, 0x4431)),
+                                     e4m3x2_to_half2(__byte_perm(y, 0, 0x4420)), e4m3x2_to_half2(__byte_perm(y, 0, 0x4431))};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[nt][2 * i + c], a, pf[nt][0], pf[nt][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t a[4];
+            ldsm4_trans(a, st + piece2(v_at, c));
+            a[0] &= keep01;
+            a[1] &= keep01;
+            a[2] &= keep23;
+            a[3] &= keep23;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<BF16>(o[nt][c], a, pf[nt][0], pf[nt][1]);
+          }
+        }
+        __syncwarp();                               // every lane has read the stage
+        if (to_issue > 0) {
+          issue(stage);
+          --to_issue;
+        }
+      }
+      if (++stage == C::STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+
+      const bool ends = at.u + 1 == at.n;
+      if (ends || to_do == 1) {
+        // ---- a piece is done: [from, to) of its segment
+        const int to = at.u + 1;
+        const int kvh = at.hc / chunks, chunk = at.hc - kvh * chunks;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = l[nt][e];
+            x += __shfl_xor_sync(FULL_MASK, x, 4);
+            x += __shfl_xor_sync(FULL_MASK, x, 8);
+            x += __shfl_xor_sync(FULL_MASK, x, 16);
+            l[nt][e] = x;
+          }
+        // an accumulator's row 0 / 1 of the pair: elements of the 16
+        const int d0 = E4M3 ? 2 * g : g, d1 = E4M3 ? 2 * g + 1 : g + 8;
+        if (from == 0 && ends) {
+          const float vs = E4M3 ? p.kv_scale[p.h_kv + kvh] : 1.f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int hg = chunk * C::HEADS + nt * 8 + 2 * t + e;
+              if (hg < p.group) {
+                const long long h = (long long)at.ri * p.h_q + kvh * p.group + hg;
+                const float inv = inverse(l[nt][e]) * vs;
+                uint16_t* row = static_cast<uint16_t*>(p.out) + h * D;
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                  const uint32_t two = pack2<QTYPE>(o[nt][c][e] * inv, o[nt][c][e + 2] * inv);
+                  row[c * 16 + d0] = (uint16_t)two;
+                  row[c * 16 + d1] = (uint16_t)(two >> 16);
+                }
+                if (p.lse && g == 0) p.lse[h] = log_sum<BF16>(m[nt][e], l[nt][e]);
+              }
+            }
+        } else {
+          // the share's last piece goes to the warp's own ring (no copy is in flight), one before it to the workspace
+          float* dst = to_do == 1 ? reinterpret_cast<float*>(smem + C::SM_RING + (size_t)warp * C::STAGES * C::STAGE)
+                                  : p.ws + ws_warp(C::PIECE, gridDim.x, C::WARPS, blockIdx.x, warp);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int h = nt * 8 + 2 * t + e;
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) {
+                dst[h * C::PROW + c * 16 + d0] = o[nt][c][e];
+                dst[h * C::PROW + c * 16 + d1] = o[nt][c][e + 2];
+              }
+              if (g == 0) {
+                dst[C::HEADS * C::PROW + h] = m[nt][e];
+                dst[C::HEADS * C::PROW + C::HEADS + h] = l[nt][e];
+              }
+            }
+          if (lane == 0) meta[warp * 2 + (to_do == 1)] = Meta{dst, at.ri, at.hc, from, to, at.n, 0};
+        }
+        fresh = true;
+      }
+      step(at);
+    }
+  }
+  __syncthreads();
+
+  // ---- pieces of the CTA, in sequence order: neighbours of one segment are joined
+  Chain chain = {0, 0, -1, 0};
+  for (int i = 0; i < 2 * C::WARPS;) {
+    const Meta a = meta[i];
+    if (!a.at) {
+      ++i;
+      continue;
+    }
+    const float* src[2 * C::WARPS];
+    int k = 0, to = a.to;
+    for (; i < 2 * C::WARPS; ++i) {
+      const Meta b = meta[i];
+      if (!b.at) continue;
+      if (b.ri != a.ri || b.hc != a.hc) break;
+      src[k++] = b.at;
+      to = b.to;
+    }
+    const bool whole = a.from == 0 && to == a.n;
+    const int kvh = a.hc / chunks, chunk = a.hc - kvh * chunks;
+    float* dst = p.ws + ws_cta(C::PIECE, blockIdx.x, a.from == 0);
+    for (int e = tid; e < C::HEADS * (D / 4); e += C::THREADS) {
+      const int h = e / (D / 4), d4 = e - h * (D / 4);
+      float mm = -INFINITY;
+      for (int j = 0; j < k; ++j) mm = fmaxf(mm, src[j][C::HEADS * C::PROW + h]);
+      const float base = mm == -INFINITY ? 0.f : mm;
+      float ll = 0.f;
+      float4 acc = {0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < k; ++j) {
+        const float w = exp2f(src[j][C::HEADS * C::PROW + h] - base);
+        const float4 x = *reinterpret_cast<const float4*>(src[j] + h * C::PROW + d4 * 4);
+        ll += w * src[j][C::HEADS * C::PROW + C::HEADS + h];
+        acc.x += w * x.x;
+        acc.y += w * x.y;
+        acc.z += w * x.z;
+        acc.w += w * x.w;
+      }
+      if (whole) {
+        const int hg = chunk * C::HEADS + h;
+        if (hg < p.group) {
+          const long long row = (long long)a.ri * p.h_q + kvh * p.group + hg;
+          const float inv = inverse(ll) * (E4M3 ? p.kv_scale[p.h_kv + kvh] : 1.f);
+          store_out4<QTYPE>(p.out, row * D + d4 * 4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+          if (p.lse && d4 == 0) p.lse[row] = log_sum<BF16>(mm, ll);
+        }
+      } else {
+        *reinterpret_cast<float4*>(dst + h * C::PROW + d4 * 4) = acc;
+        if (d4 == 0) {
+          dst[C::HEADS * C::PROW + h] = mm;
+          dst[C::HEADS * C::PROW + C::HEADS + h] = ll;
+        }
+      }
+    }
+    if (a.from == 0 && to < a.n) {
+      const long long end = (long long)pre[a.ri] * hcn + (long long)(a.hc + 1) * a.n;   // of the segment
+      chain = Chain{a.ri, a.hc, (int)((end - 1) / share), 0};
+    }
+  }
+  if (tid == 0)
+    reinterpret_cast<Chain*>(p.ws + ws_chain(C::PIECE, gridDim.x, C::WARPS))[blockIdx.x] = chain;
+
+  // ---- requests without a position
+  for (int i = blockIdx.x; i < p.n_req; i += gridDim.x) {
+    if (pre[i + 1] != pre[i]) continue;
+    for (int e = tid; e < p.h_q * (D / 4); e += C::THREADS)
+      store_out4<QTYPE>(p.out, (long long)i * p.h_q * D + e * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+    if (p.lse)
+      for (int h = tid; h < p.h_q; h += C::THREADS) p.lse[(long long)i * p.h_q + h] = -INFINITY;
+  }
+}
+
+// The chains: block (cta, head) joins the pieces of the segment that starts in `cta`
+// and goes on in cta + 1 .. last, for one head of the pass.  Groups of lanes take
+// every GROUPS-th piece and are added up in shared memory, in a fixed order.
+template <int D, int NT, int QTYPE, bool E4M3>
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
+  using C = Cfg<D, NT, QTYPE, E4M3>;
+  constexpr bool BF16 = QTYPE == HS_BF16 && !E4M3;
+  constexpr int LANES = D / 4, GROUPS = 256 / LANES;
+  __shared__ float s_m[GROUPS], s_l[GROUPS];
+  __shared__ float4 s_o[GROUPS][LANES];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int cta = blockIdx.x, h = blockIdx.y;
+  const Chain ch = reinterpret_cast<const Chain*>(p.ws + ws_chain(C::PIECE, p.grid, C::WARPS))[cta];
+  if (ch.last < 0) return;
+  const int chunks = (p.group + C::HEADS - 1) / C::HEADS;
+  const int kvh = ch.hc / chunks, hg = (ch.hc - kvh * chunks) * C::HEADS + h;
+  if (hg >= p.group) return;
+  const int grp = threadIdx.x / LANES, ln = threadIdx.x - grp * LANES;
+  const int n = ch.last - cta + 1;
+  float mm = -INFINITY, ll = 0.f;
+  float4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int j = grp; j < n; j += GROUPS) {
+    const float* src = p.ws + ws_cta(C::PIECE, cta + j, j == 0);
+    const float m = src[C::HEADS * C::PROW + h], l = src[C::HEADS * C::PROW + C::HEADS + h];
+    const float4 x = *reinterpret_cast<const float4*>(src + h * C::PROW + ln * 4);
+    const float nm = fmaxf(mm, m), base = nm == -INFINITY ? 0.f : nm;
+    const float a = exp2f(mm - base), b = exp2f(m - base);
+    mm = nm;
+    ll = ll * a + l * b;
+    acc.x = acc.x * a + x.x * b;
+    acc.y = acc.y * a + x.y * b;
+    acc.z = acc.z * a + x.z * b;
+    acc.w = acc.w * a + x.w * b;
+  }
+  s_o[grp][ln] = acc;
+  if (ln == 0) {
+    s_m[grp] = mm;
+    s_l[grp] = ll;
+  }
+  __syncthreads();
+  if (grp != 0) return;
+  mm = -INFINITY;
+  for (int j = 0; j < GROUPS; ++j) mm = fmaxf(mm, s_m[j]);
+  const float base = mm == -INFINITY ? 0.f : mm;
+  ll = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = 0; j < GROUPS; ++j) {
+    const float w = exp2f(s_m[j] - base);
+    const float4 x = s_o[j][ln];
+    ll += w * s_l[j];
+    acc.x += w * x.x;
+    acc.y += w * x.y;
+    acc.z += w * x.z;
+    acc.w += w * x.w;
+  }
+  const long long row = (long long)ch.ri * p.h_q + kvh * p.group + hg;
+  const float inv = inverse(ll) * (E4M3 ? p.kv_scale[p.h_kv + kvh] : 1.f);
+  store_out4<QTYPE>(p.out, row * D + ln * 4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  if (p.lse && ln == 0) p.lse[row] = log_sum<BF16>(mm, ll);
+}
+
+template <int D, int NT, int QTYPE, bool E4M3>
+cudaError_t go(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st) {
+  using C = Cfg<D, NT, QTYPE, E4M3>;
+  const size_t smem = C::smem(p.n_req);
+  cudaError_t e = allow_smem(paged_decode_kernel<D, NT, QTYPE, E4M3>, C::smem(PG_MAX_REQUESTS));
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged_decode_kernel<D, NT, QTYPE, E4M3>, dim3(p.grid), dim3(C::THREADS), smem, st, p, map);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(paged_join_kernel<D, NT, QTYPE, E4M3>, dim3(p.grid, C::HEADS), dim3(256), 0, st, p);
+}
+
+template <int D, int NT>
+cudaError_t by_type(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st) {
+  const bool e = p.page_type == HS_E4M3;
+  if (p.type == HS_BF16)
+    return e ? go<D, NT, HS_BF16, true>(p, map, st) : go<D, NT, HS_BF16, false>(p, map, st);
+  return e ? go<D, NT, HS_FP16, true>(p, map, st) : go<D, NT, HS_FP16, false>(p, map, st);
+}
+
+// query heads of a pass: up to 8 or 16 of a kv head's; more are taken in several passes over its rows
+template <int D>
+cudaError_t by_group(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st) {
+  return p.group <= 8 ? by_type<D, 1>(p, map, st) : by_type<D, 2>(p, map, st);
+}
+
+template <int D, int NT, bool E4M3>
+size_t ws_bytes(int grid) {
+  using C = Cfg<D, NT, HS_BF16, E4M3>;
+  return ws_chain(C::PIECE, grid, C::WARPS) * 4 + (size_t)grid * sizeof(Chain);
+}
+
+}  // namespace pa
+}  // namespace hs
+
+#endif  // HS_PAGED_ATTENTION_CUH_
