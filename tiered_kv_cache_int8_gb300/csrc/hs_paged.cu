@@ -269,6 +269,14 @@ int hs_paged_create(const hs_paged_config_t* cfg, void* pages, const float* kv_s
   if (cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, cfg->device) != cudaSuccess) {
     (void)cudaGetLastError();
     h->num_sms = 0;
+  } else {
+    h->maps.reset(new (std::nothrow) CUtensorMap[cfg->n_layers]);
+    if (!h->maps || !hs::paged_maps(h, layer_bytes(*cfg))) {
+      const bool oom = !h->maps;
+      delete h;
+      return oom ? named(HS_ERR_OOM, me, "out of host memory")
+                 : named(HS_ERR_CUDA, me, "the driver made no tensor map of the pool");
+    }
   }
   *out = h;
   return HS_OK;
@@ -405,11 +413,12 @@ int hs_paged_decode(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
   p.type = c.type;
   p.page_type = c.page_type;
   p.grid = h->num_sms;
+  p.device = c.device;
   p.scale_log2 = h->scale_log2;
   DeviceScope dev(c.device);
   if (dev.err != cudaSuccess) return fail_cuda(dev.err, "hs_paged_decode: device");
   if (h->num_sms < 1) return named(HS_ERR_CUDA, me, "the handle was created without its device");
-  const cudaError_t e = hs::launch_paged_decode(p, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = hs::launch_paged_decode(p, h->maps[layer], static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? HS_OK : fail_cuda(e, "hs_paged_decode: launch");
 }
 

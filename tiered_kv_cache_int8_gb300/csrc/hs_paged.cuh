@@ -8,9 +8,20 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include <vector>
+#include <memory>
 
 #include "hs_internal.cuh"
+
+struct hs_paged {
+  hs_paged_config_t cfg;
+  void* pages = nullptr;
+  const float* kv_scale = nullptr;
+  unsigned int* dev_error = nullptr;
+  std::unique_ptr<CUtensorMap[]> maps;   // of each layer's pool; null without a device
+  int num_sms = 0;
+  int page_shift = 0;
+  float scale_log2 = 0.f;
+};
 
 namespace hs {
 
@@ -68,25 +79,16 @@ struct PagedDecodeParams {
   unsigned int* dev_error;
   int32_t n_req, max_requests, max_pages, n_pages, page_size, page_shift;
   int32_t h_q, h_kv, group, d, window, type, page_type;
-  int32_t grid;
+  int32_t grid, device;
   float scale_log2;
 };
 
 cudaError_t launch_rotate(const RotateParams& p, int type, int page_type, bool append, bool interleaved,
                           bool wide, cudaStream_t st);
-cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t st);
+cudaError_t launch_paged_decode(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st);
+bool paged_maps(::hs_paged* h, size_t layer_bytes);   // false: no tensor maps could be made
 int64_t paged_workspace_bytes(int d, int group, int page_type, int num_sms);
 
 }  // namespace hs
-
-struct hs_paged {
-  hs_paged_config_t cfg;
-  void* pages = nullptr;
-  const float* kv_scale = nullptr;
-  unsigned int* dev_error = nullptr;
-  int num_sms = 0;
-  int page_shift = 0;
-  float scale_log2 = 0.f;
-};
 
 #endif  // HS_PAGED_CUH_

@@ -30,9 +30,9 @@ Encode encoder() {
 
 // The layer's pool as [keys or values][block of a row][row][bytes of the block]: one
 // copy brings 16 rows of keys and of values, each block's rows together and swizzled.
-cudaError_t pool_map(const PagedDecodeParams& p, CUtensorMap* map) {
+bool pool_map(const hs_paged_config_t& p, void* pages, CUtensorMap* map) {
   const Encode encode = encoder();
-  if (!encode) return cudaErrorNotSupported;
+  if (!encode) return false;
   const int es = p.page_type == HS_E4M3 ? 1 : 2;
   const int row = std::min(p.d * es, 128);            // bytes of a row in one block
   const cuuint64_t dims[4] = {(cuuint64_t)(row / es), (cuuint64_t)p.n_pages * 2 * p.h_kv * p.page_size,
@@ -41,10 +41,10 @@ cudaError_t pool_map(const PagedDecodeParams& p, CUtensorMap* map) {
   const cuuint32_t box[4] = {(cuuint32_t)(row / es), pa::UNIT, (cuuint32_t)(p.d * es / row), 2};
   const cuuint32_t one[4] = {1, 1, 1, 1};
   const CUresult r = encode(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4,
-                            const_cast<unsigned char*>(p.pages), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            pages, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                             row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return r == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -64,10 +64,13 @@ int64_t paged_workspace_bytes(int d, int group, int page_type, int num_sms) {
   return (int64_t)((n + 255) / 256 * 256);
 }
 
-cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t st) {
-  CUtensorMap map;
-  const cudaError_t e = pool_map(p, &map);
-  if (e != cudaSuccess) return e;
+bool paged_maps(hs_paged* h, size_t layer_bytes) {
+  for (int l = 0; l < h->cfg.n_layers; ++l)
+    if (!pool_map(h->cfg, static_cast<unsigned char*>(h->pages) + layer_bytes * l, &h->maps[l])) return false;
+  return true;
+}
+
+cudaError_t launch_paged_decode(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st) {
   return p.d == 64 ? paged_decode_d64(p, map, st) : p.d == 128 ? paged_decode_d128(p, map, st) : paged_decode_d256(p, map, st);
 }
 

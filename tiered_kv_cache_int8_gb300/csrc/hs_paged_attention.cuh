@@ -34,12 +34,15 @@
 #ifndef HS_PAGED_ATTENTION_CUH_
 #define HS_PAGED_ATTENTION_CUH_
 
+#include <atomic>
+
 #include "hs_paged.cuh"
 
 namespace hs {
 namespace pa {
 
 constexpr int UNIT = 16;                 // positions
+constexpr int SEGMENT_COST = 4;          // what a segment costs on top of its units, in units
 constexpr float P_SHIFT = 15.f;          // see weight()
 constexpr int RING_BYTES = 192 * 1024;
 
@@ -52,7 +55,7 @@ struct Cfg {
   static constexpr int HALF = UNIT * D * ES;                 // bytes of a unit's keys (or values)
   static constexpr int STAGE = 2 * HALF;
   // as many warps as keep three stages of the ring each; six at least are there in any case
-  static constexpr int WARPS = STAGE >= 16384 ? 4 : STAGE <= 2048 ? 16 : 8;
+  static constexpr int WARPS = STAGE >= 16384 ? 4 : STAGE <= 2048 || (E4M3 && D == 128 && NT == 1) ? 16 : 8;
   static constexpr int STAGES = RING_BYTES / (WARPS * STAGE) < 12 ? RING_BYTES / (WARPS * STAGE) : 12;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int PROW = D + 4;                         // floats of a piece's head row (bank spread)
@@ -233,31 +236,41 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
   }
   const int chunks = (p.group + C::HEADS - 1) / C::HEADS;
   const int hcn = p.h_kv * chunks;
-  const long long total = (long long)pre[p.n_req] * hcn;
+  // Shares are of cost: a segment's units and SEGMENT_COST more before them (its queries,
+  // its first page ids, its output), so that many short segments weigh what they take.
+  auto cost_before = [&](int r) { return ((long long)pre[r] + (long long)SEGMENT_COST * r) * hcn; };
+  const long long total = cost_before(p.n_req);
   long long share = (total + gridDim.x - 1) / gridDim.x;
   if (share < C::WARPS) share = C::WARPS;
   const long long wshare = (share + C::WARPS - 1) / C::WARPS;
   const long long cta0 = blockIdx.x * share;
-  const long long cta1 = min(total, cta0 + share);
-  const long long w0 = cta0 + warp * wshare;
-  const long long w1 = min(cta1, w0 + wshare);
+  // units before a cost position, and the place of the next one
+  auto find = [&](long long x, Place* at) -> long long {
+    if (x >= total) return (long long)pre[p.n_req] * hcn;
+    int lo = 0, hi = p.n_req;       // cost_before(lo) <= x < cost_before(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cost_before(mid) <= x) lo = mid; else hi = mid;
+    }
+    const int n = pre[lo + 1] - pre[lo], rem = (int)(x - cost_before(lo));
+    const int hc = rem / (n + SEGMENT_COST);
+    const int u = max(0, rem - hc * (n + SEGMENT_COST) - SEGMENT_COST);
+    if (at) *at = Place{lo, hc, u, n};
+    return (long long)pre[lo] * hcn + (long long)hc * n + u;
+  };
+  Place at = {0, 0, 0, 1};          // the unit to be consumed next
+  const long long x0 = min(total, cta0 + warp * wshare);
+  const long long w0 = find(x0, &at);
+  const long long w1 = find(min(min(total, cta0 + share), x0 + wshare), nullptr);
 
   const unsigned char* ring = smem + C::SM_RING + (size_t)warp * C::STAGES * C::STAGE;
   const uint32_t ring_s = smem_addr(ring);
 
   if (w0 < w1) {
-    Place at;                       // the unit to be consumed next
-    {
-      int lo = 0, hi = p.n_req;     // pre[lo] * hcn <= w0 < pre[hi] * hcn
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((long long)pre[mid] * hcn <= w0) lo = mid; else hi = mid;
-      }
-      at.ri = lo;
-      at.n = pre[lo + 1] - pre[lo];
-      const int rem = (int)(w0 - (long long)pre[lo] * hcn);
-      at.hc = rem / at.n;
-      at.u = rem - at.hc * at.n;
+    while (at.n == 0) {             // requests without positions have no units
+      ++at.ri;
+      at.hc = at.u = 0;
+      at.n = pre[at.ri + 1] - pre[at.ri];
     }
     Place is = at;                  // the unit whose copy starts next
     long long to_issue = w1 - w0, to_do = w1 - w0;
@@ -649,7 +662,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
       }
     }
     if (a.from == 0 && to < a.n) {
-      const long long end = (long long)pre[a.ri] * hcn + (long long)(a.hc + 1) * a.n;   // of the segment
+      const long long end = cost_before(a.ri) + (long long)(a.hc + 1) * (a.n + SEGMENT_COST);   // of the segment
       chain = Chain{a.ri, a.hc, (int)((end - 1) / share), 0};
     }
   }
@@ -732,8 +745,15 @@ template <int D, int NT, int QTYPE, bool E4M3>
 cudaError_t go(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st) {
   using C = Cfg<D, NT, QTYPE, E4M3>;
   const size_t smem = C::smem(p.n_req);
-  cudaError_t e = allow_smem(paged_decode_kernel<D, NT, QTYPE, E4M3>, C::smem(PG_MAX_REQUESTS));
-  if (e != cudaSuccess) return e;
+  // the kernel's shared-memory allowance, once per device (a bit each; devices past 63 every time)
+  static std::atomic<uint64_t> allowed{0};
+  const uint64_t bit = p.device < 64 ? 1ull << p.device : 0;
+  cudaError_t e = cudaSuccess;
+  if (!(allowed.load(std::memory_order_acquire) & bit)) {
+    e = allow_smem(paged_decode_kernel<D, NT, QTYPE, E4M3>, C::smem(PG_MAX_REQUESTS));
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(bit, std::memory_order_release);
+  }
   e = launch_pdl(paged_decode_kernel<D, NT, QTYPE, E4M3>, dim3(p.grid), dim3(C::THREADS), smem, st, p, map);
   if (e != cudaSuccess) return e;
   return launch_pdl(paged_join_kernel<D, NT, QTYPE, E4M3>, dim3(p.grid, C::HEADS), dim3(256), 0, st, p);

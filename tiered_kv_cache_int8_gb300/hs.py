@@ -149,7 +149,7 @@ def lib():
         L.hs_paged_destroy.argtypes = [VP]
         L.hs_paged_destroy.restype = None
         L.hs_paged_append.argtypes = [VP, I32, I32, VP, I32, VP, VP, VP, VP, P(HsRotary), P(HsHeads), P(HsHeads),
-                                      P(HsHeads), P(HsHeads), VP]
+                                      VP, VP, VP]
         L.hs_paged_append.restype = ctypes.c_int
         L.hs_paged_workspace_bytes.argtypes = [VP]
         L.hs_paged_workspace_bytes.restype = ctypes.c_int64

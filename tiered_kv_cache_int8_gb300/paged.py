@@ -16,7 +16,12 @@ from .hs import (HS_BF16, HS_E4M3, HS_ERR_DEVICE, HS_FP16, HS_FP32, HS_OK, HS_RO
                  HS_ROTARY_NTK, HS_ROTARY_PLAIN, HsError, HsHeads, HsPagedConfig, HsRotary, HsRotaryConfig, lib)
 
 TYPES = {torch.bfloat16: HS_BF16, torch.float16: HS_FP16, torch.float32: HS_FP32, torch.float8_e4m3fn: HS_E4M3}
+_ROTATED = {torch.bfloat16: HS_BF16, torch.float16: HS_FP16, torch.float32: HS_FP32}
+_VIEWS = (None, HsHeads * 1, HsHeads * 2)
 SCALINGS = {"linear": HS_ROTARY_LINEAR, "ntk": HS_ROTARY_NTK, "by_parts": HS_ROTARY_BY_PARTS}
+
+
+_HEADS_BYTES = ctypes.sizeof(HsHeads)
 
 
 def _check(rc: int):
@@ -42,39 +47,36 @@ def _heads(name: str, x, device, dtype, d: int | None = None, heads: int | None 
     return HsHeads(x.data_ptr(), ts, hs, h, 0)
 
 
-def _ints(name: str, x, device, shape):
-    if x.dtype != torch.int32 or x.device != device or tuple(x.shape) != tuple(shape) or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device}, "
+def _dense(x, shape) -> HsHeads:
+    """The view of a new tensor of that shape."""
+    _, h, d = shape
+    return HsHeads(x.data_ptr(), h * d, d, h, 0)
+
+
+def _ints(name: str, x, device, n: int):
+    if x.dtype != torch.int32 or x.device != device or x.shape != (n,) or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor [{n}] on {device}, "
                          f"not {list(x.shape)} {x.dtype} on {x.device}")
     return x.data_ptr()
 
 
-class _On:
-    """The stream of a call: the current one, or a given one, on which the call's
-    own tensors are then allocated and the given tensors are marked as used."""
+# the current stream's handle, without building the Stream object where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, stream, device, tensors):
-        self.ctx = None
-        if stream is None:
-            self.raw = torch.cuda.current_stream(device).cuda_stream
-            return
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        self.raw = stream.cuda_stream
-        if self.raw != torch.cuda.current_stream(device).cuda_stream:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-            self.ctx = torch.cuda.stream(stream)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.raw
-
-    def __exit__(self, *a):
-        if self.ctx is not None:
-            self.ctx.__exit__(*a)
+def _on_stream(call, stream, device, tensors):
+    """call(handle) on a given stream: what it allocates belongs to that stream, and the
+    given tensors are marked as used there."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.cuda_stream == _raw_stream(device.index):
+        return call(stream.cuda_stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 class Rotary:
@@ -114,7 +116,8 @@ class Rotary:
         self.device = torch.device("cuda", device)
         as_signed = [t - (1 << 64) if t >> 63 else t for t in self.turns]
         self._table = torch.tensor(as_signed, dtype=torch.int64, device=self.device)
-        self.plan = tuple(HsRotary(self._table.data_ptr(), rot_dim, int(interleaved), t, mag.value) for t in (0, 1))
+        self._plan = tuple(ctypes.byref(HsRotary(self._table.data_ptr(), rot_dim, int(interleaved), t, mag.value))
+                           for t in (0, 1))
         # the table's copy is on the stream of the creation; calls may be on any
         torch.cuda.current_stream(self.device).synchronize()
 
@@ -126,27 +129,41 @@ class Rotary:
         transpose : the transposed rotation (angles negated): what takes a gradient of
                     the rotated values back; the inverse where magnitude is 1
         """
-        _need(len(xs) in (1, 2), "apply takes one or two tensors")
-        dev, x0 = self.device, xs[0]
+        k = len(xs)
+        if k != 1 and k != 2:
+            raise ValueError("apply takes one or two tensors")
+        dev, x0, x1 = self.device, xs[0], xs[-1]
         dtype = x0.dtype
-        _need(dtype in (torch.bfloat16, torch.float16, torch.float32), f"no rotation of {dtype}")
-        views = [_heads("x", x, dev, dtype) for x in xs]
-        n, d = int(x0.shape[0]), int(x0.shape[2])
-        _need(all(x.shape[0] == n and x.shape[2] == d for x in xs), "the tensors have different tokens or widths")
-        pos = _ints("positions", positions, dev, (n,))
-        if out is not None:
+        if dtype not in _ROTATED:
+            raise ValueError(f"no rotation of {dtype}")
+        views = _VIEWS[k](*[_heads("x", x, dev, dtype) for x in xs])
+        n, _, d = x0.shape
+        if k == 2 and (x1.shape[0] != n or x1.shape[2] != d):
+            raise ValueError("the tensors have different tokens or widths")
+        pos = _ints("positions", positions, dev, n)
+        if out is None:
+            outs = None
+        else:
             outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
-            _need(len(outs) == len(xs) and all(o.shape == x.shape for o, x in zip(outs, xs)),
-                  "out must have the shapes of the inputs")
-        with _On(stream, dev, (positions, *xs, *(outs if out is not None else ()))) as raw:
-            if out is None:
-                outs = tuple(torch.empty(x.shape, dtype=dtype, device=dev) for x in xs)
-            k = len(xs)
-            _check(lib().hs_rotary_apply(ctypes.byref(self.plan[1 if transpose else 0]), TYPES[dtype], d, n, pos, k,
-                                         (HsHeads * k)(*views),
-                                         (HsHeads * k)(*[_heads("out", o, dev, dtype) for o in outs]),
-                                         dev.index, raw))
-        return outs[0] if k == 1 else outs
+            if len(outs) != k or any(o.shape != x.shape for o, x in zip(outs, xs)):
+                raise ValueError("out must have the shapes of the inputs")
+
+        def call(raw):
+            ys = outs
+            if ys is None:
+                ys = tuple([torch.empty(x.shape, dtype=dtype, device=dev) for x in xs])
+                into = _VIEWS[k](*[_dense(y, x.shape) for x, y in zip(xs, ys)])
+            else:
+                into = _VIEWS[k](*[_heads("out", y, dev, dtype) for y in ys])
+            rc = lib().hs_rotary_apply(self._plan[1 if transpose else 0], _ROTATED[dtype], d, n, pos, k, views, into,
+                                       dev.index, raw)
+            if rc:
+                _check(rc)
+            return ys[0] if k == 1 else ys
+
+        if stream is None:
+            return call(_raw_stream(dev.index))
+        return _on_stream(call, stream, dev, (positions, *xs, *(outs or ())))
 
 
 class PagedKVCache:
@@ -265,36 +282,48 @@ class PagedKVCache:
                       None: one row per request (with req_ids: the same number for each)
         req_ids     : int32 [requests] distinct ids; None: requests 0, 1, ...
         """
-        dev, n = self.device, int(k.shape[0])
-        hk = _heads("k", k, dev, self.dtype, self.d, self.h_kv)
-        hv = _heads("v", v, dev, self.dtype, self.d, self.h_kv)
-        _need(v.shape[0] == n, "k and v have different numbers of rows")
+        dev, dtype, n = self.device, self.dtype, k.shape[0]
+        views = _VIEWS[2](_heads("k", k, dev, dtype, self.d, self.h_kv), _heads("v", v, dev, dtype, self.d, self.h_kv))
+        if v.shape[0] != n:
+            raise ValueError("k and v have different numbers of rows")
+        n_req, ids, offs = n, None, None
         if req_ids is not None:
-            n_req = int(req_ids.shape[0])
-        elif tok_offsets is not None:
-            n_req = int(tok_offsets.shape[0]) - 1
-        else:
-            n_req = n
-        ids = None if req_ids is None else _ints("req_ids", req_ids, dev, (n_req,))
-        offs = None if tok_offsets is None else _ints("tok_offsets", tok_offsets, dev, (n_req + 1,))
-        hq = ho = None
+            n_req = req_ids.shape[0]
+            ids = _ints("req_ids", req_ids, dev, n_req)
+        if tok_offsets is not None:
+            if req_ids is None:
+                n_req = tok_offsets.shape[0] - 1
+            offs = _ints("tok_offsets", tok_offsets, dev, n_req + 1)
+        hq = None
         if q is not None:
-            _need(self.rotary is not None, "q needs a cache with a rotation")
-            hq = _heads("q", q, dev, self.dtype, self.d, self.h_q)
-            _need(q.shape[0] == n and (q_out is None or q_out.shape == q.shape), "q, q_out and k have different rows")
-        else:
-            _need(q_out is None, "q_out without q")
-        with _On(stream, dev, (k, v, q, q_out, req_ids, tok_offsets)) as raw:
-            if q is not None:
-                if q_out is None:
-                    q_out = torch.empty(q.shape, dtype=self.dtype, device=dev)
-                ho = ctypes.byref(_heads("q_out", q_out, dev, self.dtype, self.d, self.h_q))
-                hq = ctypes.byref(hq)
-            rot = None if self.rotary is None else ctypes.byref(self.rotary.plan[0])
-            _check(lib().hs_paged_append(self._h, layer, n_req, ids, n, offs, self.page_table.data_ptr(),
-                                         self.lengths.data_ptr(), self.next_lengths.data_ptr(), rot, hq, ho,
-                                         ctypes.byref(hk), ctypes.byref(hv), raw))
-        return q_out
+            if self.rotary is None:
+                raise ValueError("q needs a cache with a rotation")
+            hq = _heads("q", q, dev, dtype, self.d, self.h_q)
+            if q.shape[0] != n or (q_out is not None and q_out.shape != q.shape):
+                raise ValueError("q, q_out and k have different rows")
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+
+        def call(raw):
+            out, h_in, h_out = q_out, None, None
+            if hq is not None:
+                if out is None:
+                    out = torch.empty(q.shape, dtype=dtype, device=dev)
+                    h_out = ctypes.byref(_dense(out, q.shape))
+                else:
+                    h_out = ctypes.byref(_heads("q_out", out, dev, dtype, self.d, self.h_q))
+                h_in = ctypes.byref(hq)
+            rc = lib().hs_paged_append(self._h, layer, n_req, ids, n, offs, self.page_table.data_ptr(),
+                                       self.lengths.data_ptr(), self.next_lengths.data_ptr(),
+                                       None if self.rotary is None else self.rotary._plan[0], h_in, h_out, views,
+                                       ctypes.byref(views, _HEADS_BYTES), raw)
+            if rc:
+                _check(rc)
+            return out
+
+        if stream is None:
+            return call(_raw_stream(dev.index))
+        return _on_stream(call, stream, dev, (k, v, q, q_out, req_ids, tok_offsets))
 
     def decode(self, layer: int, q, req_ids=None, lengths=None, out=None, return_lse: bool = False, stream=None):
         """Attention of one token per request: q [requests, h_q, d] -> out of its shape
@@ -302,24 +331,32 @@ class PagedKVCache:
 
         lengths : int32 [max_requests], positions attended to; None: next_lengths
         """
-        dev, n = self.device, int(q.shape[0])
-        hq = _heads("q", q, dev, self.dtype, self.d, self.h_q)
-        ids = None if req_ids is None else _ints("req_ids", req_ids, dev, (n,))
-        if lengths is None:
-            lens = self.next_lengths.data_ptr()
-        else:
-            lens = _ints("lengths", lengths, dev, (self.max_requests,))
-        if out is not None:
-            _need(out.shape == q.shape and out.dtype == self.dtype and out.device == dev and out.is_contiguous(),
-                  "out must be contiguous, of q's shape, type and device")
-        with _On(stream, dev, (q, req_ids, lengths, out)) as raw:
-            if out is None:
-                out = torch.empty((n, self.h_q, self.d), dtype=self.dtype, device=dev)
-            lse = torch.empty((n, self.h_q), dtype=torch.float32, device=dev) if return_lse else None
+        dev, dtype, n = self.device, self.dtype, q.shape[0]
+        hq = ctypes.byref(_heads("q", q, dev, dtype, self.d, self.h_q))
+        ids = None if req_ids is None else _ints("req_ids", req_ids, dev, n)
+        lens = (self.next_lengths.data_ptr() if lengths is None
+                else _ints("lengths", lengths, dev, self.max_requests))
+        if out is not None and (out.shape != q.shape or out.dtype != dtype or out.device != dev
+                                or not out.is_contiguous()):
+            raise ValueError("out must be contiguous, of q's shape, type and device")
+
+        def call(raw):
+            o, lse, lse_ptr = out, None, None
+            if o is None:
+                o = torch.empty(q.shape, dtype=dtype, device=dev)
+            if return_lse:
+                lse = torch.empty((n, self.h_q), dtype=torch.float32, device=dev)
+                lse_ptr = lse.data_ptr()
             ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
-            _check(lib().hs_paged_decode(self._h, layer, n, ids, self.page_table.data_ptr(), lens, ctypes.byref(hq),
-                                         out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), raw))
-        return (out, lse) if return_lse else out
+            rc = lib().hs_paged_decode(self._h, layer, n, ids, self.page_table.data_ptr(), lens, hq, o.data_ptr(),
+                                       lse_ptr, ws.data_ptr(), raw)
+            if rc:
+                _check(rc)
+            return (o, lse) if return_lse else o
+
+        if stream is None:
+            return call(_raw_stream(dev.index))
+        return _on_stream(call, stream, dev, (q, req_ids, lengths, out))
 
     # -- errors ----------------------------------------------------------------------
     def device_error(self) -> int:
