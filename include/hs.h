@@ -411,7 +411,7 @@ int hs_indexer_topk_static_error(int32_t device, uint32_t* out);
 #define HS_E4M3 3 /* 8-bit e4m3 pages, with one scale per kv head */
 
 /* A [tokens][heads][d] view of 16- or 32-bit elements: element (t, h, i) is at
- * data + t * token_stride + h * head_stride + i (strides in elements, >= 0). */
+ * data + t * token_stride + h * head_stride + i (strides in elements, >= 0); 1 to 4096 heads. */
 typedef struct hs_heads {
   void* data;
   int64_t token_stride;
@@ -490,7 +490,8 @@ int hs_rotary_apply(const hs_rotary_t* rot, int32_t type, int32_t d, int32_t n_t
  * The page size must be 16, 32, 64, 128 or 256; d 64, 128 or 256 (keys and values
  * alike); h_q % h_kv == 0.  Queries, new keys and values and outputs are `type`
  * (HS_BF16 or HS_FP16); pages are the same type or HS_E4M3: then they hold
- * value / kv_scale[layer][0 key, 1 value][kv head], saturated to +-448.
+ * value * (1 / kv_scale[layer][0 key, 1 value][kv head]) in 32 bits, rounded once and
+ * saturated to +-448.
  */
 typedef struct hs_paged_config {
   int32_t n_layers;
@@ -530,7 +531,7 @@ void hs_paged_destroy(hs_paged_t* h);
  *   tok_offsets : dev int32 [n_req + 1], or NULL.  Request i of the call takes rows
  *                 tok_offsets[i] .. tok_offsets[i+1]-1 (none where they are equal); rows
  *                 before the first and from the last offset on belong to no request and
- *                 are neither read nor written.  NULL: n_tok / n_req rows each (n_tok must
+ *                 are not used, nor their rows of q_out written.  NULL: n_tok / n_req rows each (n_tok must
  *                 be a multiple of n_req)
  *   page_table  : dev int32 [max_requests][max_pages]
  *   lengths     : dev int32 [max_requests]: positions held before the call

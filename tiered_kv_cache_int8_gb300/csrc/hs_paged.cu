@@ -42,7 +42,7 @@ long long extent(const hs_heads_t& v, int n_tok, int d) {
 // "" or why the view cannot be used
 const char* check_view(const hs_heads_t& v, int n_tok, int d, size_t es, bool written) {
   if (!v.data) return "a view's data is null";
-  if (v.heads < 1 || v.heads > 65536) return "a view's heads must be in [1, 65536]";
+  if (v.heads < 1 || v.heads > 4096) return "a view's heads must be in [1, 4096]";
   const int64_t lim = (int64_t)1 << 40;
   if (v.token_stride < 0 || v.head_stride < 0 || v.token_stride > lim || v.head_stride > lim)
     return "a view's strides must be in [0, 2^40]";
@@ -226,7 +226,6 @@ int hs_rotary_apply(const hs_rotary_t* rot, int32_t type, int32_t d, int32_t n_t
     if (const char* why = check_pair(in[i], out[i], n_tok, d, es); *why) return named(HS_ERR_INVALID, me, why);
     wide = wide && wide_view(in[i], es) && wide_view(out[i], es);
     p.v[i] = row_view(in[i], &out[i], hs::VIEW_ROTATE);
-    p.rows += in[i].heads;
   }
   p.n_views = n_views;
   p.d = d;
@@ -330,7 +329,6 @@ int hs_paged_append(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
     p.v[n++] = row_view(*k, nullptr, hs::VIEW_KEYS);
     p.v[n++] = row_view(*v, nullptr, hs::VIEW_VALUES);
     p.n_views = n;
-    for (int i = 0; i < n; ++i) p.rows += p.v[i].heads;
   }
   p.d = c.d;
   p.n_tok = n_tok;

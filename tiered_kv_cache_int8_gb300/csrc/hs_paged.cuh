@@ -38,15 +38,16 @@ struct RowView {
   int64_t in_ts, in_hs, out_ts, out_hs;
   int32_t heads;
   int32_t kind;
+  int32_t chunk_heads, chunks;   // heads of a thread, threads for a row's heads
 };
 
 struct RotateParams {
   RowView v[3];
   int32_t n_views;
-  int32_t rows;          // heads of all views together
   int32_t d;
   int32_t n_tok;
-  int32_t tok_per_cta;
+  uint32_t first_cta[3]; // of each view
+  int32_t groups;        // (token, chunk of heads) pairs of a CTA
   int32_t rot_dim;       // 0: no rotation
   int32_t items;         // work items of a row
   float magnitude;

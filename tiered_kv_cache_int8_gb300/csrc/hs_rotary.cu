@@ -7,8 +7,7 @@
 // The angle is kept as a fraction of a turn in 64-bit fixed point: position times
 // the table entry wraps modulo one turn exactly, so a position of a million loses
 // nothing (in 32-bit floats its angle would be off by 0.06 rad); the top 32 bits
-// then go through sincospi.  The cosines and sines of a CTA's tokens are computed
-// once per pair, into shared memory, and serve every head.
+// then go through sincospi.
 //
 // Memory-bound: each element is read and written once, 16 bytes at a time where
 // the views allow it.
@@ -18,24 +17,30 @@ namespace hs {
 namespace {
 
 constexpr int ROT_THREADS = 256;
-constexpr int ROT_MAX_TOK = 4;   // tokens of a CTA
+constexpr int ROT_HEADS = 16;   // most heads of a thread
 
 template <typename T>
 struct Elem;
 template <>
 struct Elem<__nv_bfloat16> {
+  using Two = __nv_bfloat162;
   static __device__ __forceinline__ float up(__nv_bfloat16 x) { return __bfloat162float(x); }
   static __device__ __forceinline__ __nv_bfloat16 down(float x) { return __float2bfloat16_rn(x); }
+  static __device__ __forceinline__ Two down2(float x, float y) { return __floats2bfloat162_rn(x, y); }
 };
 template <>
 struct Elem<__half> {
+  using Two = __half2;
   static __device__ __forceinline__ float up(__half x) { return __half2float(x); }
   static __device__ __forceinline__ __half down(float x) { return __float2half_rn(x); }
+  static __device__ __forceinline__ Two down2(float x, float y) { return __floats2half2_rn(x, y); }
 };
 template <>
 struct Elem<float> {
+  using Two = float2;
   static __device__ __forceinline__ float up(float x) { return x; }
   static __device__ __forceinline__ float down(float x) { return x; }
+  static __device__ __forceinline__ Two down2(float x, float y) { return make_float2(x, y); }
 };
 
 // VEC consecutive elements: one 16-byte access, or one element (VEC = 1).
@@ -50,27 +55,36 @@ __device__ __forceinline__ void load_row(const T* p, T (&x)[VEC]) {
 }
 template <typename T, int VEC>
 __device__ __forceinline__ void store_row(T* p, const float (&x)[VEC]) {
-  alignas(16) T y[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) y[i] = Elem<T>::down(x[i]);
   if constexpr (VEC == 1) {
-    p[0] = y[0];
+    p[0] = Elem<T>::down(x[0]);
   } else {
+    alignas(16) typename Elem<T>::Two y[VEC / 2];
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) y[i / 2] = Elem<T>::down2(x[i], x[i + 1]);
     *reinterpret_cast<int4*>(p) = *reinterpret_cast<const int4*>(y);
   }
 }
-// the same into 8-bit pages: value / scale, saturated (a NaN stays one)
+// the same into 8-bit pages: times 1 / scale, saturated (a NaN stays one)
 template <int VEC>
-__device__ __forceinline__ void store_e4m3(unsigned char* p, const float (&x)[VEC], float scale) {
-  alignas(8) unsigned char y[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) y[i] = __nv_cvt_float_to_fp8(__fdiv_rn(x[i], scale), __NV_SATFINITE, __NV_E4M3);
-  if constexpr (VEC == 8) {
-    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(y);
+__device__ __forceinline__ void store_e4m3(unsigned char* p, const float (&x)[VEC], float inv_scale) {
+  if constexpr (VEC == 1) {
+    p[0] = __nv_cvt_float_to_fp8(x[0] * inv_scale, __NV_SATFINITE, __NV_E4M3);
   } else {
+    static_assert(VEC == 8, "8-byte stores");
+    alignas(8) __nv_fp8x2_storage_t y[VEC / 2];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) p[i] = y[i];
+    for (int i = 0; i < VEC; i += 2)
+      y[i / 2] = __nv_cvt_float2_to_fp8x2(make_float2(x[i] * inv_scale, x[i + 1] * inv_scale), __NV_SATFINITE, __NV_E4M3);
+    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(y);
   }
+}
+
+// One rounding of each product and sum is fixed here, so that every variant of the
+// kernel (access widths, layouts, alone or on the way into the pages) gives the same bits.
+__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
+  const float x = __fmaf_rn(a, c, -__fmul_rn(b, s));
+  b = __fmaf_rn(b, c, __fmul_rn(a, s));
+  a = x;
 }
 
 // Where a token goes: its position, and its page row (pages of the layer are
@@ -125,10 +139,24 @@ __device__ __forceinline__ bool takes(const RotateParams& p, int req, int len, i
   return true;
 }
 
-__device__ Token locate(const RotateParams& p, int t) {   // one warp
+// The place of token row t, of request `near` or one behind it.
+__device__ Token locate(const RotateParams& p, int t, int near) {
   Token k = {0, 0, -1, 0};
   unsigned err = 0;
-  const int i = p.tok_offsets ? request_of(p.tok_offsets, p.n_req, t) : t / p.tok_per_req;
+  int i = near;
+  if (p.tok_offsets) {
+    // strides that double from the neighbour's request, then halve
+    int hi = i + 1, step = 1;
+    while (hi < p.n_req && p.tok_offsets[hi] <= t) {
+      i = hi;
+      step <<= 1;
+      hi = min(p.n_req, hi + step);
+    }
+    while (hi - i > 1) {
+      const int mid = (i + hi) >> 1;
+      if (p.tok_offsets[mid] <= t) i = mid; else hi = mid;
+    }
+  }
   int first;
   const int n = new_tokens(p, i, &first, &err);
   const int j = t - first;
@@ -150,7 +178,7 @@ __device__ Token locate(const RotateParams& p, int t) {   // one warp
       }
     }
   }
-  if (err && (threadIdx.x & 31) == 0) set_error(p.dev_error, err);
+  if (err) set_error(p.dev_error, err);
   return k;
 }
 
@@ -158,24 +186,72 @@ __device__ Token locate(const RotateParams& p, int t) {   // one warp
 // (i, i + rot/2); APPEND: positions from lengths, views of kind KEYS and VALUES go
 // to the pages (E4M3: 8-bit pages).
 //
-// Work items of a row, in order: half layout: rot / (2 VEC) items of two accesses
-// (i and i + rot/2), then (d - rot) / VEC copies; interleaved: d / VEC accesses.
+// Work items of a row, in order: half layout (and VEC = 1): rot / (2 VEC) items of two
+// accesses (i and i + rot/2), then (d - rot) / VEC copies; interleaved: d / VEC accesses.
+// A thread has one item of one token and goes down the token's heads with it, so the
+// cosines and sines of its pairs are computed once, by it, and stay in registers: no
+// table, no barrier, and the next head is a stride further.  BATCH heads are loaded
+// ahead of those being turned, the first before the token's position is known.  A view's
+// heads are split over several threads where there are few tokens.
+template <typename T, int VEC, bool INTER>
+struct Shape {
+  static constexpr bool PAIRS = INTER && VEC > 1;              // both elements of a pair in one access
+  static constexpr int PER_ITEM = PAIRS ? VEC / 2 : VEC;       // pairs of an item
+  static constexpr int BATCH = PAIRS ? 4 : 2;                  // 64 bytes a thread in flight
+  // rows of single elements may need a thread each: up to 1023 of them
+  static constexpr int MAX_THREADS = VEC > 1 ? ROT_THREADS : 1024;
+};
+
+template <typename T, int VEC>
+struct Item {
+  alignas(16) T a[VEC];
+  alignas(16) T b[VEC];
+};
+
 template <typename T, int VEC, bool INTER, bool APPEND, bool E4M3>
-__global__ void __launch_bounds__(ROT_THREADS) rotate_kernel(const __grid_constant__ RotateParams p) {
-  extern __shared__ float2 s_cs[];              // [tok_per_cta][rot / 2]: (cos, sin) times magnitude
-  __shared__ Token s_tok[ROT_MAX_TOK];
+__global__ void __launch_bounds__(Shape<T, VEC, INTER>::MAX_THREADS, VEC > 1 ? 3 : 1)
+    rotate_kernel(const __grid_constant__ RotateParams p) {
+  using S = Shape<T, VEC, INTER>;
+  const int tid = threadIdx.x;
+  const int vi = blockIdx.x >= p.first_cta[2] ? 2 : blockIdx.x >= p.first_cta[1] ? 1 : 0;
+  const RowView& view = p.v[vi];
+  const int per = p.items, half = p.rot_dim / 2;
+  const int pairs = half / S::PER_ITEM;         // items that turn pairs
+  const int grp = tid / per, j = tid - grp * per;
+  const unsigned unit = (blockIdx.x - p.first_cta[vi]) * p.groups + grp;
+  const unsigned tu = unit / view.chunks;       // the token
+  const int chunk = unit - tu * view.chunks;
+  const bool mine = grp < p.groups && tu < (unsigned)p.n_tok;
+  const int t = mine ? (int)tu : 0;
+  int h = chunk * view.chunk_heads;
+  const int h1 = mine ? min(view.heads, h + view.chunk_heads) : h;
   griddep_wait();
   griddep_launch_dependents();
-  const int tid = threadIdx.x;
-  const int t0 = blockIdx.x * p.tok_per_cta;
-  const int nt = min(p.tok_per_cta, p.n_tok - t0);
+
+  const T* in = static_cast<const T*>(view.in) + t * view.in_ts + h * view.in_hs;
+  // the item's places in a row
+  const bool two = !S::PAIRS && j < pairs;
+  const int ia = S::PAIRS ? j * VEC : two ? (INTER ? 2 * j : j * VEC) : p.rot_dim + (j - pairs) * VEC;
+  const int ib = INTER ? 2 * j + 1 : half + j * VEC;
+  const long long in_hs = view.in_hs;
+  auto load_batch = [&](const T* from, int n, Item<T, VEC>(&d)[S::BATCH]) {
+#pragma unroll
+    for (int u = 0; u < S::BATCH; ++u)
+      if (u < n) {
+        load_row<T, VEC>(from + u * in_hs + ia, d[u].a);
+        if (two) load_row<T, VEC>(from + u * in_hs + ib, d[u].b);
+      }
+  };
+  Item<T, VEC> cur[S::BATCH], nxt[S::BATCH];
+  load_batch(in, h1 - h, cur);
+
+  const int kind = APPEND ? view.kind : VIEW_ROTATE;
+  const bool turn = kind != VIEW_VALUES && j < pairs;
+  int pos = 0;
+  Token tok = {0, 1, -1, 0};
   if constexpr (APPEND) {
-    for (int w = tid >> 5; w < nt; w += ROT_THREADS / 32) {
-      const Token k = locate(p, t0 + w);
-      if ((tid & 31) == 0) s_tok[w] = k;
-    }
     if (p.next_lengths) {
-      for (int i = blockIdx.x * ROT_THREADS + tid; i < p.n_req; i += gridDim.x * ROT_THREADS) {
+      for (int i = blockIdx.x * blockDim.x + tid; i < p.n_req; i += gridDim.x * blockDim.x) {
         const int req = p.req_ids ? p.req_ids[i] : i;
         unsigned err = 0;
         int first;
@@ -189,118 +265,121 @@ __global__ void __launch_bounds__(ROT_THREADS) rotate_kernel(const __grid_consta
         if (err) set_error(p.dev_error, err);
       }
     }
-    if (nt <= 0) return;
-    __syncthreads();
+    if (p.n_tok == 0) return;
+    // the request of the warp's first token, then each lane's from there (tokens do not descend along a warp)
+    __syncwarp();
+    int near = 0;
+    if (p.tok_offsets) {
+      const int t_first = __reduce_min_sync(FULL_MASK, mine ? t : p.n_tok - 1);
+      near = request_of(p.tok_offsets, p.n_req, t_first);
+    } else if (mine) {
+      near = t / p.tok_per_req;
+    }
+    if (mine) tok = locate(p, t, near);
+    pos = tok.pos;
+  } else {
+    if (mine) pos = p.positions[t];
   }
-  const int half = p.rot_dim / 2;
-  for (int e = tid; e < nt * half; e += ROT_THREADS) {
-    const int t = e / half, i = e - t * half;
-    int pos;
-    if constexpr (APPEND) pos = s_tok[t].pos; else pos = p.positions[t0 + t];
-    const uint64_t turn = (uint64_t)(int64_t)pos * p.turns[i];
-    // the top 32 bits, signed: a fraction of a turn in [-1/2, 1/2)
-    const float x = (float)(int32_t)(turn >> 32) * (1.0f / 2147483648.0f);
-    float s, c;
-    sincospif(x, &s, &c);
-    s_cs[e] = make_float2(c * p.magnitude, s * p.magnitude * p.sign);
-  }
-  __syncthreads();
+  if (!mine) return;
 
-  const int n_turn = INTER ? p.rot_dim / VEC : half / VEC;   // items that turn pairs (VEC = 1, INTER: see below)
-  const int per = p.items;
-  for (int it = tid; it < nt * p.rows * per; it += ROT_THREADS) {
-    const int j = it % per;
-    const int r = it / per;
-    const int t = r / p.rows;
-    int h = r - t * p.rows;
-    int v = 0;
-    while (h >= p.v[v].heads) h -= p.v[v++].heads;
-    const RowView& view = p.v[v];
-    Token tok = {0, 1, 0, 0};
-    if constexpr (APPEND) {
-      tok = s_tok[t];
-      if (!tok.ok || (view.kind != VIEW_ROTATE && tok.page < 0)) continue;
-    }
-    const T* in = static_cast<const T*>(view.in) + (t0 + t) * view.in_ts + h * view.in_hs;
-    T* out = nullptr;
-    unsigned char* out8 = nullptr;
-    float scale = 1.0f;
-    if (!APPEND || view.kind == VIEW_ROTATE) {
-      out = static_cast<T*>(view.out) + (t0 + t) * view.out_ts + h * view.out_hs;
-    } else {
-      const int which = view.kind == VIEW_VALUES;
-      const long long row = ((((long long)tok.page * 2 + which) * p.h_kv + h) << p.page_shift) + tok.slot;
-      if constexpr (E4M3) {
-        out8 = p.pages + row * p.d;
-        scale = p.kv_scale[which * p.h_kv + h];
-      } else {
-        out = reinterpret_cast<T*>(p.pages) + row * p.d;
-      }
-    }
-    auto put = [&](int at, const float (&y)[VEC]) {
-      if (E4M3 && out8)
-        store_e4m3<VEC>(out8 + at, y, scale);
-      else
-        store_row<T, VEC>(out + at, y);
-    };
-    const bool turn = view.kind != VIEW_VALUES;
-    const float2* cs = s_cs + t * half;
-    if (INTER && VEC > 1) {
-      alignas(16) T x[VEC];
-      float y[VEC];
-      load_row<T, VEC>(in + j * VEC, x);
+  float cs[S::PER_ITEM], sn[S::PER_ITEM];
+  if (turn) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) y[e] = Elem<T>::up(x[e]);
-      if (turn && j < n_turn) {
-#pragma unroll
-        for (int e = 0; e < VEC; e += 2) {
-          const float2 w = cs[(j * VEC + e) / 2];
-          const float a = y[e], b = y[e + 1];
-          y[e] = a * w.x - b * w.y;
-          y[e + 1] = b * w.x + a * w.y;
-        }
-      }
-      put(j * VEC, y);
+    for (int e = 0; e < S::PER_ITEM; ++e) {
+      const uint64_t angle = (uint64_t)(int64_t)pos * p.turns[j * S::PER_ITEM + e];
+      // the top 32 bits, signed: a fraction of a turn in [-1/2, 1/2)
+      const float x = (float)(int32_t)(angle >> 32) * (1.0f / 2147483648.0f);
+      sincospif(x, &sn[e], &cs[e]);
+      cs[e] *= p.magnitude;
+      sn[e] *= p.magnitude * p.sign;
+    }
+  }
+
+  T* out = nullptr;
+  unsigned char* out8 = nullptr;
+  long long out_hs = view.out_hs;
+  const float* scale = nullptr;
+  if (kind == VIEW_ROTATE) {
+    if (!tok.ok) return;
+    out = static_cast<T*>(view.out) + t * view.out_ts + h * out_hs;
+  } else {
+    if (tok.page < 0) return;
+    const int which = kind == VIEW_VALUES;
+    const long long row = ((((long long)tok.page * 2 + which) * p.h_kv + h) << p.page_shift) + tok.slot;
+    out_hs = (long long)p.d << p.page_shift;
+    if constexpr (E4M3) {
+      out8 = p.pages + row * p.d;
+      scale = p.kv_scale + which * p.h_kv;
     } else {
-      // pairs at (ia, ib): VEC of them per item; VEC = 1 takes either layout
-      const int pairs = half / VEC;
-      if (j < pairs) {
-        const int ia = INTER ? 2 * j : j * VEC, ib = INTER ? 2 * j + 1 : half + j * VEC;
-        alignas(16) T xa[VEC];
-        alignas(16) T xb[VEC];
+      out = reinterpret_cast<T*>(p.pages) + row * p.d;
+    }
+  }
+  for (; h < h1; h += S::BATCH) {
+    in += S::BATCH * in_hs;
+    load_batch(in, h1 - h - S::BATCH, nxt);
+#pragma unroll
+    for (int u = 0; u < S::BATCH; ++u) {
+      if (h + u < h1) {
         float ya[VEC], yb[VEC];
-        load_row<T, VEC>(in + ia, xa);
-        load_row<T, VEC>(in + ib, xb);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float a = Elem<T>::up(xa[e]), b = Elem<T>::up(xb[e]);
-          const float2 w = turn ? cs[j * VEC + e] : make_float2(1.f, 0.f);
-          ya[e] = turn ? a * w.x - b * w.y : a;
-          yb[e] = turn ? b * w.x + a * w.y : b;
+        for (int e = 0; e < VEC; ++e) ya[e] = Elem<T>::up(cur[u].a[e]);
+        if constexpr (S::PAIRS) {
+          if (turn) {
+#pragma unroll
+            for (int e = 0; e < VEC; e += 2) turn_pair(ya[e], ya[e + 1], cs[e / 2], sn[e / 2]);
+          }
+        } else if (two) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            yb[e] = Elem<T>::up(cur[u].b[e]);
+            if (turn) turn_pair(ya[e], yb[e], cs[e], sn[e]);
+          }
         }
-        put(ia, ya);
-        put(ib, yb);
-      } else {
-        const int at = p.rot_dim + (j - pairs) * VEC;
-        alignas(16) T x[VEC];
-        float y[VEC];
-        load_row<T, VEC>(in + at, x);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) y[e] = Elem<T>::up(x[e]);
-        put(at, y);
+        bool to8 = false;
+        if constexpr (E4M3) {
+          if (out8) {
+            const float inv = 1.0f / scale[h + u];
+            store_e4m3<VEC>(out8 + u * out_hs + ia, ya, inv);
+            if (two) store_e4m3<VEC>(out8 + u * out_hs + ib, yb, inv);
+            to8 = true;
+          }
+        }
+        if (!to8) {
+          store_row<T, VEC>(out + u * out_hs + ia, ya);
+          if (two) store_row<T, VEC>(out + u * out_hs + ib, yb);
+        }
       }
     }
+    if (E4M3 && out8) out8 += S::BATCH * out_hs; else out += S::BATCH * out_hs;
+#pragma unroll
+    for (int u = 0; u < S::BATCH; ++u) cur[u] = nxt[u];
   }
 }
 
 template <typename T, int VEC, bool INTER, bool APPEND, bool E4M3>
 cudaError_t go(RotateParams p, cudaStream_t st) {
+  using S = Shape<T, VEC, INTER>;
   const int half = p.rot_dim / 2;
-  p.items = INTER && VEC > 1 ? p.d / VEC : half / VEC + (p.d - p.rot_dim) / VEC;
-  p.tok_per_cta = p.n_tok >= 4 * 152 * ROT_MAX_TOK ? ROT_MAX_TOK : 1;
-  const int grid = std::max(1, (p.n_tok + p.tok_per_cta - 1) / p.tok_per_cta);
-  const size_t smem = (size_t)p.tok_per_cta * half * sizeof(float2);
-  return launch_pdl(rotate_kernel<T, VEC, INTER, APPEND, E4M3>, dim3(grid), dim3(ROT_THREADS), smem, st, p);
+  p.items = S::PAIRS ? p.d / VEC : half / VEC + (p.d - p.rot_dim) / VEC;
+  const int threads = p.items <= ROT_THREADS ? ROT_THREADS : (p.items + 31) / 32 * 32;
+  p.groups = threads / p.items;
+  if (p.n_views == 0) p.v[0].heads = p.v[0].chunks = p.v[0].chunk_heads = 1;   // no tokens: next_lengths only
+  long long cta = 0;
+  for (int v = 0; v < 3; ++v) {
+    p.first_cta[v] = v < p.n_views ? (unsigned)cta : v ? 0xffffffffu : 0u;
+    if (v >= p.n_views) continue;
+    // a thread's heads: all of the view's (ROT_HEADS at most), fewer while the call has not four CTAs for each SM
+    const long long rows = (long long)p.n_tok * p.v[v].heads;
+    const long long wide = (rows * p.items + 4 * 152 * ROT_THREADS - 1) / (4 * 152 * ROT_THREADS);
+    p.v[v].chunk_heads = (int)std::min<long long>(std::min(ROT_HEADS, p.v[v].heads), std::max<long long>(1, wide));
+    p.v[v].chunks = (p.v[v].heads + p.v[v].chunk_heads - 1) / p.v[v].chunk_heads;
+    const long long units = (long long)p.n_tok * p.v[v].chunks;
+    if (units > 0xf0000000LL) return cudaErrorInvalidConfiguration;   // counted with 32 bits
+    cta += (units + p.groups - 1) / p.groups;
+  }
+  if (cta > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const auto kern = rotate_kernel<T, VEC, INTER, APPEND, E4M3>;
+  return launch_pdl(kern, dim3((unsigned)std::max(1LL, cta)), dim3(threads), 0, st, p);
 }
 
 template <typename T, int W, bool APPEND, bool E4M3>
