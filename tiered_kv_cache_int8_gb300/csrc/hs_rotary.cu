@@ -17,7 +17,7 @@ namespace hs {
 namespace {
 
 constexpr int ROT_THREADS = 256;
-constexpr int ROT_HEADS = 16;   // most heads of a thread
+constexpr int ROT_AHEAD = 128;    // most bytes of a thread in flight (256: no faster, fewer CTAs an SM)
 
 template <typename T>
 struct Elem;
@@ -43,16 +43,7 @@ struct Elem<float> {
   static __device__ __forceinline__ Two down2(float x, float y) { return make_float2(x, y); }
 };
 
-// VEC consecutive elements: one 16-byte access, or one element (VEC = 1).
-template <typename T, int VEC>
-__device__ __forceinline__ void load_row(const T* p, T (&x)[VEC]) {
-  if constexpr (VEC == 1) {
-    x[0] = p[0];
-  } else {
-    static_assert(sizeof(T) * VEC == 16, "16-byte accesses");
-    *reinterpret_cast<int4*>(x) = *reinterpret_cast<const int4*>(p);
-  }
-}
+// VEC consecutive elements: one 16-byte store, or one element (VEC = 1).
 template <typename T, int VEC>
 __device__ __forceinline__ void store_row(T* p, const float (&x)[VEC]) {
   if constexpr (VEC == 1) {
@@ -190,26 +181,37 @@ __device__ Token locate(const RotateParams& p, int t, int near) {
 // accesses (i and i + rot/2), then (d - rot) / VEC copies; interleaved: d / VEC accesses.
 // A thread has one item of one token and goes down the token's heads with it, so the
 // cosines and sines of its pairs are computed once, by it, and stay in registers: no
-// table, no barrier, and the next head is a stride further.  BATCH heads are loaded
-// ahead of those being turned, the first before the token's position is known.  A view's
-// heads are split over several threads where there are few tokens.
+// table, no barrier, and the next head is a stride further.  All its heads start on
+// their way into shared memory (each thread's own 16-byte places: nothing to wait for but
+// its own copies) before the token's position and pages are looked up, which takes five
+// dependent reads: with the next heads in registers instead, those reads and the latency
+// of each pair of heads were exposed (20 K tokens of 48 heads into 8-bit pages: 103 us;
+// now 75 us, 6.2 TB/s).  A view's heads are split over several threads, fewer each
+// where there are few tokens.
 template <typename T, int VEC, bool INTER>
 struct Shape {
   static constexpr bool PAIRS = INTER && VEC > 1;              // both elements of a pair in one access
   static constexpr int PER_ITEM = PAIRS ? VEC / 2 : VEC;       // pairs of an item
-  static constexpr int BATCH = PAIRS ? 4 : 2;                  // 64 bytes a thread in flight
+  static constexpr int ACCESSES = PAIRS ? 1 : 2;
+  static constexpr int GROUPS = 4;                             // copies are waited for in this many steps
+  static constexpr int STEP = VEC > 1 ? ROT_AHEAD / (16 * ACCESSES * GROUPS) : 1;   // heads of a step
+  static constexpr int HEADS = STEP * GROUPS;                  // most heads of a thread
   // rows of single elements may need a thread each: up to 1023 of them
   static constexpr int MAX_THREADS = VEC > 1 ? ROT_THREADS : 1024;
 };
 
-template <typename T, int VEC>
-struct Item {
-  alignas(16) T a[VEC];
-  alignas(16) T b[VEC];
-};
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_left(int n) {   // n: a constant once unrolled
+  switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+  }
+}
 
 template <typename T, int VEC, bool INTER, bool APPEND, bool E4M3>
-__global__ void __launch_bounds__(Shape<T, VEC, INTER>::MAX_THREADS, VEC > 1 ? 3 : 1)
+__global__ void __launch_bounds__(Shape<T, VEC, INTER>::MAX_THREADS, VEC > 1 ? 4 : 1)
     rotate_kernel(const __grid_constant__ RotateParams p) {
   using S = Shape<T, VEC, INTER>;
   const int tid = threadIdx.x;
@@ -234,16 +236,21 @@ __global__ void __launch_bounds__(Shape<T, VEC, INTER>::MAX_THREADS, VEC > 1 ? 3
   const int ia = S::PAIRS ? j * VEC : two ? (INTER ? 2 * j : j * VEC) : p.rot_dim + (j - pairs) * VEC;
   const int ib = INTER ? 2 * j + 1 : half + j * VEC;
   const long long in_hs = view.in_hs;
-  auto load_batch = [&](const T* from, int n, Item<T, VEC>(&d)[S::BATCH]) {
+  extern __shared__ int4 s_in[];                // [head][access][thread]
+  if constexpr (VEC > 1) {
 #pragma unroll
-    for (int u = 0; u < S::BATCH; ++u)
-      if (u < n) {
-        load_row<T, VEC>(from + u * in_hs + ia, d[u].a);
-        if (two) load_row<T, VEC>(from + u * in_hs + ib, d[u].b);
+    for (int g = 0; g < S::GROUPS; ++g) {
+#pragma unroll
+      for (int i = 0; i < S::STEP; ++i) {
+        const int u = g * S::STEP + i;
+        if (h + u < h1) {
+          cp_async_16(&s_in[(u * S::ACCESSES) * ROT_THREADS + tid], in + u * in_hs + ia);
+          if (two) cp_async_16(&s_in[(u * S::ACCESSES + 1) * ROT_THREADS + tid], in + u * in_hs + ib);
+        }
       }
-  };
-  Item<T, VEC> cur[S::BATCH], nxt[S::BATCH];
-  load_batch(in, h1 - h, cur);
+      cp_async_commit();
+    }
+  }
 
   const int kind = APPEND ? view.kind : VIEW_ROTATE;
   const bool turn = kind != VIEW_VALUES && j < pairs;
@@ -314,15 +321,26 @@ __global__ void __launch_bounds__(Shape<T, VEC, INTER>::MAX_THREADS, VEC > 1 ? 3
       out = reinterpret_cast<T*>(p.pages) + row * p.d;
     }
   }
-  for (; h < h1; h += S::BATCH) {
-    in += S::BATCH * in_hs;
-    load_batch(in, h1 - h - S::BATCH, nxt);
 #pragma unroll
-    for (int u = 0; u < S::BATCH; ++u) {
+  for (int g = 0; g < S::GROUPS; ++g) {
+    if (h + g * S::STEP >= h1) break;
+    if constexpr (VEC > 1) cp_async_left(S::GROUPS - 1 - g);
+#pragma unroll
+    for (int i = 0; i < S::STEP; ++i) {
+      const int u = g * S::STEP + i;
       if (h + u < h1) {
+        alignas(16) T xa[VEC];
+        alignas(16) T xb[VEC];
+        if constexpr (VEC > 1) {
+          *reinterpret_cast<int4*>(xa) = s_in[(u * S::ACCESSES) * ROT_THREADS + tid];
+          if (two) *reinterpret_cast<int4*>(xb) = s_in[(u * S::ACCESSES + 1) * ROT_THREADS + tid];
+        } else {
+          xa[0] = in[u * in_hs + ia];
+          if (two) xb[0] = in[u * in_hs + ib];
+        }
         float ya[VEC], yb[VEC];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) ya[e] = Elem<T>::up(cur[u].a[e]);
+        for (int e = 0; e < VEC; ++e) ya[e] = Elem<T>::up(xa[e]);
         if constexpr (S::PAIRS) {
           if (turn) {
 #pragma unroll
@@ -331,7 +349,7 @@ __global__ void __launch_bounds__(Shape<T, VEC, INTER>::MAX_THREADS, VEC > 1 ? 3
         } else if (two) {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            yb[e] = Elem<T>::up(cur[u].b[e]);
+            yb[e] = Elem<T>::up(xb[e]);
             if (turn) turn_pair(ya[e], yb[e], cs[e], sn[e]);
           }
         }
@@ -350,9 +368,6 @@ __global__ void __launch_bounds__(Shape<T, VEC, INTER>::MAX_THREADS, VEC > 1 ? 3
         }
       }
     }
-    if (E4M3 && out8) out8 += S::BATCH * out_hs; else out += S::BATCH * out_hs;
-#pragma unroll
-    for (int u = 0; u < S::BATCH; ++u) cur[u] = nxt[u];
   }
 }
 
@@ -365,13 +380,15 @@ cudaError_t go(RotateParams p, cudaStream_t st) {
   p.groups = threads / p.items;
   if (p.n_views == 0) p.v[0].heads = p.v[0].chunks = p.v[0].chunk_heads = 1;   // no tokens: next_lengths only
   long long cta = 0;
+  int heads = 1;
   for (int v = 0; v < 3; ++v) {
     p.first_cta[v] = v < p.n_views ? (unsigned)cta : v ? 0xffffffffu : 0u;
     if (v >= p.n_views) continue;
-    // a thread's heads: all of the view's (ROT_HEADS at most), fewer while the call has not four CTAs for each SM
+    // a thread's heads: as many as it has places for, fewer while the call has not four CTAs for each SM
     const long long rows = (long long)p.n_tok * p.v[v].heads;
     const long long wide = (rows * p.items + 4 * 152 * ROT_THREADS - 1) / (4 * 152 * ROT_THREADS);
-    p.v[v].chunk_heads = (int)std::min<long long>(std::min(ROT_HEADS, p.v[v].heads), std::max<long long>(1, wide));
+    p.v[v].chunk_heads = (int)std::min<long long>(std::min(S::HEADS, p.v[v].heads), std::max<long long>(1, wide));
+    heads = std::max(heads, p.v[v].chunk_heads);
     p.v[v].chunks = (p.v[v].heads + p.v[v].chunk_heads - 1) / p.v[v].chunk_heads;
     const long long units = (long long)p.n_tok * p.v[v].chunks;
     if (units > 0xf0000000LL) return cudaErrorInvalidConfiguration;   // counted with 32 bits
@@ -379,7 +396,9 @@ cudaError_t go(RotateParams p, cudaStream_t st) {
   }
   if (cta > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const auto kern = rotate_kernel<T, VEC, INTER, APPEND, E4M3>;
-  return launch_pdl(kern, dim3((unsigned)std::max(1LL, cta)), dim3(threads), 0, st, p);
+  const size_t smem = VEC > 1 ? (size_t)heads * S::ACCESSES * ROT_THREADS * 16 : 0;
+  static_assert(ROT_AHEAD * ROT_THREADS <= 48 * 1024, "within what needs no allowance");
+  return launch_pdl(kern, dim3((unsigned)std::max(1LL, cta)), dim3(threads), smem, st, p);
 }
 
 template <typename T, int W, bool APPEND, bool E4M3>
