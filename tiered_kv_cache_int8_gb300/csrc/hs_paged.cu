@@ -1,6 +1,8 @@
 // Host side of the rotary and paged-cache entry points declared in include/hs.h:
 // frequency tables, argument checks and launches.
+#include <algorithm>
 #include <cmath>
+#include <cstdio>
 #include <new>
 #include <string>
 
@@ -265,10 +267,11 @@ int hs_paged_create(const hs_paged_config_t* cfg, void* pages, const float* kv_s
   h->scale_log2 = scale * 1.4426950408889634f;
   h->dev_error = error_word;
   // a handle is host memory only: without a device the calls' checks still run
-  if (cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, cfg->device) != cudaSuccess) {
+  if (cudaDeviceGetAttribute(&h->ctas, cudaDevAttrMultiProcessorCount, cfg->device) != cudaSuccess) {
     (void)cudaGetLastError();
-    h->num_sms = 0;
+    h->ctas = 0;
   } else {
+    h->ctas = std::min(h->ctas, hs::PG_MAX_CTAS);
     h->maps.reset(new (std::nothrow) CUtensorMap[cfg->n_layers]);
     if (!h->maps || !hs::paged_maps(h, layer_bytes(*cfg))) {
       const bool oom = !h->maps;
@@ -362,7 +365,7 @@ int hs_paged_append(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
 }
 
 int64_t hs_paged_workspace_bytes(const hs_paged_t* h) {
-  return h ? hs::paged_workspace_bytes(h->cfg.d, h->cfg.h_q / h->cfg.h_kv, h->cfg.page_type, h->num_sms) : 0;
+  return h ? hs::paged_workspace_bytes(h->cfg.d, h->cfg.h_q / h->cfg.h_kv, h->cfg.page_type, h->ctas) : 0;
 }
 
 int hs_paged_decode(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* req_ids, const int32_t* page_table,
@@ -410,12 +413,12 @@ int hs_paged_decode(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
   p.window = c.window;
   p.type = c.type;
   p.page_type = c.page_type;
-  p.grid = h->num_sms;
+  p.grid = h->ctas;
   p.device = c.device;
   p.scale_log2 = h->scale_log2;
   DeviceScope dev(c.device);
   if (dev.err != cudaSuccess) return fail_cuda(dev.err, "hs_paged_decode: device");
-  if (h->num_sms < 1) return named(HS_ERR_CUDA, me, "the handle was created without its device");
+  if (h->ctas < 1) return named(HS_ERR_CUDA, me, "the handle was created without its device");
   const cudaError_t e = hs::launch_paged_decode(p, h->maps[layer], static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? HS_OK : fail_cuda(e, "hs_paged_decode: launch");
 }

@@ -18,7 +18,7 @@ struct hs_paged {
   const float* kv_scale = nullptr;
   unsigned int* dev_error = nullptr;
   std::unique_ptr<CUtensorMap[]> maps;   // of each layer's pool; null without a device
-  int num_sms = 0;
+  int ctas = 0;                          // of the attention kernel; 0 without a device
   int page_shift = 0;
   float scale_log2 = 0.f;
 };
@@ -27,6 +27,7 @@ namespace hs {
 
 constexpr int PG_MAX_REQUESTS = 4096;
 constexpr int PG_MAX_POSITIONS = 1 << 22;
+constexpr int PG_MAX_CTAS = 160;   // of the attention kernel: one per SM; its join holds five pieces a lane
 
 inline size_t type_bytes(int t) { return t == HS_FP32 ? 4 : t == HS_E4M3 ? 1 : 2; }
 
@@ -88,7 +89,7 @@ cudaError_t launch_rotate(const RotateParams& p, int type, int page_type, bool a
                           bool wide, cudaStream_t st);
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st);
 bool paged_maps(::hs_paged* h, size_t layer_bytes);   // false: no tensor maps could be made
-int64_t paged_workspace_bytes(int d, int group, int page_type, int num_sms);
+int64_t paged_workspace_bytes(int d, int group, int page_type, int ctas);
 
 }  // namespace hs
 

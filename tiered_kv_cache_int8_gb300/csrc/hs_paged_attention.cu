@@ -49,18 +49,18 @@ bool pool_map(const hs_paged_config_t& p, void* pages, CUtensorMap* map) {
 
 }  // namespace
 
-int64_t paged_workspace_bytes(int d, int group, int page_type, int num_sms) {
+int64_t paged_workspace_bytes(int d, int group, int page_type, int ctas) {
   const bool e = page_type == HS_E4M3, two = group > 8;
   size_t n;
   if (d == 64)
-    n = e ? (two ? pa::ws_bytes<64, 2, true>(num_sms) : pa::ws_bytes<64, 1, true>(num_sms))
-          : (two ? pa::ws_bytes<64, 2, false>(num_sms) : pa::ws_bytes<64, 1, false>(num_sms));
+    n = e ? (two ? pa::ws_bytes<64, 2, true>(ctas) : pa::ws_bytes<64, 1, true>(ctas))
+          : (two ? pa::ws_bytes<64, 2, false>(ctas) : pa::ws_bytes<64, 1, false>(ctas));
   else if (d == 128)
-    n = e ? (two ? pa::ws_bytes<128, 2, true>(num_sms) : pa::ws_bytes<128, 1, true>(num_sms))
-          : (two ? pa::ws_bytes<128, 2, false>(num_sms) : pa::ws_bytes<128, 1, false>(num_sms));
+    n = e ? (two ? pa::ws_bytes<128, 2, true>(ctas) : pa::ws_bytes<128, 1, true>(ctas))
+          : (two ? pa::ws_bytes<128, 2, false>(ctas) : pa::ws_bytes<128, 1, false>(ctas));
   else
-    n = e ? (two ? pa::ws_bytes<256, 2, true>(num_sms) : pa::ws_bytes<256, 1, true>(num_sms))
-          : (two ? pa::ws_bytes<256, 2, false>(num_sms) : pa::ws_bytes<256, 1, false>(num_sms));
+    n = e ? (two ? pa::ws_bytes<256, 2, true>(ctas) : pa::ws_bytes<256, 1, true>(ctas))
+          : (two ? pa::ws_bytes<256, 2, false>(ctas) : pa::ws_bytes<256, 1, false>(ctas));
   return (int64_t)((n + 255) / 256 * 256);
 }
 

@@ -183,6 +183,40 @@ __device__ __forceinline__ void store_out4(void* out, long long at, float4 v) {
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = w;
 }
 
+// a lane's VW elements of a row of 32 VW
+template <int VW>
+__device__ __forceinline__ void load_lane(const float* p, float (&x)[VW]) {
+  if constexpr (VW == 2) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    x[0] = v.x; x[1] = v.y;
+  } else {
+#pragma unroll
+    for (int e = 0; e < VW; e += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + e);
+      x[e] = v.x; x[e + 1] = v.y; x[e + 2] = v.z; x[e + 3] = v.w;
+    }
+  }
+}
+template <int VW>
+__device__ __forceinline__ void save_lane(float* p, const float (&x)[VW]) {
+  if constexpr (VW == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VW; e += 4) *reinterpret_cast<float4*>(p + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+  }
+}
+template <int QTYPE, int VW>
+__device__ __forceinline__ void store_lane(void* out, long long at, const float (&x)[VW]) {
+  uint32_t w[VW / 2];
+#pragma unroll
+  for (int e = 0; e < VW / 2; ++e) w[e] = pack2<QTYPE>(x[2 * e], x[2 * e + 1]);
+  uint16_t* dst = static_cast<uint16_t*>(out) + at;
+  if constexpr (VW == 2) *reinterpret_cast<uint32_t*>(dst) = w[0];
+  if constexpr (VW == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  if constexpr (VW == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // 1 / l of a finished row: 0 where nothing was attended, NaN where a score was one
 __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
@@ -218,21 +252,35 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
   griddep_wait();
   griddep_launch_dependents();
 
-  // ---- the sequence: units before each request, for one head
+  // ---- the sequence: units before each request, for one head.  Few requests: every
+  // warp by itself (they all write the same values), no barrier; many: the CTA together
   {
-    const int per = (p.n_req + C::THREADS - 1) / C::THREADS;
-    const int i0 = min(p.n_req, tid * per), i1 = min(p.n_req, i0 + per);
+    const bool few = p.n_req <= 4 * 32;
+    const int width = few ? 32 : C::THREADS, who = few ? lane : tid;
+    const int per = (p.n_req + width - 1) / width;
+    const int i0 = min(p.n_req, who * per), i1 = min(p.n_req, i0 + per);
     int sum = 0, a, b, c, r;
     unsigned err = 0;
     for (int i = i0; i < i1; ++i) sum += request_units(p, i, &a, &b, &c, &r, &err);
-    int at = block_exclusive_scan<C::THREADS>(sum, scan, nullptr);
+    int at;
+    if (few) {
+      at = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(FULL_MASK, at, o);
+        if (lane >= o) at += x;
+      }
+      at -= sum;
+    } else {
+      at = block_exclusive_scan<C::THREADS>(sum, scan, nullptr);
+    }
     for (int i = i0; i < i1; ++i) {
       pre[i] = at;
       at += request_units(p, i, &a, &b, &c, &r, &err);
     }
     if (i1 == p.n_req && i0 < i1) pre[p.n_req] = at;
-    if (err && blockIdx.x == 0) set_error(p.dev_error, err);
-    __syncthreads();
+    if (err && blockIdx.x == 0 && (!few || warp == 0)) set_error(p.dev_error, err);
+    if (few) __syncwarp(); else __syncthreads();
   }
   const int chunks = (p.group + C::HEADS - 1) / C::HEADS;
   const int hcn = p.h_kv * chunks;
@@ -240,28 +288,41 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
   // its first page ids, its output), so that many short segments weigh what they take.
   auto cost_before = [&](int r) { return ((long long)pre[r] + (long long)SEGMENT_COST * r) * hcn; };
   const long long total = cost_before(p.n_req);
-  long long share = (total + gridDim.x - 1) / gridDim.x;
+  // (64-bit divisions take a while: only for sequences that need them)
+  long long share = total < (1 << 30) ? ((int)total + (int)gridDim.x - 1) / (int)gridDim.x
+                                      : (total + gridDim.x - 1) / gridDim.x;
   if (share < C::WARPS) share = C::WARPS;
   const long long wshare = (share + C::WARPS - 1) / C::WARPS;
   const long long cta0 = blockIdx.x * share;
-  // units before a cost position, and the place of the next one
-  auto find = [&](long long x, Place* at) -> long long {
-    if (x >= total) return (long long)pre[p.n_req] * hcn;
-    int lo = 0, hi = p.n_req;       // cost_before(lo) <= x < cost_before(hi)
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (cost_before(mid) <= x) lo = mid; else hi = mid;
-    }
-    const int n = pre[lo + 1] - pre[lo], rem = (int)(x - cost_before(lo));
-    const int hc = rem / (n + SEGMENT_COST);
-    const int u = max(0, rem - hc * (n + SEGMENT_COST) - SEGMENT_COST);
-    if (at) *at = Place{lo, hc, u, n};
-    return (long long)pre[lo] * hcn + (long long)hc * n + u;
-  };
-  Place at = {0, 0, 0, 1};          // the unit to be consumed next
+  // units before a cost position, and the place of the next one: the share's begin by the
+  // even lanes, its end by the odd ones
   const long long x0 = min(total, cta0 + warp * wshare);
-  const long long w0 = find(x0, &at);
-  const long long w1 = find(min(min(total, cta0 + share), x0 + wshare), nullptr);
+  const long long x1 = min(min(total, cta0 + share), x0 + wshare);
+  Place at = {0, 0, 0, 1};          // the unit to be consumed next
+  long long w0, w1;
+  {
+    const long long x = lane & 1 ? x1 : x0;
+    long long units = (long long)pre[p.n_req] * hcn;
+    if (x < total) {
+      int lo = 0, hi = p.n_req;     // cost_before(lo) <= x < cost_before(hi)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cost_before(mid) <= x) lo = mid; else hi = mid;
+      }
+      const int n = pre[lo + 1] - pre[lo], rem = (int)(x - cost_before(lo));
+      const int hc = rem / (n + SEGMENT_COST);
+      const int u = max(0, rem - hc * (n + SEGMENT_COST) - SEGMENT_COST);
+      at = Place{lo, hc, u, n};
+      units = (long long)pre[lo] * hcn + (long long)hc * n + u;
+    }
+    __syncwarp();
+    w0 = __shfl_sync(FULL_MASK, units, 0);
+    w1 = __shfl_sync(FULL_MASK, units, 1);
+    at.ri = __shfl_sync(FULL_MASK, at.ri, 0);
+    at.hc = __shfl_sync(FULL_MASK, at.hc, 0);
+    at.u = __shfl_sync(FULL_MASK, at.u, 0);
+    at.n = __shfl_sync(FULL_MASK, at.n, 0);
+  }
 
   const unsigned char* ring = smem + C::SM_RING + (size_t)warp * C::STAGES * C::STAGE;
   const uint32_t ring_s = smem_addr(ring);
@@ -609,65 +670,85 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
   }
   __syncthreads();
 
-  // ---- pieces of the CTA, in sequence order: neighbours of one segment are joined
-  Chain chain = {0, 0, -1, 0};
-  for (int i = 0; i < 2 * C::WARPS;) {
-    const Meta a = meta[i];
-    if (!a.at) {
-      ++i;
-      continue;
-    }
-    const float* src[2 * C::WARPS];
-    int k = 0, to = a.to;
-    for (; i < 2 * C::WARPS; ++i) {
-      const Meta b = meta[i];
-      if (!b.at) continue;
-      if (b.ri != a.ri || b.hc != a.hc) break;
-      src[k++] = b.at;
-      to = b.to;
-    }
-    const bool whole = a.from == 0 && to == a.n;
-    const int kvh = a.hc / chunks, chunk = a.hc - kvh * chunks;
-    float* dst = p.ws + ws_cta(C::PIECE, blockIdx.x, a.from == 0);
-    for (int e = tid; e < C::HEADS * (D / 4); e += C::THREADS) {
-      const int h = e / (D / 4), d4 = e - h * (D / 4);
-      float mm = -INFINITY;
-      for (int j = 0; j < k; ++j) mm = fmaxf(mm, src[j][C::HEADS * C::PROW + h]);
-      const float base = mm == -INFINITY ? 0.f : mm;
-      float ll = 0.f;
-      float4 acc = {0.f, 0.f, 0.f, 0.f};
-      for (int j = 0; j < k; ++j) {
-        const float w = exp2f(src[j][C::HEADS * C::PROW + h] - base);
-        const float4 x = *reinterpret_cast<const float4*>(src[j] + h * C::PROW + d4 * 4);
-        ll += w * src[j][C::HEADS * C::PROW + C::HEADS + h];
-        acc.x += w * x.x;
-        acc.y += w * x.y;
-        acc.z += w * x.z;
-        acc.w += w * x.w;
+  // ---- pieces of the CTA, in sequence order: neighbours of one segment are joined, a
+  // warp per group of them and head.  Lane i knows piece i.
+  {
+    static_assert(2 * C::WARPS <= 32, "a piece per lane");
+    constexpr int VW = D / 32;                      // elements of a lane
+    const Meta a = lane < 2 * C::WARPS ? meta[lane] : Meta{};
+    const unsigned valid = __ballot_sync(FULL_MASK, a.at != nullptr);
+    const unsigned before = valid & ((1u << lane) - 1);
+    const int prev = before ? 31 - __clz(before) : 0;
+    const int prev_ri = __shfl_sync(FULL_MASK, a.ri, prev), prev_hc = __shfl_sync(FULL_MASK, a.hc, prev);
+    const bool lead = a.at && (!before || prev_ri != a.ri || prev_hc != a.hc);
+    unsigned leads = __ballot_sync(FULL_MASK, lead);
+    Chain chain = {0, 0, -1, 0};
+    for (int grp = 0; leads; ++grp) {
+      const int first_piece = __ffs(leads) - 1;
+      leads &= leads - 1;
+      const unsigned members = valid & ~((1u << first_piece) - 1) & (leads ? (1u << (__ffs(leads) - 1)) - 1 : ~0u);
+      const int last_piece = 31 - __clz(members);
+      const int from = __shfl_sync(FULL_MASK, a.from, first_piece), to = __shfl_sync(FULL_MASK, a.to, last_piece);
+      const int n = __shfl_sync(FULL_MASK, a.n, first_piece);
+      const int ri = __shfl_sync(FULL_MASK, a.ri, first_piece), hc = __shfl_sync(FULL_MASK, a.hc, first_piece);
+      const int kvh = hc / chunks, chunk = hc - kvh * chunks;
+      if (from == 0 && to < n) {                    // goes on in other CTAs: to the one with the segment's end
+        const long long end = cost_before(ri) + (long long)(hc + 1) * (n + SEGMENT_COST) - 1;
+        chain = Chain{ri, hc, (int)(end / share), 0};
       }
-      if (whole) {
+      // the next group's heads go to the warps behind this one's
+      for (int h = (unsigned)(warp - grp * min(C::HEADS, p.group)) % C::WARPS; h < C::HEADS; h += C::WARPS) {
         const int hg = chunk * C::HEADS + h;
-        if (hg < p.group) {
-          const long long row = (long long)a.ri * p.h_q + kvh * p.group + hg;
-          const float inv = inverse(ll) * (E4M3 ? p.kv_scale[p.h_kv + kvh] : 1.f);
-          store_out4<QTYPE>(p.out, row * D + d4 * 4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-          if (p.lse && d4 == 0) p.lse[row] = log_sum<BF16>(mm, ll);
+        if (hg >= p.group) continue;
+        const bool in = (members >> lane) & 1;
+        const float pm = in ? a.at[C::HEADS * C::PROW + h] : -INFINITY;
+        const float pl = in ? a.at[C::HEADS * C::PROW + C::HEADS + h] : 0.f;
+        float mm = pm;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(FULL_MASK, mm, o));
+        const float w = exp2f(pm - (mm == -INFINITY ? 0.f : mm));
+        float ll = in ? w * pl : 0.f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) ll += __shfl_xor_sync(FULL_MASK, ll, o);
+        float acc[VW] = {};
+        for (unsigned rest = members; rest;) {
+          float x[4][VW], wj[4];                    // four pieces' loads at a time
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j = rest ? __ffs(rest) - 1 : first_piece;
+            wj[k] = rest ? __shfl_sync(FULL_MASK, w, j) : 0.f;
+            const float* at_j = reinterpret_cast<const float*>(
+                __shfl_sync(FULL_MASK, reinterpret_cast<unsigned long long>(a.at), j));
+            const bool have = rest != 0;
+            rest &= rest - 1;
+#pragma unroll
+            for (int e = 0; e < VW; ++e) x[k][e] = 0.f;
+            if (have) load_lane<VW>(at_j + h * C::PROW + lane * VW, x[k]);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int e = 0; e < VW; ++e) acc[e] += wj[k] * x[k][e];
         }
-      } else {
-        *reinterpret_cast<float4*>(dst + h * C::PROW + d4 * 4) = acc;
-        if (d4 == 0) {
-          dst[C::HEADS * C::PROW + h] = mm;
-          dst[C::HEADS * C::PROW + C::HEADS + h] = ll;
+        if (from == 0 && to == n) {
+          const long long row = (long long)ri * p.h_q + kvh * p.group + hg;
+          const float inv = inverse(ll) * (E4M3 ? p.kv_scale[p.h_kv + kvh] : 1.f);
+#pragma unroll
+          for (int e = 0; e < VW; ++e) acc[e] *= inv;
+          store_lane<QTYPE, VW>(p.out, row * D + lane * VW, acc);
+          if (p.lse && lane == 0) p.lse[row] = log_sum<BF16>(mm, ll);
+        } else {
+          float* dst = p.ws + ws_cta(C::PIECE, blockIdx.x, from == 0);
+          save_lane<VW>(dst + h * C::PROW + lane * VW, acc);
+          if (lane == 0) {
+            dst[C::HEADS * C::PROW + h] = mm;
+            dst[C::HEADS * C::PROW + C::HEADS + h] = ll;
+          }
         }
       }
     }
-    if (a.from == 0 && to < a.n) {
-      const long long end = cost_before(a.ri) + (long long)(a.hc + 1) * (a.n + SEGMENT_COST);   // of the segment
-      chain = Chain{a.ri, a.hc, (int)((end - 1) / share), 0};
-    }
+    if (tid == 0) reinterpret_cast<Chain*>(p.ws + ws_chain(C::PIECE, gridDim.x, C::WARPS))[blockIdx.x] = chain;
   }
-  if (tid == 0)
-    reinterpret_cast<Chain*>(p.ws + ws_chain(C::PIECE, gridDim.x, C::WARPS))[blockIdx.x] = chain;
 
   // ---- requests without a position
   for (int i = blockIdx.x; i < p.n_req; i += gridDim.x) {
@@ -680,15 +761,17 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
 }
 
 // The chains: block (cta, head) joins the pieces of the segment that starts in `cta`
-// and goes on in cta + 1 .. last, for one head of the pass.  Groups of lanes take
-// every GROUPS-th piece and are added up in shared memory, in a fixed order.
+// and goes on in cta + 1 .. last, for one head of the pass.  Every warp works out all
+// pieces' weights (a lane per piece, five times over), then takes every eighth piece's
+// row; the warps' sums are added in a fixed order.
+constexpr int JOIN_WARPS = 8;
+
 template <int D, int NT, int QTYPE, bool E4M3>
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
+__global__ void __launch_bounds__(32 * JOIN_WARPS) paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
   using C = Cfg<D, NT, QTYPE, E4M3>;
   constexpr bool BF16 = QTYPE == HS_BF16 && !E4M3;
-  constexpr int LANES = D / 4, GROUPS = 256 / LANES;
-  __shared__ float s_m[GROUPS], s_l[GROUPS];
-  __shared__ float4 s_o[GROUPS][LANES];
+  constexpr int VW = D / 32, PER = PG_MAX_CTAS / 32;
+  __shared__ float s_o[JOIN_WARPS][D];
   griddep_wait();
   griddep_launch_dependents();
   const int cta = blockIdx.x, h = blockIdx.y;
@@ -697,48 +780,68 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
   const int chunks = (p.group + C::HEADS - 1) / C::HEADS;
   const int kvh = ch.hc / chunks, hg = (ch.hc - kvh * chunks) * C::HEADS + h;
   if (hg >= p.group) return;
-  const int grp = threadIdx.x / LANES, ln = threadIdx.x - grp * LANES;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = ch.last - cta + 1;
-  float mm = -INFINITY, ll = 0.f;
-  float4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int j = grp; j < n; j += GROUPS) {
-    const float* src = p.ws + ws_cta(C::PIECE, cta + j, j == 0);
-    const float m = src[C::HEADS * C::PROW + h], l = src[C::HEADS * C::PROW + C::HEADS + h];
-    const float4 x = *reinterpret_cast<const float4*>(src + h * C::PROW + ln * 4);
-    const float nm = fmaxf(mm, m), base = nm == -INFINITY ? 0.f : nm;
-    const float a = exp2f(mm - base), b = exp2f(m - base);
-    mm = nm;
-    ll = ll * a + l * b;
-    acc.x = acc.x * a + x.x * b;
-    acc.y = acc.y * a + x.y * b;
-    acc.z = acc.z * a + x.z * b;
-    acc.w = acc.w * a + x.w * b;
+  auto piece = [&](int j) { return p.ws + ws_cta(C::PIECE, cta + j, j == 0); };
+  float m[PER], l[PER], mm = -INFINITY, ll = 0.f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int j = i * 32 + lane;
+    m[i] = j < n ? piece(j)[C::HEADS * C::PROW + h] : -INFINITY;
+    l[i] = j < n ? piece(j)[C::HEADS * C::PROW + C::HEADS + h] : 0.f;
   }
-  s_o[grp][ln] = acc;
-  if (ln == 0) {
-    s_m[grp] = mm;
-    s_l[grp] = ll;
-  }
-  __syncthreads();
-  if (grp != 0) return;
-  mm = -INFINITY;
-  for (int j = 0; j < GROUPS; ++j) mm = fmaxf(mm, s_m[j]);
+  float acc[VW] = {};
+  float x[4][VW];
+  auto fetch = [&](int i) {                // pieces warp + 8 (4 i + k) = 32 i + (warp + 8 k)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int e = 0; e < VW; ++e) x[k][e] = 0.f;
+      const int j = 32 * i + warp + 8 * k;
+      if (j < n) load_lane<VW>(piece(j) + h * C::PROW + lane * VW, x[k]);
+    }
+  };
+  fetch(0);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) mm = fmaxf(mm, m[i]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(FULL_MASK, mm, o));
   const float base = mm == -INFINITY ? 0.f : mm;
-  ll = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j = 0; j < GROUPS; ++j) {
-    const float w = exp2f(s_m[j] - base);
-    const float4 x = s_o[j][ln];
-    ll += w * s_l[j];
-    acc.x += w * x.x;
-    acc.y += w * x.y;
-    acc.z += w * x.z;
-    acc.w += w * x.w;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    m[i] = exp2f(m[i] - base);
+    ll += m[i] * l[i];
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) ll += __shfl_xor_sync(FULL_MASK, ll, o);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (32 * i < n) {
+      if (i) fetch(i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float w = __shfl_sync(FULL_MASK, m[i], warp + 8 * k);
+#pragma unroll
+        for (int e = 0; e < VW; ++e) acc[e] += w * x[k][e];
+      }
+    }
+  }
+  save_lane<VW>(&s_o[warp][lane * VW], acc);
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int g = 1; g < JOIN_WARPS; ++g) {
+    float y[VW];
+    load_lane<VW>(&s_o[g][lane * VW], y);
+#pragma unroll
+    for (int e = 0; e < VW; ++e) acc[e] += y[e];
   }
   const long long row = (long long)ch.ri * p.h_q + kvh * p.group + hg;
   const float inv = inverse(ll) * (E4M3 ? p.kv_scale[p.h_kv + kvh] : 1.f);
-  store_out4<QTYPE>(p.out, row * D + ln * 4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-  if (p.lse && ln == 0) p.lse[row] = log_sum<BF16>(mm, ll);
+#pragma unroll
+  for (int e = 0; e < VW; ++e) acc[e] *= inv;
+  store_lane<QTYPE, VW>(p.out, row * D + lane * VW, acc);
+  if (p.lse && lane == 0) p.lse[row] = log_sum<BF16>(mm, ll);
 }
 
 template <int D, int NT, int QTYPE, bool E4M3>
@@ -756,7 +859,7 @@ cudaError_t go(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t 
   }
   e = launch_pdl(paged_decode_kernel<D, NT, QTYPE, E4M3>, dim3(p.grid), dim3(C::THREADS), smem, st, p, map);
   if (e != cudaSuccess) return e;
-  return launch_pdl(paged_join_kernel<D, NT, QTYPE, E4M3>, dim3(p.grid, C::HEADS), dim3(256), 0, st, p);
+  return launch_pdl(paged_join_kernel<D, NT, QTYPE, E4M3>, dim3(p.grid, C::HEADS), dim3(32 * JOIN_WARPS), 0, st, p);
 }
 
 template <int D, int NT>
