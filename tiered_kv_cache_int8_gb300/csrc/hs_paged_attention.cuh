@@ -256,31 +256,48 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
   // warp by itself (they all write the same values), no barrier; many: the CTA together
   {
     const bool few = p.n_req <= 4 * 32;
-    const int width = few ? 32 : C::THREADS, who = few ? lane : tid;
-    const int per = (p.n_req + width - 1) / width;
-    const int i0 = min(p.n_req, who * per), i1 = min(p.n_req, i0 + per);
-    int sum = 0, a, b, c, r;
+    int a, b, c, r;
     unsigned err = 0;
-    for (int i = i0; i < i1; ++i) sum += request_units(p, i, &a, &b, &c, &r, &err);
-    int at;
     if (few) {
-      at = sum;
+      const int per = (p.n_req + 31) / 32;
+      int n[4], sum = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = lane * per + k;
+        n[k] = k < per && i < p.n_req ? request_units(p, i, &a, &b, &c, &r, &err) : 0;
+        sum += n[k];
+      }
+      int at = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(FULL_MASK, at, o);
         if (lane >= o) at += x;
       }
+      if (lane == 31) pre[p.n_req] = at;
       at -= sum;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = lane * per + k;
+        if (k < per && i < p.n_req) pre[i] = at;
+        at += n[k];
+      }
+      if (err && blockIdx.x == 0 && warp == 0) set_error(p.dev_error, err);
+      __syncwarp();
     } else {
-      at = block_exclusive_scan<C::THREADS>(sum, scan, nullptr);
+      const int per = (p.n_req + C::THREADS - 1) / C::THREADS;
+      const int i0 = min(p.n_req, tid * per), i1 = min(p.n_req, i0 + per);
+      int sum = 0;
+      for (int i = i0; i < i1; ++i) sum += request_units(p, i, &a, &b, &c, &r, &err);
+      int all;
+      int at = block_exclusive_scan<C::THREADS>(sum, scan, &all);
+      for (int i = i0; i < i1; ++i) {
+        pre[i] = at;
+        at += request_units(p, i, &a, &b, &c, &r, &err);
+      }
+      if (tid == 0) pre[p.n_req] = all;
+      if (err && blockIdx.x == 0) set_error(p.dev_error, err);
+      __syncthreads();
     }
-    for (int i = i0; i < i1; ++i) {
-      pre[i] = at;
-      at += request_units(p, i, &a, &b, &c, &r, &err);
-    }
-    if (i1 == p.n_req && i0 < i1) pre[p.n_req] = at;
-    if (err && blockIdx.x == 0 && (!few || warp == 0)) set_error(p.dev_error, err);
-    if (few) __syncwarp(); else __syncthreads();
   }
   const int chunks = (p.group + C::HEADS - 1) / C::HEADS;
   const int hcn = p.h_kv * chunks;
@@ -543,7 +560,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
               }
             }
         }
-        uint32_t pf[NT][2];
+        // Weights for bf16 products go as two bf16, a rounded value and what it leaves: one alone
+        // would put 2^-9 on every weight, as much again as the output's own rounding.  (The tensor
+        // pipe has the time.)  fp16 weights are within 2^-12 as they are.
+        constexpr int PARTS = BF16 ? 2 : 1;
+        uint32_t pf[NT][PARTS][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float w[4];
@@ -554,8 +575,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
             w[e + 2] = weight<BF16>(s[nt][e + 2] - base);
             l[nt][e] += w[e] + w[e + 2];
           }
-          pf[nt][0] = transpose8(pack2<BF16 ? HS_BF16 : HS_FP16>(w[0], w[1]));
-          pf[nt][1] = transpose8(pack2<BF16 ? HS_BF16 : HS_FP16>(w[2], w[3]));
+          const uint32_t x = pack2<BF16 ? HS_BF16 : HS_FP16>(w[0], w[1]), y = pack2<BF16 ? HS_BF16 : HS_FP16>(w[2], w[3]);
+          pf[nt][0][0] = transpose8(x);
+          pf[nt][0][1] = transpose8(y);
+          if constexpr (BF16) {
+            pf[nt][1][0] = transpose8(pack2<HS_BF16>(w[0] - bf16lo(x), w[1] - bf16hi(x)));
+            pf[nt][1][1] = transpose8(pack2<HS_BF16>(w[2] - bf16lo(y), w[3] - bf16hi(y)));
+          }
         }
         // ---- O^T += V^T P^T.  Rows that are not attended may hold anything: their values become 0
         uint32_t keep01 = 0xffffffffu, keep23 = 0xffffffffu;
@@ -578,7 +604,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
               const uint32_t a[4] = {e4m3x2_to_half2(__byte_perm(x, 0, 0x4420)), e4m3x2_to_half2(__byte_perm(x, 0, 0x4431)),
                                      e4m3x2_to_half2(__byte_perm(y, 0, 0x4420)), e4m3x2_to_half2(__byte_perm(y, 0, 0x4431))};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[nt][2 * i + c], a, pf[nt][0], pf[nt][1]);
+              for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[nt][2 * i + c], a, pf[nt][0][0], pf[nt][0][1]);
             }
           }
         } else {
@@ -591,7 +617,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
             a[2] &= keep23;
             a[3] &= keep23;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<BF16>(o[nt][c], a, pf[nt][0], pf[nt][1]);
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int part = 0; part < PARTS; ++part) mma16816<BF16>(o[nt][c], a, pf[nt][part][0], pf[nt][part][1]);
           }
         }
         __syncwarp();                               // every lane has read the stage
@@ -694,41 +722,50 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
       const int kvh = hc / chunks, chunk = hc - kvh * chunks;
       if (from == 0 && to < n) {                    // goes on in other CTAs: to the one with the segment's end
         const long long end = cost_before(ri) + (long long)(hc + 1) * (n + SEGMENT_COST) - 1;
-        chain = Chain{ri, hc, (int)(end / share), 0};
+        chain = Chain{ri, hc, total < (1 << 30) ? (int)end / (int)share : (int)(end / share), 0};
       }
       // the next group's heads go to the warps behind this one's
       for (int h = (unsigned)(warp - grp * min(C::HEADS, p.group)) % C::WARPS; h < C::HEADS; h += C::WARPS) {
         const int hg = chunk * C::HEADS + h;
         if (hg >= p.group) continue;
+        // the first four pieces' rows are on their way before the weights are known
+        float x[4][VW];
+        int j[4];
+        unsigned rest = members;
+        auto fetch = [&] {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            j[k] = rest ? __ffs(rest) - 1 : -1;
+            const float* at_j = reinterpret_cast<const float*>(
+                __shfl_sync(FULL_MASK, reinterpret_cast<unsigned long long>(a.at), j[k] & 31));
+            rest &= rest - 1;
+#pragma unroll
+            for (int e = 0; e < VW; ++e) x[k][e] = 0.f;
+            if (j[k] >= 0) load_lane<VW>(at_j + h * C::PROW + lane * VW, x[k]);
+          }
+        };
+        fetch();
         const bool in = (members >> lane) & 1;
         const float pm = in ? a.at[C::HEADS * C::PROW + h] : -INFINITY;
         const float pl = in ? a.at[C::HEADS * C::PROW + C::HEADS + h] : 0.f;
         float mm = pm;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(FULL_MASK, mm, o));
+        for (int o = C::WARPS; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(FULL_MASK, mm, o));
+        mm = __shfl_sync(FULL_MASK, mm, 0);
         const float w = exp2f(pm - (mm == -INFINITY ? 0.f : mm));
-        float ll = in ? w * pl : 0.f;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) ll += __shfl_xor_sync(FULL_MASK, ll, o);
-        float acc[VW] = {};
-        for (unsigned rest = members; rest;) {
-          float x[4][VW], wj[4];                    // four pieces' loads at a time
+        float ll = 0.f, acc[VW] = {};
+        while (true) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int j = rest ? __ffs(rest) - 1 : first_piece;
-            wj[k] = rest ? __shfl_sync(FULL_MASK, w, j) : 0.f;
-            const float* at_j = reinterpret_cast<const float*>(
-                __shfl_sync(FULL_MASK, reinterpret_cast<unsigned long long>(a.at), j));
-            const bool have = rest != 0;
-            rest &= rest - 1;
+            const float wj = __shfl_sync(FULL_MASK, w, j[k] & 31), lj = __shfl_sync(FULL_MASK, pl, j[k] & 31);
+            if (j[k] >= 0) {
+              ll += wj * lj;
 #pragma unroll
-            for (int e = 0; e < VW; ++e) x[k][e] = 0.f;
-            if (have) load_lane<VW>(at_j + h * C::PROW + lane * VW, x[k]);
+              for (int e = 0; e < VW; ++e) acc[e] += wj * x[k][e];
+            }
           }
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int e = 0; e < VW; ++e) acc[e] += wj[k] * x[k][e];
+          if (!rest) break;
+          fetch();
         }
         if (from == 0 && to == n) {
           const long long row = (long long)ri * p.h_q + kvh * p.group + hg;

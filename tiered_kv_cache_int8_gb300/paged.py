@@ -64,7 +64,6 @@ def _ints(name: str, x, device, n: int):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-
 def _on_stream(call, stream, device, tensors):
     """call(handle) on a given stream: what it allocates belongs to that stream, and the
     given tensors are marked as used there."""
