@@ -476,7 +476,7 @@ typedef struct hs_rotary {
  *   n_tok    : tokens (0: a no-op);  positions: dev int32 [n_tok]
  *   in, out  : n_views (1 or 2) views each; out[i] is in[i] itself (same data and
  *              strides: in place) or memory apart from it.  Output elements must be
- *              distinct.  Any alignment of the element type; 16-byte aligned views
+ *              distinct, and none of them an element of the other view's input.  Any alignment of the element type; 16-byte aligned views
  *              and strides take the faster loads
  *   device   : CUDA device of the buffers (the current device is left as it was)
  */
@@ -540,7 +540,8 @@ void hs_paged_destroy(hs_paged_t* h);
  *   rot         : rotation of k (and q) at the token's position, or NULL for none
  *                 (its transpose field must be 0)
  *   q, q_out    : views of the step's queries and of their rotated values, or both
- *                 NULL; in place or apart as for hs_rotary_apply; needs rot
+ *                 NULL; in place or apart as for hs_rotary_apply (no element of q_out
+ *                 one of k or v); needs rot
  *   k, v        : views of the new keys and values (h_kv heads)
  * The row of token j of request r takes position lengths[r] + j.  `lengths` itself is
  * not changed, so every layer of a step is given the same one, and a call that is
@@ -559,9 +560,12 @@ int hs_paged_append(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
  * hs_paged_decode — attention of one token per request over its cached positions
  * (stream-ordered, capturable): with N = lengths[r] and the last min(N, window) positions,
  *   o_h = sum_n softmax_n(softmax_scale * q_h . K_n) V_n,   kv head floor(h * h_kv / h_q).
+ *   req_ids  : dev int32 [n_req] request ids (the same one may come twice), or NULL for
+ *              0 .. n_req-1
  *   lengths  : dev int32 [max_requests], the new token's own position counted
  *   q        : view of [n_req][h_q][d], 16-byte aligned rows
- *   out      : dev [n_req][h_q][d] (type), 16-byte aligned
+ *   out      : dev [n_req][h_q][d] (type), 16-byte aligned; q's own memory in the same
+ *              order, or apart from it
  *   lse      : dev float [n_req][h_q] or NULL: ln sum_n exp(softmax_scale * q_h . K_n)
  *   workspace: dev, hs_paged_workspace_bytes(h) bytes, 256-byte aligned; its contents
  *              matter only within the call: calls that may overlap need one each

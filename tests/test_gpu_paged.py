@@ -676,6 +676,96 @@ def test_cache_refuses_what_the_binding_sees():
         PagedKVCache(**base, rotary=Rotary(128)).append(0, k[:1, :, :64].contiguous(), v[:1, :, :64].contiguous())
 
 
+def test_a_first_call_may_be_captured():
+    # a process whose first calls of every kernel are inside a capture
+    import subprocess
+    import sys
+    from tests.conftest import ROOT
+    code = """
+import torch
+from tiered_kv_cache_int8_gb300 import PagedKVCache, Rotary
+rot = Rotary(64)
+c = PagedKVCache(n_layers=1, n_pages=8, page_size=16, max_requests=2, max_pages=4, h_q=4, h_kv=2, d=64, rotary=rot)
+c.reserve(0, 20); c.reserve(1, 1)
+k = torch.randn(2, 2, 64, device="cuda").bfloat16(); q = torch.randn(2, 4, 64, device="cuda").bfloat16()
+pos = torch.zeros(2, dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    x = rot.apply(pos, q)
+    qr = c.append(0, k, k, q=q)
+    o = c.decode(0, qr)
+g.replay(); torch.cuda.synchronize()
+assert torch.equal(x, q) and torch.equal(qr, q) and c.device_error() == 0
+assert torch.equal(o, k.repeat_interleave(2, dim=1))
+print("fine")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+def test_decode_of_the_most_requests():
+    torch = T()
+    R, d, page = 4096, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(2)
+    from tiered_kv_cache_int8_gb300 import PagedKVCache
+    c = PagedKVCache(n_layers=1, n_pages=R, page_size=page, max_requests=R, max_pages=1, h_q=3, h_kv=1, d=d)
+    c.pages.copy_(filled(c.pages.shape, torch.bfloat16, g, False))
+    c.page_table[:, 0] = torch.randperm(R, generator=g, device="cuda").to(torch.int32)
+    lengths = torch.randint(0, page + 1, (R,), generator=g, device="cuda", dtype=torch.int32)
+    c.set_lengths(lengths)
+    q = torch.randn(R, 3, d, generator=g, device="cuda").bfloat16()
+    out, lse = c.decode(0, q, return_lse=True)
+    kv = c.pages[0][c.page_table[:, 0].long(), :, 0].double()               # [R, 2, page, d]
+    seen = torch.arange(page, device="cuda")[None] < lengths[:, None]
+    s = torch.einsum("rhd,rnd->rhn", q.double(), kv[:, 0]) / math.sqrt(d)
+    s = torch.where(seen[:, None], s, -math.inf)
+    p = torch.nan_to_num(torch.softmax(s, -1))
+    want = torch.einsum("rhn,rnd->rhd", p, kv[:, 1])
+    size = torch.einsum("rhn,rnd->rhd", p, kv[:, 1].abs())
+    # scores of 64 products each, at most 16 of them; weights and output rounded as in paged_plain.attend
+    dots = torch.einsum("rhd,rnd->rhn", q.double().abs(), kv[:, 0].abs()).amax(-1, keepdim=True) / math.sqrt(d)
+    tol = size * (2.0 ** -8 + 2 * (d + 8) * 2.0 ** -23 * dots + 2.0 ** -16) + 2.0 ** -20 * want.abs()
+    within(out, want, tol + 2.0 ** -8 * (want.abs() + tol) + plain.TINY[q.dtype], "out")
+    some = lengths > 0
+    within(lse[some], torch.logsumexp(s[some], -1), ((d + 8) * 2.0 ** -23 * dots[some, :, 0] + 2.0 ** -16), "lse")
+    assert (lse[~some] == -math.inf).all() and (~some).any() and c.device_error() == 0
+
+
+def test_decode_in_place_and_repeated_ids():
+    torch = T()
+    from tiered_kv_cache_int8_gb300 import HsError
+    lengths = [3000, 17, 0, 400]
+    c, g = make(4, 40, 2, 128, 32, "bf16", "bf16", lengths)
+    q = torch.randn(6, 40, 128, generator=g, device="cuda").bfloat16()
+    ids = [0, 3, 0, 1, 2, 0]
+    i32 = torch.tensor(ids[:4], dtype=torch.int32, device="cuda")
+    out, lse = check_decode(c, q[:4].contiguous(), lengths, ids=ids[:4])
+    x = q[:4].clone()
+    assert c.decode(0, x, req_ids=i32, out=x) is x and torch.equal(x, out)
+    with pytest.raises(HsError):
+        c.decode(0, q[:4], req_ids=i32, out=q[1:5])
+    # a single request's query with any stride
+    wide = torch.randn(1, 41 * 128 + 3, generator=g, device="cuda").bfloat16()
+    check_decode(c, wide[:, :40 * 128].view(1, 40, 128), lengths, ids=[3])
+
+
+@pytest.mark.parametrize("offsets", [False, True])
+def test_append_of_no_tokens(offsets):
+    torch = T()
+    from tiered_kv_cache_int8_gb300 import Rotary
+    c, g = make(3, 2, 1, 64, 16, "bf16", "e4m3", [3, 0, 20], rotary=Rotary(64))
+    c.next_lengths.fill_(-7)
+    before = c.pages.view(torch.uint8).clone()
+    none = torch.zeros(0, 1, 64, dtype=torch.bfloat16, device="cuda")
+    nq = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    kw = dict(tok_offsets=torch.zeros(4, dtype=torch.int32, device="cuda")) if offsets else dict(
+        req_ids=torch.arange(3, dtype=torch.int32, device="cuda"))
+    assert c.append(0, none, none, q=nq, **kw).shape == (0, 2, 64)
+    assert c.next_lengths.tolist() == [3, 0, 20] and torch.equal(c.pages.view(torch.uint8), before)
+    assert c.device_error() == 0
+
+
 def test_the_two_tier_cache_takes_rotated_rows():
     # the rotation feeds the two-tier cache: rows and queries rotated by it give the attention of rotated rows
     torch = T()

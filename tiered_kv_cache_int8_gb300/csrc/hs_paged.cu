@@ -70,8 +70,9 @@ bool apart(const hs_heads_t& a, const hs_heads_t& b, int n_tok, int d, size_t es
   return a0 + (size_t)extent(a, n_tok, d) * es <= b0 || b0 + (size_t)extent(b, n_tok, d) * es <= a0;
 }
 
-bool wide_view(const hs_heads_t& v, size_t es) {
-  return reinterpret_cast<uintptr_t>(v.data) % 16 == 0 && (v.token_stride * es) % 16 == 0 &&
+// whether every row of a view is 16-byte aligned (the stride of a single token or head says nothing)
+bool wide_view(const hs_heads_t& v, int n_tok, size_t es) {
+  return reinterpret_cast<uintptr_t>(v.data) % 16 == 0 && (n_tok == 1 || (v.token_stride * es) % 16 == 0) &&
          (v.heads == 1 || (v.head_stride * es) % 16 == 0);
 }
 
@@ -226,7 +227,7 @@ int hs_rotary_apply(const hs_rotary_t* rot, int32_t type, int32_t d, int32_t n_t
   bool wide = wide_rotary(rot, d, es);
   for (int i = 0; i < n_views; ++i) {
     if (const char* why = check_pair(in[i], out[i], n_tok, d, es); *why) return named(HS_ERR_INVALID, me, why);
-    wide = wide && wide_view(in[i], es) && wide_view(out[i], es);
+    wide = wide && wide_view(in[i], n_tok, es) && wide_view(out[i], n_tok, es);
     p.v[i] = row_view(in[i], &out[i], hs::VIEW_ROTATE);
   }
   p.n_views = n_views;
@@ -273,11 +274,22 @@ int hs_paged_create(const hs_paged_config_t* cfg, void* pages, const float* kv_s
   } else {
     h->ctas = std::min(h->ctas, hs::PG_MAX_CTAS);
     h->maps.reset(new (std::nothrow) CUtensorMap[cfg->n_layers]);
-    if (!h->maps || !hs::paged_maps(h, layer_bytes(*cfg))) {
-      const bool oom = !h->maps;
+    if (!h->maps) {
       delete h;
-      return oom ? named(HS_ERR_OOM, me, "out of host memory")
-                 : named(HS_ERR_CUDA, me, "the driver made no tensor map of the pool");
+      return named(HS_ERR_OOM, me, "out of host memory");
+    }
+    if (!hs::paged_maps(h, layer_bytes(*cfg))) {
+      delete h;
+      return named(HS_ERR_CUDA, me, "the driver made no tensor map of the pool");
+    }
+    // the kernels are loaded here, so that a first call may be a captured one
+    DeviceScope dev(cfg->device);
+    cudaError_t e = dev.err;
+    if (e == cudaSuccess) e = hs::prepare_paged(cfg->d, cfg->h_q / cfg->h_kv, cfg->type, cfg->page_type);
+    if (e == cudaSuccess) e = hs::prepare_rotate(cfg->type, cfg->page_type, true);
+    if (e != cudaSuccess) {
+      delete h;
+      return fail_cuda(e, "hs_paged_create: kernel set-up");
     }
   }
   *out = h;
@@ -325,10 +337,10 @@ int hs_paged_append(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
     if (q && q->heads != c.h_q) return named(HS_ERR_INVALID, me, "q must have h_q heads");
     int n = 0;
     if (q) {
-      wide = wide && wide_view(*q, es) && wide_view(*q_out, es);
+      wide = wide && wide_view(*q, n_tok, es) && wide_view(*q_out, n_tok, es);
       p.v[n++] = row_view(*q, q_out, hs::VIEW_ROTATE);
     }
-    wide = wide && wide_view(*k, es) && wide_view(*v, es);
+    wide = wide && wide_view(*k, n_tok, es) && wide_view(*v, n_tok, es);
     p.v[n++] = row_view(*k, nullptr, hs::VIEW_KEYS);
     p.v[n++] = row_view(*v, nullptr, hs::VIEW_VALUES);
     p.n_views = n;
@@ -386,7 +398,10 @@ int hs_paged_decode(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
   const size_t es = hs::type_bytes(c.type);
   if (const char* why = check_view(*q, n_req, c.d, es, false); *why) return named(HS_ERR_INVALID, me, why);
   if (q->heads != c.h_q) return named(HS_ERR_INVALID, me, "q must have h_q heads");
-  if (!wide_view(*q, es)) return named(HS_ERR_INVALID, me, "q's rows must be 16-byte aligned");
+  if (!wide_view(*q, n_req, es)) return named(HS_ERR_INVALID, me, "q's rows must be 16-byte aligned");
+  hs_heads_t o = {out, (int64_t)c.h_q * c.d, c.d, c.h_q, 0};
+  if (!same_view(*q, o, n_req) && !apart(*q, o, n_req, c.d, es))
+    return named(HS_ERR_INVALID, me, "out overlaps q without being the same memory in the same order");
   hs::PagedDecodeParams p = {};
   p.req_ids = req_ids;
   p.page_table = page_table;
@@ -414,7 +429,6 @@ int hs_paged_decode(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
   p.type = c.type;
   p.page_type = c.page_type;
   p.grid = h->ctas;
-  p.device = c.device;
   p.scale_log2 = h->scale_log2;
   DeviceScope dev(c.device);
   if (dev.err != cudaSuccess) return fail_cuda(dev.err, "hs_paged_decode: device");

@@ -7,6 +7,9 @@ namespace hs {
 cudaError_t paged_decode_d64(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st);
 cudaError_t paged_decode_d128(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st);
 cudaError_t paged_decode_d256(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st);
+cudaError_t prepare_paged_d64(int group, int type, int page_type);
+cudaError_t prepare_paged_d128(int group, int type, int page_type);
+cudaError_t prepare_paged_d256(int group, int type, int page_type);
 
 namespace {
 
@@ -68,6 +71,12 @@ bool paged_maps(hs_paged* h, size_t layer_bytes) {
   for (int l = 0; l < h->cfg.n_layers; ++l)
     if (!pool_map(h->cfg, static_cast<unsigned char*>(h->pages) + layer_bytes * l, &h->maps[l])) return false;
   return true;
+}
+
+cudaError_t prepare_paged(int d, int group, int type, int page_type) {
+  return d == 64    ? prepare_paged_d64(group, type, page_type)
+         : d == 128 ? prepare_paged_d128(group, type, page_type)
+                    : prepare_paged_d256(group, type, page_type);
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st) {

@@ -34,8 +34,6 @@
 #ifndef HS_PAGED_ATTENTION_CUH_
 #define HS_PAGED_ATTENTION_CUH_
 
-#include <atomic>
-
 #include "hs_paged.cuh"
 
 namespace hs {
@@ -882,35 +880,32 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_join_kernel(const __gri
 }
 
 template <int D, int NT, int QTYPE, bool E4M3>
-cudaError_t go(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st) {
+struct Kernels {
   using C = Cfg<D, NT, QTYPE, E4M3>;
-  const size_t smem = C::smem(p.n_req);
-  // the kernel's shared-memory allowance, once per device (a bit each; devices past 63 every time)
-  static std::atomic<uint64_t> allowed{0};
-  const uint64_t bit = p.device < 64 ? 1ull << p.device : 0;
-  cudaError_t e = cudaSuccess;
-  if (!(allowed.load(std::memory_order_acquire) & bit)) {
-    e = allow_smem(paged_decode_kernel<D, NT, QTYPE, E4M3>, C::smem(PG_MAX_REQUESTS));
-    if (e != cudaSuccess) return e;
-    allowed.fetch_or(bit, std::memory_order_release);
+  static cudaError_t prepare() {
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, paged_join_kernel<D, NT, QTYPE, E4M3>);
+    return e != cudaSuccess ? e : allow_smem(paged_decode_kernel<D, NT, QTYPE, E4M3>, C::smem(PG_MAX_REQUESTS));
   }
-  e = launch_pdl(paged_decode_kernel<D, NT, QTYPE, E4M3>, dim3(p.grid), dim3(C::THREADS), smem, st, p, map);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(paged_join_kernel<D, NT, QTYPE, E4M3>, dim3(p.grid, C::HEADS), dim3(32 * JOIN_WARPS), 0, st, p);
-}
+  static cudaError_t launch(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st) {
+    const cudaError_t e = launch_pdl(paged_decode_kernel<D, NT, QTYPE, E4M3>, dim3(p.grid), dim3(C::THREADS),
+                                     C::smem(p.n_req), st, p, map);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(paged_join_kernel<D, NT, QTYPE, E4M3>, dim3(p.grid, C::HEADS), dim3(32 * JOIN_WARPS), 0, st, p);
+  }
+};
 
-template <int D, int NT>
-cudaError_t by_type(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st) {
-  const bool e = p.page_type == HS_E4M3;
-  if (p.type == HS_BF16)
-    return e ? go<D, NT, HS_BF16, true>(p, map, st) : go<D, NT, HS_BF16, false>(p, map, st);
-  return e ? go<D, NT, HS_FP16, true>(p, map, st) : go<D, NT, HS_FP16, false>(p, map, st);
+// f(kernels) for a configuration.  Query heads of a pass: up to 8 or 16 of a kv head's; more
+// are taken in several passes over its rows.
+template <int D, int NT, typename F>
+cudaError_t by_type(int type, int page_type, F f) {
+  const bool e = page_type == HS_E4M3;
+  if (type == HS_BF16) return e ? f(Kernels<D, NT, HS_BF16, true>{}) : f(Kernels<D, NT, HS_BF16, false>{});
+  return e ? f(Kernels<D, NT, HS_FP16, true>{}) : f(Kernels<D, NT, HS_FP16, false>{});
 }
-
-// query heads of a pass: up to 8 or 16 of a kv head's; more are taken in several passes over its rows
-template <int D>
-cudaError_t by_group(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st) {
-  return p.group <= 8 ? by_type<D, 1>(p, map, st) : by_type<D, 2>(p, map, st);
+template <int D, typename F>
+cudaError_t by_group(int group, int type, int page_type, F f) {
+  return group <= 8 ? by_type<D, 1>(type, page_type, f) : by_type<D, 2>(type, page_type, f);
 }
 
 template <int D, int NT, bool E4M3>

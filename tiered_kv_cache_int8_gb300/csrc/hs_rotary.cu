@@ -188,8 +188,9 @@ __device__ Token locate(const RotateParams& p, int t, int near) {
 // of each pair of heads were exposed (20 K tokens of 48 heads into 8-bit pages: 103 us;
 // now 75 us, 6.2 TB/s).  A view's heads are split over several threads, fewer each
 // where there are few tokens.
-template <typename T, int VEC, bool INTER>
+template <typename T, int VEC_, bool INTER>
 struct Shape {
+  static constexpr int VEC = VEC_;
   static constexpr bool PAIRS = INTER && VEC > 1;              // both elements of a pair in one access
   static constexpr int PER_ITEM = PAIRS ? VEC / 2 : VEC;       // pairs of an item
   static constexpr int ACCESSES = PAIRS ? 1 : 2;
@@ -306,11 +307,13 @@ __global__ void __launch_bounds__(Shape<T, VEC, INTER>::MAX_THREADS, VEC > 1 ? 4
   unsigned char* out8 = nullptr;
   long long out_hs = view.out_hs;
   const float* scale = nullptr;
+  if (APPEND && (kind == VIEW_ROTATE ? !tok.ok : tok.page < 0)) {   // nothing to store
+    cp_async_wait_all();
+    return;
+  }
   if (kind == VIEW_ROTATE) {
-    if (!tok.ok) return;
     out = static_cast<T*>(view.out) + t * view.out_ts + h * out_hs;
   } else {
-    if (tok.page < 0) return;
     const int which = kind == VIEW_VALUES;
     const long long row = ((((long long)tok.page * 2 + which) * p.h_kv + h) << p.page_shift) + tok.slot;
     out_hs = (long long)p.d << p.page_shift;
@@ -371,9 +374,9 @@ __global__ void __launch_bounds__(Shape<T, VEC, INTER>::MAX_THREADS, VEC > 1 ? 4
   }
 }
 
-template <typename T, int VEC, bool INTER, bool APPEND, bool E4M3>
-cudaError_t go(RotateParams p, cudaStream_t st) {
-  using S = Shape<T, VEC, INTER>;
+template <typename S, typename K>
+cudaError_t go(K kern, RotateParams p, cudaStream_t st) {
+  constexpr int VEC = S::VEC;
   const int half = p.rot_dim / 2;
   p.items = S::PAIRS ? p.d / VEC : half / VEC + (p.d - p.rot_dim) / VEC;
   const int threads = p.items <= ROT_THREADS ? ROT_THREADS : (p.items + 31) / 32 * 32;
@@ -395,33 +398,52 @@ cudaError_t go(RotateParams p, cudaStream_t st) {
     cta += (units + p.groups - 1) / p.groups;
   }
   if (cta > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const auto kern = rotate_kernel<T, VEC, INTER, APPEND, E4M3>;
   const size_t smem = VEC > 1 ? (size_t)heads * S::ACCESSES * ROT_THREADS * 16 : 0;
   static_assert(ROT_AHEAD * ROT_THREADS <= 48 * 1024, "within what needs no allowance");
   return launch_pdl(kern, dim3((unsigned)std::max(1LL, cta)), dim3(threads), smem, st, p);
 }
 
-template <typename T, int W, bool APPEND, bool E4M3>
-cudaError_t pick(const RotateParams& p, bool interleaved, bool wide, cudaStream_t st) {
-  if (wide) return interleaved ? go<T, W, true, APPEND, E4M3>(p, st) : go<T, W, false, APPEND, E4M3>(p, st);
-  return interleaved ? go<T, 1, true, APPEND, E4M3>(p, st) : go<T, 1, false, APPEND, E4M3>(p, st);
+// f(kernel shape) for the variant that takes a call
+template <typename T, int W, bool APPEND, bool E4M3, typename F>
+cudaError_t pick(bool interleaved, bool wide, F f) {
+  if (wide)
+    return interleaved ? f(rotate_kernel<T, W, true, APPEND, E4M3>, Shape<T, W, true>{})
+                       : f(rotate_kernel<T, W, false, APPEND, E4M3>, Shape<T, W, false>{});
+  return interleaved ? f(rotate_kernel<T, 1, true, APPEND, E4M3>, Shape<T, 1, true>{})
+                     : f(rotate_kernel<T, 1, false, APPEND, E4M3>, Shape<T, 1, false>{});
+}
+
+template <typename F>
+cudaError_t by_type(int type, int page_type, bool append, bool interleaved, bool wide, F f) {
+  const bool e = page_type == HS_E4M3;
+  if (append) {
+    if (type == HS_BF16)
+      return e ? pick<__nv_bfloat16, 8, true, true>(interleaved, wide, f)
+               : pick<__nv_bfloat16, 8, true, false>(interleaved, wide, f);
+    return e ? pick<__half, 8, true, true>(interleaved, wide, f) : pick<__half, 8, true, false>(interleaved, wide, f);
+  }
+  if (type == HS_BF16) return pick<__nv_bfloat16, 8, false, false>(interleaved, wide, f);
+  if (type == HS_FP16) return pick<__half, 8, false, false>(interleaved, wide, f);
+  return pick<float, 4, false, false>(interleaved, wide, f);
 }
 
 }  // namespace
 
 cudaError_t launch_rotate(const RotateParams& p, int type, int page_type, bool append, bool interleaved,
                           bool wide, cudaStream_t st) {
-  const bool e = page_type == HS_E4M3;
-  if (append) {
-    if (type == HS_BF16)
-      return e ? pick<__nv_bfloat16, 8, true, true>(p, interleaved, wide, st)
-               : pick<__nv_bfloat16, 8, true, false>(p, interleaved, wide, st);
-    return e ? pick<__half, 8, true, true>(p, interleaved, wide, st)
-             : pick<__half, 8, true, false>(p, interleaved, wide, st);
+  return by_type(type, page_type, append, interleaved, wide,
+                 [&](auto kern, auto shape) { return go<decltype(shape)>(kern, p, st); });
+}
+
+cudaError_t prepare_rotate(int type, int page_type, bool append) {
+  for (int variant = 0; variant < 4; ++variant) {
+    const cudaError_t e = by_type(type, page_type, append, variant & 1, variant & 2, [](auto kern, auto) {
+      cudaFuncAttributes fa;
+      return cudaFuncGetAttributes(&fa, kern);
+    });
+    if (e != cudaSuccess) return e;
   }
-  if (type == HS_BF16) return pick<__nv_bfloat16, 8, false, false>(p, interleaved, wide, st);
-  if (type == HS_FP16) return pick<__half, 8, false, false>(p, interleaved, wide, st);
-  return pick<float, 4, false, false>(p, interleaved, wide, st);
+  return cudaSuccess;
 }
 
 }  // namespace hs

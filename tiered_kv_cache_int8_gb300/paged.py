@@ -21,6 +21,7 @@ _VIEWS = (None, HsHeads * 1, HsHeads * 2)
 SCALINGS = {"linear": HS_ROTARY_LINEAR, "ntk": HS_ROTARY_NTK, "by_parts": HS_ROTARY_BY_PARTS}
 
 
+_MOST = (1 << 31) - 1
 _HEADS_BYTES = ctypes.sizeof(HsHeads)
 
 
@@ -137,6 +138,8 @@ class Rotary:
             raise ValueError(f"no rotation of {dtype}")
         views = _VIEWS[k](*[_heads("x", x, dev, dtype) for x in xs])
         n, _, d = x0.shape
+        if n > _MOST:
+            raise ValueError("more than 2^31 - 1 tokens")
         if k == 2 and (x1.shape[0] != n or x1.shape[2] != d):
             raise ValueError("the tensors have different tokens or widths")
         pos = _ints("positions", positions, dev, n)
@@ -162,7 +165,7 @@ class Rotary:
 
         if stream is None:
             return call(_raw_stream(dev.index))
-        return _on_stream(call, stream, dev, (positions, *xs, *(outs or ())))
+        return _on_stream(call, stream, dev, (positions, self._table, *xs, *(outs or ())))
 
 
 class PagedKVCache:
@@ -233,6 +236,11 @@ class PagedKVCache:
     def __exit__(self, *a):
         self.close()
 
+    def _tensors(self):
+        """The cache's own tensors that a call uses."""
+        table = None if self.rotary is None else self.rotary._table
+        return self.pages, self.page_table, self.lengths, self.next_lengths, self.kv_scale, self._error, table
+
     # -- pages and lengths -------------------------------------------------------
     def reserve(self, req: int, n_positions: int):
         """Gives request ``req`` pages for ``n_positions`` positions in all (on the current stream)."""
@@ -285,6 +293,8 @@ class PagedKVCache:
         views = _VIEWS[2](_heads("k", k, dev, dtype, self.d, self.h_kv), _heads("v", v, dev, dtype, self.d, self.h_kv))
         if v.shape[0] != n:
             raise ValueError("k and v have different numbers of rows")
+        if n > _MOST:
+            raise ValueError("more than 2^31 - 1 rows")
         n_req, ids, offs = n, None, None
         if req_ids is not None:
             n_req = req_ids.shape[0]
@@ -322,13 +332,14 @@ class PagedKVCache:
 
         if stream is None:
             return call(_raw_stream(dev.index))
-        return _on_stream(call, stream, dev, (k, v, q, q_out, req_ids, tok_offsets))
+        return _on_stream(call, stream, dev, (k, v, q, q_out, req_ids, tok_offsets, *self._tensors()))
 
     def decode(self, layer: int, q, req_ids=None, lengths=None, out=None, return_lse: bool = False, stream=None):
         """Attention of one token per request: q [requests, h_q, d] -> out of its shape
         (and, with return_lse, the float32 [requests, h_q] logarithms of the softmax sums).
 
         lengths : int32 [max_requests], positions attended to; None: next_lengths
+        out     : where to write (q itself, if it is contiguous: in place)
         """
         dev, dtype, n = self.device, self.dtype, q.shape[0]
         hq = ctypes.byref(_heads("q", q, dev, dtype, self.d, self.h_q))
@@ -355,7 +366,7 @@ class PagedKVCache:
 
         if stream is None:
             return call(_raw_stream(dev.index))
-        return _on_stream(call, stream, dev, (q, req_ids, lengths, out))
+        return _on_stream(call, stream, dev, (q, req_ids, lengths, out, *self._tensors()))
 
     # -- errors ----------------------------------------------------------------------
     def device_error(self) -> int:
