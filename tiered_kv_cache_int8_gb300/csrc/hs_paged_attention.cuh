@@ -41,7 +41,6 @@ namespace pa {
 
 constexpr int UNIT = 16;                 // positions
 constexpr int SEGMENT_COST = 4;          // what a segment costs on top of its units, in units
-constexpr float P_SHIFT = 15.f;          // see weight()
 constexpr int RING_BYTES = 192 * 1024;
 
 template <int D, int NT, int QTYPE, bool E4M3>
@@ -131,11 +130,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// two e4m3 values (low byte first) as two fp16: exact
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
-  uint32_t y;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(y) : "r"(two));
-  return y;
+// four e4m3 values (low byte first) as two and two fp16: exact
+__device__ __forceinline__ void e4m3x4_to_half2(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
 }
 
 __device__ __forceinline__ void tma_unit(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
@@ -145,13 +144,21 @@ __device__ __forceinline__ void tma_unit(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// softmax weight 2^x.  Weights that go to fp16 are taken 2^15 times as large (and
-// so is their sum): with the largest at 2^15, a weight keeps fp16's full precision
-// down to 2^-29 of the largest, where unscaled ones would lose it below 2^-14.
-template <bool BF16>
-__device__ __forceinline__ float weight(float x) {
-  return BF16 ? exp2f(x) : exp2f(x + P_SHIFT);
+// 2^x (to 2^-22 of it; below 2^-126: 0)
+__device__ __forceinline__ float pow2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
+
+// The softmax's reference m.  Weights are 2^(s - m) with m near the running maximum, not
+// at it: m is raised (to the maximum, by shuffles, with o and l rescaled) only once a score
+// is more than SLACK above it, so most units need no exchange between lanes.  Weights are
+// then at most 2^SLACK.  Those that go to fp16 are taken 2^FP16_SHIFT times as large (and
+// so is their sum): at most 2^15, and with fp16's full precision down to 2^-21 of the
+// reference, where unscaled ones would lose it below 2^-14.
+constexpr float SLACK = 8.f;
+constexpr float FP16_SHIFT = 7.f;
 
 // Units of request i of the call (0 with an error bit for a bad one).
 __device__ __forceinline__ int request_units(const PagedDecodeParams& p, int i, int* first_unit, int* first, int* len,
@@ -220,7 +227,7 @@ __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f 
 
 template <bool BF16>
 __device__ __forceinline__ float log_sum(float m, float l) {
-  return l == 0.f ? -INFINITY : (m + log2f(l) - (BF16 ? 0.f : P_SHIFT)) * 0.693147180559945f;
+  return l == 0.f ? -INFINITY : (m + log2f(l) - (BF16 ? 0.f : FP16_SHIFT)) * 0.693147180559945f;
 }
 
 struct Place {   // a unit of the sequence
@@ -349,7 +356,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
       at.n = pre[at.ri + 1] - pre[at.ri];
     }
     Place is = at;                  // the unit whose copy starts next
-    long long to_issue = w1 - w0, to_do = w1 - w0;
+    int to_issue = (int)(w1 - w0), to_do = to_issue;   // (2^40 units at the most, over 1000 warps)
     auto step = [&](Place& x) {
       if (++x.u == x.n) {
         x.u = 0;
@@ -365,39 +372,44 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
     int i_ri = -1, i_unit0 = 0, i_pages = 0;        // the request whose copies are being started
     const int32_t* i_table = nullptr;
     int win = 0, win_page = -1;                     // its page ids win .. win + 31, one per lane
-    bool win_ok = false;
-    unsigned bad = 0;                               // stages whose page id was out of range
+    int i_row = 0, i_left = 0;                      // pool row of the next unit, units left on its page
+    bool i_bad = false;                             // its page id was out of range
+    unsigned bad = 0;                               // the same of each stage
     const int upp = p.page_shift - 4;               // units of a page: 2^upp
     auto issue = [&](int stage) {
-      if (is.ri != i_ri) {
-        int first, len, req;
-        unsigned err = 0;
-        request_units(p, is.ri, &i_unit0, &first, &len, &req, &err);
-        i_ri = is.ri;
-        i_pages = (len + p.page_size - 1) >> p.page_shift;
-        i_table = p.page_table + (long long)req * p.max_pages;
-        win_ok = false;
+      if (i_left == 0) {                            // a page begins, or a segment
+        if (is.ri != i_ri) {
+          int first, len, req;
+          unsigned err = 0;
+          request_units(p, is.ri, &i_unit0, &first, &len, &req, &err);
+          i_ri = is.ri;
+          i_pages = (len + p.page_size - 1) >> p.page_shift;
+          i_table = p.page_table + (long long)req * p.max_pages;
+          win = -64;
+        }
+        const int ua = i_unit0 + is.u;
+        const int pg = ua >> upp;
+        if (pg < win || pg >= win + 32) {
+          win = pg;
+          win_page = win + lane < i_pages ? i_table[win + lane] : -1;
+        }
+        int page = __shfl_sync(FULL_MASK, win_page, pg - win);
+        i_bad = page < 0 || page >= p.n_pages;
+        if (i_bad) {
+          page = 0;                 // some page: its rows are not used
+          if (lane == 0) set_error(p.dev_error, HS_DEVERR_PAGE);
+        }
+        const int in_page = ua & ((1 << upp) - 1);
+        i_row = ((page * 2 * p.h_kv + is.hc / chunks) << p.page_shift) + in_page * UNIT;
+        i_left = min((1 << upp) - in_page, is.n - is.u);
       }
-      const int ua = i_unit0 + is.u;
-      const int pg = ua >> upp;
-      if (!win_ok || pg < win || pg >= win + 32) {
-        win = pg;
-        win_page = win + lane < i_pages ? i_table[win + lane] : -1;
-        win_ok = true;
-      }
-      int page = __shfl_sync(FULL_MASK, win_page, pg - win);
-      if (page < 0 || page >= p.n_pages) {
-        page = 0;                   // some page: its rows are not used
-        bad |= 1u << stage;
-        if (lane == 0) set_error(p.dev_error, HS_DEVERR_PAGE);
-      } else {
-        bad &= ~(1u << stage);
-      }
+      bad = (bad & ~(1u << stage)) | ((unsigned)i_bad << stage);
       if (lane == 0) {
-        const int row = ((page * 2 * p.h_kv + is.hc / chunks) << p.page_shift) + ((ua << 4) & (p.page_size - 1));
         mbar_arrive_expect_tx(&bar[stage], C::STAGE);
-        tma_unit(ring_s + stage * C::STAGE, &map, row, smem_addr(&bar[stage]));
+        tma_unit(ring_s + stage * C::STAGE, &map, i_row, smem_addr(&bar[stage]));
       }
+      i_row += UNIT;
+      --i_left;
       step(is);
     };
     for (int s = 0; s < C::STAGES && to_issue > 0; ++s, --to_issue) issue(s);
@@ -485,7 +497,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
         if (!alive) {                               // a copy did not come: none is started any more
           if (lane == 0) set_error(p.dev_error, HS_DEVERR_TIMEOUT);
           // those in flight get their time before the shared memory goes on to something else
-          const int flying = (int)min(to_do, (long long)C::STAGES);
+          const int flying = min(to_do, C::STAGES);
           for (int j = 0; j < flying; ++j) {
             const int s = stage + j;
             mbar_wait_bounded(&bar[s < C::STAGES ? s : s - C::STAGES], s < C::STAGES ? phase : phase ^ 1u);
@@ -507,8 +519,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
             ldsm4(r, st + piece2(k_at, i));
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const uint32_t a[4] = {e4m3x2_to_half2(r[2 * c]), e4m3x2_to_half2(r[2 * c + 1]),
-                                     e4m3x2_to_half2(r[2 * c] >> 16), e4m3x2_to_half2(r[2 * c + 1] >> 16)};
+              uint32_t a[4];
+              e4m3x4_to_half2(r[2 * c], a[0], a[2]);
+              e4m3x4_to_half2(r[2 * c + 1], a[1], a[3]);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma16816<false>(c ? s2[nt] : s[nt], a, qf[nt][2 * i + c][0], qf[nt][2 * i + c][1]);
             }
@@ -527,7 +540,17 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
         const int lo = max(0, first - pos), hi = (bad >> stage) & 1 ? 0 : min(UNIT, len - pos);
         const bool part = lo > 0 || hi < UNIT;
         const bool in0 = !part || (g >= lo && g < hi), in1 = !part || (g + 8 >= lo && g + 8 < hi);
-        float mx[NT][2];
+        if (part) {
+          // the others may hold anything: their values become 0 (a weight of 0 would leave a NaN one)
+          for (int e = lane; e < UNIT * C::BLOCKS * (C::ROW / 16); e += 32) {
+            const int row = (e / (C::ROW / 16)) % UNIT;
+            if (row < lo || row >= hi)
+              *reinterpret_cast<int4*>(smem + C::SM_RING + ((size_t)warp * C::STAGES + stage) * C::STAGE + C::HALF + e * 16) =
+                  make_int4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();                 // before the next copy to this place
+          __syncwarp();
+        }
         bool grows = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -535,20 +558,19 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
           for (int e = 0; e < 2; ++e) {
             s[nt][e] = in0 ? (s[nt][e] + s2[nt][e]) * fac[nt][e] : -INFINITY;
             s[nt][e + 2] = in1 ? (s[nt][e + 2] + s2[nt][e + 2]) * fac[nt][e] : -INFINITY;
-            float x = fmaxf(s[nt][e], s[nt][e + 2]);
-            x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, 16));
-            mx[nt][e] = x;
-            grows = grows || x > m[nt][e];
+            grows = grows || fmaxf(s[nt][e], s[nt][e + 2]) > m[nt][e] + SLACK;
           }
         if (__any_sync(FULL_MASK, grows)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float n = fmaxf(m[nt][e], mx[nt][e]);
-              const float keep = exp2f(m[nt][e] - (n == -INFINITY ? 0.f : n));
+              float n = fmaxf(s[nt][e], s[nt][e + 2]);
+              n = fmaxf(n, __shfl_xor_sync(FULL_MASK, n, 4));
+              n = fmaxf(n, __shfl_xor_sync(FULL_MASK, n, 8));
+              n = fmaxf(n, __shfl_xor_sync(FULL_MASK, n, 16));
+              n = fmaxf(n, m[nt][e]);
+              const float keep = pow2(m[nt][e] - (n == -INFINITY ? 0.f : n));
               m[nt][e] = n;
               l[nt][e] *= keep;
 #pragma unroll
@@ -568,9 +590,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
           float w[4];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float base = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
-            w[e] = weight<BF16>(s[nt][e] - base);
-            w[e + 2] = weight<BF16>(s[nt][e + 2] - base);
+            const float base = (m[nt][e] == -INFINITY ? 0.f : m[nt][e]) - (BF16 ? 0.f : FP16_SHIFT);
+            w[e] = pow2(s[nt][e] - base);
+            w[e + 2] = pow2(s[nt][e + 2] - base);
             l[nt][e] += w[e] + w[e + 2];
           }
           const uint32_t x = pack2<BF16 ? HS_BF16 : HS_FP16>(w[0], w[1]), y = pack2<BF16 ? HS_BF16 : HS_FP16>(w[2], w[3]);
@@ -581,15 +603,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
             pf[nt][1][1] = transpose8(pack2<HS_BF16>(w[2] - bf16lo(y), w[3] - bf16hi(y)));
           }
         }
-        // ---- O^T += V^T P^T.  Rows that are not attended may hold anything: their values become 0
-        uint32_t keep01 = 0xffffffffu, keep23 = 0xffffffffu;
-        if (part) {
-          auto halves = [&](int r) {
-            return (r >= lo && r < hi ? 0xffffu : 0u) | (r + 1 >= lo && r + 1 < hi ? 0xffff0000u : 0u);
-          };
-          keep01 = halves(2 * t);
-          keep23 = halves(2 * t + 8);
-        }
+        // ---- O^T += V^T P^T
         if constexpr (E4M3) {
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
@@ -597,10 +611,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
             ldsm4_trans(r, st + piece2(v_at, i));
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const uint32_t x = r[2 * c] & keep01, y = r[2 * c + 1] & keep23;
+              const uint32_t x = r[2 * c], y = r[2 * c + 1];
               // a row pair of the tile is elements 2g and 2g+1 of the 16
-              const uint32_t a[4] = {e4m3x2_to_half2(__byte_perm(x, 0, 0x4420)), e4m3x2_to_half2(__byte_perm(x, 0, 0x4431)),
-                                     e4m3x2_to_half2(__byte_perm(y, 0, 0x4420)), e4m3x2_to_half2(__byte_perm(y, 0, 0x4431))};
+              uint32_t a[4];
+              e4m3x4_to_half2(__byte_perm(x, 0, 0x3120), a[0], a[1]);
+              e4m3x4_to_half2(__byte_perm(y, 0, 0x3120), a[2], a[3]);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[nt][2 * i + c], a, pf[nt][0][0], pf[nt][0][1]);
             }
@@ -610,10 +625,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
           for (int c = 0; c < D / 16; ++c) {
             uint32_t a[4];
             ldsm4_trans(a, st + piece2(v_at, c));
-            a[0] &= keep01;
-            a[1] &= keep01;
-            a[2] &= keep23;
-            a[3] &= keep23;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
