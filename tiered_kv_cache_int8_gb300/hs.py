@@ -142,18 +142,18 @@ def lib():
         L.hs_indexer_topk_static_error.restype = ctypes.c_int
         L.hs_rotary_table.argtypes = [P(HsRotaryConfig), P(ctypes.c_double), P(ctypes.c_uint64), P(ctypes.c_float)]
         L.hs_rotary_table.restype = ctypes.c_int
-        L.hs_rotary_apply.argtypes = [P(HsRotary), I32, I32, I32, VP, I32, P(HsHeads), P(HsHeads), I32, VP]
+        L.hs_rotary_apply.argtypes = [P(HsRotary), I32, I32, I32, VP, I32, VP, VP, I32, VP]   # VP: HsHeads, or packed
         L.hs_rotary_apply.restype = ctypes.c_int
         L.hs_paged_create.argtypes = [P(HsPagedConfig), VP, VP, VP, P(VP)]
         L.hs_paged_create.restype = ctypes.c_int
         L.hs_paged_destroy.argtypes = [VP]
         L.hs_paged_destroy.restype = None
-        L.hs_paged_append.argtypes = [VP, I32, I32, VP, I32, VP, VP, VP, VP, P(HsRotary), P(HsHeads), P(HsHeads),
-                                      VP, VP, VP]
+        L.hs_paged_append.argtypes = [VP, I32, I32, VP, I32, VP, VP, VP, VP, P(HsRotary), VP, VP, VP, VP,
+                                      VP]
         L.hs_paged_append.restype = ctypes.c_int
         L.hs_paged_workspace_bytes.argtypes = [VP]
         L.hs_paged_workspace_bytes.restype = ctypes.c_int64
-        L.hs_paged_decode.argtypes = [VP, I32, I32, VP, VP, VP, P(HsHeads), VP, VP, VP, VP]
+        L.hs_paged_decode.argtypes = [VP, I32, I32, VP, VP, VP, VP, VP, VP, VP, VP]
         L.hs_paged_decode.restype = ctypes.c_int
         L.hs_paged_error.argtypes = [VP, P(ctypes.c_uint32)]
         L.hs_paged_error.restype = ctypes.c_int

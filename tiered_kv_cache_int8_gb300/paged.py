@@ -9,6 +9,7 @@ device, ``HsError`` for what the library refuses.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -17,12 +18,11 @@ from .hs import (HS_BF16, HS_E4M3, HS_ERR_DEVICE, HS_FP16, HS_FP32, HS_OK, HS_RO
 
 TYPES = {torch.bfloat16: HS_BF16, torch.float16: HS_FP16, torch.float32: HS_FP32, torch.float8_e4m3fn: HS_E4M3}
 _ROTATED = {torch.bfloat16: HS_BF16, torch.float16: HS_FP16, torch.float32: HS_FP32}
-_VIEWS = (None, HsHeads * 1, HsHeads * 2)
-SCALINGS = {"linear": HS_ROTARY_LINEAR, "ntk": HS_ROTARY_NTK, "by_parts": HS_ROTARY_BY_PARTS}
-
-
+# one and two hs_heads_t in a row (packed: a ctypes structure of each costs a small call much of its time)
+_ONE, _TWO = struct.Struct("Pqqii").pack, struct.Struct("PqqiiPqqii").pack
+assert struct.calcsize("Pqqii") == ctypes.sizeof(HsHeads)
 _MOST = (1 << 31) - 1
-_HEADS_BYTES = ctypes.sizeof(HsHeads)
+SCALINGS = {"linear": HS_ROTARY_LINEAR, "ntk": HS_ROTARY_NTK, "by_parts": HS_ROTARY_BY_PARTS}
 
 
 def _check(rc: int):
@@ -35,23 +35,17 @@ def _need(ok: bool, why: str):
         raise ValueError(why)
 
 
-def _heads(name: str, x, device, dtype, d: int | None = None, heads: int | None = None) -> HsHeads:
-    """The [tokens, heads, d] view of a tensor whose last dimension is dense."""
+def _heads(name: str, x, device, dtype, d: int | None = None, heads: int | None = None) -> tuple:
+    """hs_heads_t of a [tokens, heads, d] tensor whose last dimension is dense."""
     if x.dim() != 3 or x.device != device or x.dtype != dtype:
         raise ValueError(f"{name} must be [tokens, heads, d] {dtype} on {device}, not {list(x.shape)} {x.dtype} on {x.device}")
-    _, h, e = x.shape
-    if (d is not None and e != d) or (heads is not None and h != heads):
-        raise ValueError(f"{name} must be [tokens, {heads}, {d}], not {list(x.shape)}")
+    n, h, e = x.shape
+    if (d is not None and e != d) or (heads is not None and h != heads) or n > _MOST:
+        raise ValueError(f"{name} must be [at most 2^31 - 1 tokens, {heads}, {d}], not {list(x.shape)}")
     ts, hs, es = x.stride()
     if es != 1 and e > 1:
         raise ValueError(f"{name}'s last dimension must be dense")
-    return HsHeads(x.data_ptr(), ts, hs, h, 0)
-
-
-def _dense(x, shape) -> HsHeads:
-    """The view of a new tensor of that shape."""
-    _, h, d = shape
-    return HsHeads(x.data_ptr(), h * d, d, h, 0)
+    return x.data_ptr(), ts, hs, h, 0
 
 
 def _ints(name: str, x, device, n: int):
@@ -65,18 +59,18 @@ def _ints(name: str, x, device, n: int):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-def _on_stream(call, stream, device, tensors):
-    """call(handle) on a given stream: what it allocates belongs to that stream, and the
-    given tensors are marked as used there."""
+
+def _on_stream(stream, device, tensors, call):
+    """call() with a given stream as the current one: what it allocates belongs to that
+    stream, and the given tensors are marked as used there."""
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
-    if stream.cuda_stream == _raw_stream(device.index):
-        return call(stream.cuda_stream)
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
+    if stream.cuda_stream != _raw_stream(device.index):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
     with torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
+        return call()
 
 
 class Rotary:
@@ -129,43 +123,48 @@ class Rotary:
         transpose : the transposed rotation (angles negated): what takes a gradient of
                     the rotated values back; the inverse where magnitude is 1
         """
-        k = len(xs)
+        dev, k = self.device, len(xs)
+        if stream is not None:
+            outs = () if out is None else (out,) if isinstance(out, torch.Tensor) else tuple(out)
+            return _on_stream(stream, dev, (positions, self._table, *xs, *outs),
+                              lambda: self.apply(positions, *xs, out=out, transpose=transpose))
         if k != 1 and k != 2:
             raise ValueError("apply takes one or two tensors")
-        dev, x0, x1 = self.device, xs[0], xs[-1]
-        dtype = x0.dtype
+        x0 = xs[0]
+        dtype, (n, h, d) = x0.dtype, x0.shape if x0.dim() == 3 else (0, 0, 0)
         if dtype not in _ROTATED:
             raise ValueError(f"no rotation of {dtype}")
-        views = _VIEWS[k](*[_heads("x", x, dev, dtype) for x in xs])
-        n, _, d = x0.shape
-        if n > _MOST:
-            raise ValueError("more than 2^31 - 1 tokens")
-        if k == 2 and (x1.shape[0] != n or x1.shape[2] != d):
-            raise ValueError("the tensors have different tokens or widths")
+        views = _heads("x", x0, dev, dtype)
         pos = _ints("positions", positions, dev, n)
         if out is None:
-            outs = None
+            y0 = torch.empty((n, h, d), dtype=dtype, device=dev)
+            into = (y0.data_ptr(), h * d, d, h, 0)
         else:
-            outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
-            if len(outs) != k or any(o.shape != x.shape for o, x in zip(outs, xs)):
+            y0, y1 = (out, None) if isinstance(out, torch.Tensor) else (*out, None)[:2]
+            if y0.shape != x0.shape or (y1 is None) != (k == 1):
                 raise ValueError("out must have the shapes of the inputs")
-
-        def call(raw):
-            ys = outs
-            if ys is None:
-                ys = tuple([torch.empty(x.shape, dtype=dtype, device=dev) for x in xs])
-                into = _VIEWS[k](*[_dense(y, x.shape) for x, y in zip(xs, ys)])
+            into = _heads("out", y0, dev, dtype)
+        if k == 1:
+            views, into = _ONE(*views), _ONE(*into)
+        else:
+            x1 = xs[1]
+            more = _heads("x", x1, dev, dtype, d)
+            if x1.shape[0] != n:
+                raise ValueError("the tensors have different tokens")
+            if out is None:
+                h = more[3]
+                y1 = torch.empty((n, h, d), dtype=dtype, device=dev)
+                into = _TWO(*into, y1.data_ptr(), h * d, d, h, 0)
             else:
-                into = _VIEWS[k](*[_heads("out", y, dev, dtype) for y in ys])
-            rc = lib().hs_rotary_apply(self._plan[1 if transpose else 0], _ROTATED[dtype], d, n, pos, k, views, into,
-                                       dev.index, raw)
-            if rc:
-                _check(rc)
-            return ys[0] if k == 1 else ys
-
-        if stream is None:
-            return call(_raw_stream(dev.index))
-        return _on_stream(call, stream, dev, (positions, self._table, *xs, *(outs or ())))
+                if y1.shape != x1.shape:
+                    raise ValueError("out must have the shapes of the inputs")
+                into = _TWO(*into, *_heads("out", y1, dev, dtype))
+            views = _TWO(*views, *more)
+        rc = lib().hs_rotary_apply(self._plan[1 if transpose else 0], _ROTATED[dtype], d, n, pos, k, views, into,
+                                   dev.index, _raw_stream(dev.index))
+        if rc:
+            _check(rc)
+        return y0 if k == 1 else (y0, y1)
 
 
 class PagedKVCache:
@@ -289,13 +288,15 @@ class PagedKVCache:
                       None: one row per request (with req_ids: the same number for each)
         req_ids     : int32 [requests] distinct ids; None: requests 0, 1, ...
         """
-        dev, dtype, n = self.device, self.dtype, k.shape[0]
-        views = _VIEWS[2](_heads("k", k, dev, dtype, self.d, self.h_kv), _heads("v", v, dev, dtype, self.d, self.h_kv))
+        dev, dtype = self.device, self.dtype
+        if stream is not None:
+            return _on_stream(stream, dev, (k, v, q, q_out, req_ids, tok_offsets, *self._tensors()),
+                              lambda: self.append(layer, k, v, q, q_out, req_ids, tok_offsets))
+        hk, hv = _heads("k", k, dev, dtype, self.d, self.h_kv), _heads("v", v, dev, dtype, self.d, self.h_kv)
+        n_req = n = k.shape[0]
         if v.shape[0] != n:
             raise ValueError("k and v have different numbers of rows")
-        if n > _MOST:
-            raise ValueError("more than 2^31 - 1 rows")
-        n_req, ids, offs = n, None, None
+        ids = offs = hq = ho = rot = None
         if req_ids is not None:
             n_req = req_ids.shape[0]
             ids = _ints("req_ids", req_ids, dev, n_req)
@@ -303,36 +304,27 @@ class PagedKVCache:
             if req_ids is None:
                 n_req = tok_offsets.shape[0] - 1
             offs = _ints("tok_offsets", tok_offsets, dev, n_req + 1)
-        hq = None
+        if self.rotary is not None:
+            rot = self.rotary._plan[0]
         if q is not None:
-            if self.rotary is None:
+            if rot is None:
                 raise ValueError("q needs a cache with a rotation")
-            hq = _heads("q", q, dev, dtype, self.d, self.h_q)
+            hq = _ONE(*_heads("q", q, dev, dtype, self.d, self.h_q))
             if q.shape[0] != n or (q_out is not None and q_out.shape != q.shape):
                 raise ValueError("q, q_out and k have different rows")
+            if q_out is None:
+                q_out = torch.empty((n, self.h_q, self.d), dtype=dtype, device=dev)
+                ho = _ONE(q_out.data_ptr(), self.h_q * self.d, self.d, self.h_q, 0)
+            else:
+                ho = _ONE(*_heads("q_out", q_out, dev, dtype, self.d, self.h_q))
         elif q_out is not None:
             raise ValueError("q_out without q")
-
-        def call(raw):
-            out, h_in, h_out = q_out, None, None
-            if hq is not None:
-                if out is None:
-                    out = torch.empty(q.shape, dtype=dtype, device=dev)
-                    h_out = ctypes.byref(_dense(out, q.shape))
-                else:
-                    h_out = ctypes.byref(_heads("q_out", out, dev, dtype, self.d, self.h_q))
-                h_in = ctypes.byref(hq)
-            rc = lib().hs_paged_append(self._h, layer, n_req, ids, n, offs, self.page_table.data_ptr(),
-                                       self.lengths.data_ptr(), self.next_lengths.data_ptr(),
-                                       None if self.rotary is None else self.rotary._plan[0], h_in, h_out, views,
-                                       ctypes.byref(views, _HEADS_BYTES), raw)
-            if rc:
-                _check(rc)
-            return out
-
-        if stream is None:
-            return call(_raw_stream(dev.index))
-        return _on_stream(call, stream, dev, (k, v, q, q_out, req_ids, tok_offsets, *self._tensors()))
+        rc = lib().hs_paged_append(self._h, layer, n_req, ids, n, offs, self.page_table.data_ptr(),
+                                   self.lengths.data_ptr(), self.next_lengths.data_ptr(), rot, hq, ho, _ONE(*hk),
+                                   _ONE(*hv), _raw_stream(dev.index))
+        if rc:
+            _check(rc)
+        return q_out
 
     def decode(self, layer: int, q, req_ids=None, lengths=None, out=None, return_lse: bool = False, stream=None):
         """Attention of one token per request: q [requests, h_q, d] -> out of its shape
@@ -341,32 +333,28 @@ class PagedKVCache:
         lengths : int32 [max_requests], positions attended to; None: next_lengths
         out     : where to write (q itself, if it is contiguous: in place)
         """
-        dev, dtype, n = self.device, self.dtype, q.shape[0]
-        hq = ctypes.byref(_heads("q", q, dev, dtype, self.d, self.h_q))
+        dev, dtype = self.device, self.dtype
+        if stream is not None:
+            return _on_stream(stream, dev, (q, req_ids, lengths, out, *self._tensors()),
+                              lambda: self.decode(layer, q, req_ids, lengths, out, return_lse))
+        hq = _ONE(*_heads("q", q, dev, dtype, self.d, self.h_q))
+        n, lse, lse_ptr = q.shape[0], None, None
         ids = None if req_ids is None else _ints("req_ids", req_ids, dev, n)
         lens = (self.next_lengths.data_ptr() if lengths is None
                 else _ints("lengths", lengths, dev, self.max_requests))
-        if out is not None and (out.shape != q.shape or out.dtype != dtype or out.device != dev
-                                or not out.is_contiguous()):
+        if out is None:
+            out = torch.empty((n, self.h_q, self.d), dtype=dtype, device=dev)
+        elif out.shape != q.shape or out.dtype != dtype or out.device != dev or not out.is_contiguous():
             raise ValueError("out must be contiguous, of q's shape, type and device")
-
-        def call(raw):
-            o, lse, lse_ptr = out, None, None
-            if o is None:
-                o = torch.empty(q.shape, dtype=dtype, device=dev)
-            if return_lse:
-                lse = torch.empty((n, self.h_q), dtype=torch.float32, device=dev)
-                lse_ptr = lse.data_ptr()
-            ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
-            rc = lib().hs_paged_decode(self._h, layer, n, ids, self.page_table.data_ptr(), lens, hq, o.data_ptr(),
-                                       lse_ptr, ws.data_ptr(), raw)
-            if rc:
-                _check(rc)
-            return (o, lse) if return_lse else o
-
-        if stream is None:
-            return call(_raw_stream(dev.index))
-        return _on_stream(call, stream, dev, (q, req_ids, lengths, out, *self._tensors()))
+        if return_lse:
+            lse = torch.empty((n, self.h_q), dtype=torch.float32, device=dev)
+            lse_ptr = lse.data_ptr()
+        ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
+        rc = lib().hs_paged_decode(self._h, layer, n, ids, self.page_table.data_ptr(), lens, hq, out.data_ptr(),
+                                   lse_ptr, ws.data_ptr(), _raw_stream(dev.index))
+        if rc:
+            _check(rc)
+        return (out, lse) if return_lse else out
 
     # -- errors ----------------------------------------------------------------------
     def device_error(self) -> int:
