@@ -574,7 +574,7 @@ int hs_paged_append(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
  * (HS_DEVERR_CAPACITY).  Positions on a page whose id is out of range are left out
  * (HS_DEVERR_PAGE).  Rows of a page at and behind the length are never used, whatever
  * they hold.  Scores, the softmax and the sums are in 32 bits; the weights that multiply
- * 16-bit (8-bit) values are rounded to the page type (to 16 bits).
+ * values are held as two numbers of 16 bits (8-bit pages: as one).
  * The result does not depend on which page ids hold a request, and is the same bits
  * from call to call.
  */

@@ -96,7 +96,9 @@ def attend(q, pages, table_row, length, window, scale, kv_scale=None):
     if kv_scale is not None:
         e_s = e_s + 2.0 ** -24 * (q64.abs().amax(1) * k.abs().sum(-1).amax(0)) * scale
     e_p = 2 * e_s + 2.0 ** -20 + (n + 64) * 2.0 ** -23        # weights and their sum, sums over n
-    u_p = HALF_STEP[dtype if kv_scale is None else torch.float16]   # the weights' rounding
-    tol = size * (u_p + e_p[:, None]) + 2.0 ** -20 * out.abs()
+    # the weights' rounding: twice to 16 bits (once for 8-bit pages), and fp16's smallest spacing under the
+    # scale of 2^7, against a sum that is 1 at least
+    u_p = HALF_STEP[torch.float16] if kv_scale is not None else HALF_STEP[dtype] ** 2
+    tol = size * (u_p + e_p[:, None]) + 2.0 ** -20 * out.abs() + n * 2.0 ** -32 * v.abs().amax()
     tol = tol + HALF_STEP[dtype] * (out.abs() + tol) + TINY[dtype]
     return out, lse, tol, e_s + 2.0 ** -20 + (n + 64) * 2.0 ** -24 + 2.0 ** -22 * lse.abs()
