@@ -549,7 +549,8 @@ void hs_paged_destroy(hs_paged_t* h);
  * length below 0 or tokens past max_pages * page_size (HS_DEVERR_CAPACITY) is skipped
  * whole (its next length is its length); a position whose page id is out of range is
  * not stored (HS_DEVERR_PAGE).  Offsets that decrease or leave [0, n_tok]
- * (HS_DEVERR_OFFSETS) give their request no tokens.
+ * (HS_DEVERR_OFFSETS) give their request no tokens; which rows the other requests of
+ * the call store is then undefined.
  */
 int hs_paged_append(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* req_ids, int32_t n_tok,
                     const int32_t* tok_offsets, const int32_t* page_table, const int32_t* lengths,

@@ -54,8 +54,8 @@ namespace hs {
 namespace pa {
 
 constexpr int UNIT = 16;                 // positions
-// what a segment costs on top of its units, in units (64 ragged requests: 129 us with 0, 83, 78 and 76 us
-// with 1, 2 and 4; no change up to 12)
+// what a segment costs on top of its units, in units: about two of them by the warps' ends (64 ragged
+// requests over 8-bit pages: 83, 78 and 76 us with 1, 2 and 4; no change from there up to 12)
 constexpr int SEGMENT_COST = 4;
 constexpr int RING_BYTES = 192 * 1024;
 
@@ -252,7 +252,7 @@ __device__ __forceinline__ void store_lane(void* out, long long at, const float 
   if constexpr (VW == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 1 / l of a finished row: 0 where nothing was attended, NaN where a score was one
+// 1 / l of a finished row: 0 where nothing was attended
 __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
 template <bool BF16>
