@@ -180,7 +180,9 @@ __device__ Token locate(const RotateParams& p, int t, int near) {
 // to the pages (E4M3: 8-bit pages).
 //
 // Work items of a row, in order: half layout (and VEC = 1): rot / (2 VEC) items of two
-// accesses (i and i + rot/2), then (d - rot) / VEC copies; interleaved: d / VEC accesses.
+// accesses (i and i + rot/2), then the rest of the row by two accesses (single ones kept
+// half the bytes in flight: 132 instead of 96 us for 32768 tokens of 40 heads of 128 with
+// a quarter rotated); interleaved: d / VEC accesses.
 // A thread has one item of one token and goes down the token's heads with it, so the
 // cosines and sines of its pairs are computed once, by it, and stay in registers: no
 // table, no barrier, and the next head is a stride further.  All its heads start on
@@ -199,8 +201,8 @@ struct Shape {
   static constexpr int GROUPS = 4;                             // copies are waited for in this many steps
   static constexpr int STEP = VEC > 1 ? ROT_AHEAD / (16 * ACCESSES * GROUPS) : 1;   // heads of a step
   static constexpr int HEADS = STEP * GROUPS;                  // most heads of a thread
-  // rows of single elements may need a thread each: up to 1023 of them
-  static constexpr int MAX_THREADS = VEC > 1 ? ROT_THREADS : 1024;
+  // rows taken by single elements may need 512 threads
+  static constexpr int MAX_THREADS = VEC > 1 ? ROT_THREADS : 512;
 };
 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -235,9 +237,10 @@ __global__ void __launch_bounds__(Shape<T, VEC, INTER>::MAX_THREADS, VEC > 1 ? 4
 
   const T* in = static_cast<const T*>(view.in) + t * view.in_ts + h * view.in_hs;
   // the item's places in a row
-  const bool two = !S::PAIRS && j < pairs;
-  const int ia = S::PAIRS ? j * VEC : two ? (INTER ? 2 * j : j * VEC) : p.rot_dim + (j - pairs) * VEC;
-  const int ib = INTER ? 2 * j + 1 : half + j * VEC;
+  const int rest = p.rot_dim + (j - pairs) * VEC;   // of an item behind the pairs: neighbours side by side, twice
+  const int ia = S::PAIRS ? j * VEC : j >= pairs ? rest : INTER ? 2 * j : j * VEC;
+  const int ib = j >= pairs ? rest + (per - pairs) * VEC : INTER ? 2 * j + 1 : half + j * VEC;
+  const bool two = !S::PAIRS && ib < p.d;
   const long long in_hs = view.in_hs;
   extern __shared__ int4 s_in[];                // [head][access][thread]
   if constexpr (VEC > 1) {
@@ -380,7 +383,7 @@ template <typename S, typename K>
 cudaError_t go(K kern, RotateParams p, cudaStream_t st) {
   constexpr int VEC = S::VEC;
   const int half = p.rot_dim / 2;
-  p.items = S::PAIRS ? p.d / VEC : half / VEC + (p.d - p.rot_dim) / VEC;
+  p.items = S::PAIRS ? p.d / VEC : half / VEC + ((p.d - p.rot_dim) / VEC + 1) / 2;
   const int threads = p.items <= ROT_THREADS ? ROT_THREADS : (p.items + 31) / 32 * 32;
   p.groups = threads / p.items;
   if (p.n_views == 0) p.v[0].heads = p.v[0].chunks = p.v[0].chunk_heads = 1;   // no tokens: next_lengths only
