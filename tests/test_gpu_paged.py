@@ -439,6 +439,50 @@ def test_append(typ, kv, d, hq, hk, page, rot, inter, scaling, ragged):
     assert c.device_error() == 0
 
 
+@pytest.mark.parametrize("R", [1, 31, 32, 33, 65])
+def test_append_counts_of_requests(R):
+    # up to 32 requests are found another way than more
+    torch = T()
+    from tiered_kv_cache_int8_gb300 import Rotary, hs
+    counts = [(3 * r + 1) % 4 for r in range(R)]
+    counts[-1] += 2
+    lengths = [(5 * r) % 40 for r in range(R)]
+    offs = [1 + sum(counts[:i]) for i in range(R + 1)]
+    ids = [(7 * r + 3) % R for r in range(R)] if R % 7 else list(range(R))
+    assert sorted(ids) == list(range(R))
+    c, g = make(R, 4, 2, 64, 16, "bf16", "bf16", lengths, rotary=Rotary(32), extra_pages=1)
+    n = offs[-1] + 2
+    q, k, v = (torch.randn(n, h, 64, generator=g, device="cuda").bfloat16() for h in (4, 2, 2))
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")   # noqa: E731
+    qo = torch.full_like(q, 5.0)
+    c.append(0, k, v, q=q, q_out=qo, req_ids=i32(ids), tok_offsets=i32(offs))
+    rows, pos = expected_append(c, 0, k, v, offs, ids, lengths, plain.frequencies(32), 1.0, False)
+    assert len(rows) == 2 * sum(counts)
+    for (p, which, slot), (want, tol) in rows.items():
+        within(c.pages[0, p, which, :, slot], want, tol, f"row {p} {which} {slot}")
+    ts = sorted(pos)
+    want, tol = plain.rotate(q[ts], torch.tensor([pos[t] for t in ts], device="cuda"), plain.frequencies(32))
+    within(qo[ts], want, tol + 2.0 ** -8 * (want.abs() + tol) + plain.TINY[q.dtype], "q")
+    others = [t for t in range(n) if t not in pos]
+    assert (qo[others] == 5.0).all()
+    want = list(lengths)
+    for i, r in enumerate(ids):
+        want[r] += counts[i]
+    assert c.next_lengths.tolist() == want and c.device_error() == 0
+    # a bad id among them: only its request is skipped
+    if R > 1:
+        b = c.pages.view(torch.int16).clone()
+        bad = list(ids)
+        bad[R // 2] = R
+        c.append(0, k * 2, v * 2, req_ids=i32(bad), tok_offsets=i32(offs))
+        assert c.device_error() == hs.HS_DEVERR_REQ_RANGE
+        i, r = R // 2, ids[R // 2]
+        for j in range(counts[i]):
+            at = lengths[r] + j
+            assert torch.equal(c.pages.view(torch.int16)[0, c.page_table[r, at // 16].long(), :, :, at % 16],
+                               b[0, c.page_table[r, at // 16].long(), :, :, at % 16])
+
+
 def test_append_many_requests_and_long_prompts():
     # the search over many offsets (most of them empty), and CTAs that take several tokens
     torch = T()
