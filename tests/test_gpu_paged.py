@@ -267,6 +267,22 @@ def test_decode_splits(lengths, typ, kv, hq, hk, d):
     assert torch.equal(out, again) and torch.equal(lse, lse2)      # the same bits from call to call
 
 
+@pytest.mark.parametrize("typ, kv, hq, hk, d, page", [("bf16", "bf16", 32, 8, 128, 64), ("fp16", "e4m3", 40, 2, 64, 16),
+                                                      ("bf16", "e4m3", 8, 8, 256, 32), ("fp16", "fp16", 12, 4, 256, 128)])
+@pytest.mark.parametrize("most", [40, 512, 513, 1024, 1025])
+def test_decode_short_contexts(typ, kv, hq, hk, d, page, most):
+    # tables whose width decides between whole segments for each CTA and shared ones
+    torch = T()
+    for R in (1, 9, 40):
+        lengths = [(most if r == 0 else (97 * r + most // 3) % (most + 1)) for r in range(R)]
+        if R > 2:
+            lengths[2] = 0
+        c, g = make(R, hq, hk, d, page, typ, kv, lengths, seed=R + most)
+        q = torch.randn(R, hq, d, generator=g, device="cuda").to(dtype(typ))
+        check_decode(c, q, lengths)
+        assert c.device_error() == 0
+
+
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_decode_values_at_the_border(kv):
     # large and tiny scores, a row that wins alone, equal rows, zero queries

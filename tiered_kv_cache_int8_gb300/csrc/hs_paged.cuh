@@ -82,12 +82,13 @@ struct PagedDecodeParams {
   int32_t n_req, max_requests, max_pages, n_pages, page_size, page_shift;
   int32_t h_q, h_kv, group, d, window, type, page_type;
   int32_t grid;
+  int32_t whole;         // every CTA takes whole segments
   float scale_log2;
 };
 
 cudaError_t launch_rotate(const RotateParams& p, int type, int page_type, bool append, bool interleaved,
                           bool wide, cudaStream_t st);
-cudaError_t launch_paged_decode(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st);
+cudaError_t launch_paged_decode(PagedDecodeParams p, const CUtensorMap& map, cudaStream_t st);
 // load the kernels of a configuration on the current device and set what they need
 cudaError_t prepare_paged(int d, int group, int type, int page_type);
 cudaError_t prepare_rotate(int type, int page_type, bool append);

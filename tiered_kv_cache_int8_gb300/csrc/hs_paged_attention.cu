@@ -79,7 +79,11 @@ cudaError_t prepare_paged(int d, int group, int type, int page_type) {
                     : prepare_paged_d256(group, type, page_type);
 }
 
-cudaError_t launch_paged_decode(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st) {
+cudaError_t launch_paged_decode(PagedDecodeParams p, const CUtensorMap& map, cudaStream_t st) {
+  // the most units a request can have: a window may lie across one more than it fills
+  const int units = p.max_pages << (p.page_shift - 4);
+  const int most = p.window > 0 ? std::min(units, p.window / pa::UNIT + 2) : units;
+  p.whole = most <= (p.n_req * p.h_kv >= pa::MANY_SEGMENTS ? pa::WHOLE_UNITS_MANY : pa::WHOLE_UNITS);
   return p.d == 64 ? paged_decode_d64(p, map, st) : p.d == 128 ? paged_decode_d128(p, map, st) : paged_decode_d256(p, map, st);
 }
 

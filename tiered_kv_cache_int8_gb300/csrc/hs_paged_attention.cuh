@@ -39,6 +39,10 @@
 // needs no shuffling: queries are loaded in the order in which key bytes come, and
 // output rows leave in that of the value bytes.
 //
+// Short contexts.  Where no request of the call can have more than a few dozen units (by
+// the table's width or the window), CTAs take whole segments: nothing crosses CTAs, and
+// the second kernel, 3 us on the GPU and 4 of a call through the API, is not launched.
+//
 // Pieces.  A (request, head) wholly inside a warp's share is written out by the
 // warp.  What crosses warps is joined by the CTA at its end, what crosses CTAs goes
 // to the workspace and is joined by the second kernel (a programmatic dependent):
@@ -58,6 +62,10 @@ constexpr int UNIT = 16;                 // positions
 // requests over 8-bit pages: 83, 78 and 76 us with 1, 2 and 4; no change from there up to 12)
 constexpr int SEGMENT_COST = 4;
 constexpr int RING_BYTES = 192 * 1024;
+// Units of a segment up to which CTAs take whole ones (see above).  Of 32/8 heads of 128, bf16: one
+// request of 512 positions 7.9 us either way, of 1024 11.0 instead of 8.0, but 16 of 1024 15.2 instead of
+// 18.6 and 128 of them 89 instead of 93; through the API every such call takes 12.4 us instead of 16.3.
+constexpr int WHOLE_UNITS = 32, WHOLE_UNITS_MANY = 64, MANY_SEGMENTS = 64;
 
 template <int D, int NT, int QTYPE, bool E4M3>
 struct Cfg {
@@ -343,24 +351,35 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
   // (64-bit divisions take a while: only for sequences that need them)
   long long share = total < (1 << 30) ? ((int)total + (int)gridDim.x - 1) / (int)gridDim.x
                                       : (total + gridDim.x - 1) / gridDim.x;
-  if (share < C::WARPS) share = C::WARPS;
-  const long long wshare = (share + C::WARPS - 1) / C::WARPS;
-  const long long cta0 = blockIdx.x * share;
-  // units before a cost position, and the place of the next one: the share's begin by the
-  // even lanes, its end by the odd ones
-  const long long x0 = min(total, cta0 + warp * wshare);
-  const long long x1 = min(min(total, cta0 + share), x0 + wshare);
+  if (share < C::WARPS && !p.whole) share = C::WARPS;
+  // the request in which a cost position x < total lies
+  auto request_at = [&](long long x) {
+    int lo = 0, hi = p.n_req;       // cost_before(lo) <= x < cost_before(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cost_before(mid) <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+  };
+  // Each of these is worked out for the share's begin by the even lanes, for its end by the odd ones.
+  long long edge = min(total, (blockIdx.x + (lane & 1)) * share);
+  if (p.whole && edge < total) {    // whole segments: up to where one begins
+    const int r = request_at(edge), n = pre[r + 1] - pre[r] + SEGMENT_COST;
+    const int off = (int)(edge - cost_before(r)) % n;
+    edge += off ? n - off : 0;
+  }
+  const long long cta0 = __shfl_sync(FULL_MASK, edge, 0), cta1 = __shfl_sync(FULL_MASK, edge, 1);
+  const long long wshare = (cta1 - cta0 + C::WARPS - 1) / C::WARPS;
+  // units before a cost position, and the place of the next one
+  const long long x0 = min(cta1, cta0 + warp * wshare);
+  const long long x1 = min(cta1, x0 + wshare);
   Place at = {0, 0, 0, 1};          // the unit to be consumed next
   long long w0, w1;
   {
     const long long x = lane & 1 ? x1 : x0;
     long long units = (long long)pre[p.n_req] * hcn;
     if (x < total) {
-      int lo = 0, hi = p.n_req;     // cost_before(lo) <= x < cost_before(hi)
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cost_before(mid) <= x) lo = mid; else hi = mid;
-      }
+      const int lo = request_at(x);
       const int n = pre[lo + 1] - pre[lo], rem = (int)(x - cost_before(lo));
       const int hc = rem / (n + SEGMENT_COST);
       const int u = max(0, rem - hc * (n + SEGMENT_COST) - SEGMENT_COST);
@@ -828,7 +847,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
         }
       }
     }
-    if (tid == 0) reinterpret_cast<Chain*>(p.ws + ws_chain(C::PIECE, gridDim.x, C::WARPS))[blockIdx.x] = chain;
+    if (tid == 0 && !p.whole) reinterpret_cast<Chain*>(p.ws + ws_chain(C::PIECE, gridDim.x, C::WARPS))[blockIdx.x] = chain;
   }
 
   // ---- requests without a position
@@ -936,7 +955,7 @@ struct Kernels {
   static cudaError_t launch(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st) {
     const cudaError_t e = launch_pdl(paged_decode_kernel<D, NT, QTYPE, E4M3>, dim3(p.grid), dim3(C::THREADS),
                                      C::smem(p.n_req), st, p, map);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || p.whole) return e;
     return launch_pdl(paged_join_kernel<D, NT, QTYPE, E4M3>, dim3(p.grid, C::HEADS), dim3(32 * JOIN_WARPS), 0, st, p);
   }
 };
