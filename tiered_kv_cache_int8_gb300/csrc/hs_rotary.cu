@@ -11,8 +11,8 @@
 //
 // Memory-bound: each element is read and written once, 16 bytes at a time where
 // the views allow it.  Measured (GB300, copy rate 6.7 TB/s): 32768 tokens of 40 heads
-// of 128, bf16: 98 us, 6.9 TB/s; 20 K tokens of 32 + 8 + 8 heads into 8-bit pages: 75
-// us, 6.2 TB/s (issue slots 70 % busy); 16 tokens: 1.9 us, and 3.1 us into pages.
+// of 128, bf16: 98 us, 6.9 TB/s; 20 K tokens of 32 + 8 + 8 heads into 8-bit pages: 73
+// us, 6.3 TB/s (issue slots 70 % busy); 16 tokens: 1.9 us, and 2.8 us into pages.
 #include "hs_paged.cuh"
 
 namespace hs {
