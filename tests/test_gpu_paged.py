@@ -155,7 +155,7 @@ def test_rotary_refuses_what_the_binding_sees():
     with pytest.raises(HsError):
         R.apply(pos, x, out=x[:1].expand(4, 2, 64))   # outputs share memory
     for bad in (dict(scaling={"kind": "no"}), dict(scaling={"kind": "linear"}), dict(scaling={"kind": "linear", "factor": 2, "low": 1}),
-                dict(inv_freq=[1.0]), dict(magnitude=0.0)):
+                dict(inv_freq=[1.0]), dict(magnitude=0.0), dict(inv_freq=[1.0] * 32, scaling={"kind": "linear", "factor": 2})):
         with pytest.raises(ValueError):
             Rotary(64, **bad)
     with pytest.raises(HsError):
@@ -677,6 +677,42 @@ def test_captured_steps_share_nothing():
             assert torch.equal(c.pages[0, c.page_table[r, n // 32].long(), 1, :, n % 32], v[r])
         check_decode(c, qr, after, out=o, lse=l)
     assert c.device_error() == 0
+
+
+def test_two_threads():
+    # two threads, a stream each, on one cache: appends to their own layers, then attention
+    import threading
+    torch = T()
+    from tiered_kv_cache_int8_gb300 import Rotary
+    c, g = make(3, 8, 2, 64, 16, "bf16", "bf16", [500, 20, 0], layers=2, rotary=Rotary(64), extra_pages=1)
+    c.pages[1] = c.pages[0]
+    ins = [[tuple(torch.randn(3, h, 64, generator=g, device="cuda").bfloat16() for h in (8, 2, 2)) for _ in range(20)] for _ in range(2)]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def work(layer):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for q, k, v in ins[layer]:
+                    qr = c.append(layer, k, v, q=q)
+                    got[layer].append((qr, *c.decode(layer, qr, return_lse=True)))
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:   # noqa: BLE001 (told by the main thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(layer,)) for layer in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not errors
+    for layer in range(2):
+        for (q, k, v), (qr, out, lse) in zip(ins[layer], got[layer]):
+            again = c.append(layer, k, v, q=q)
+            assert torch.equal(again, qr)
+            o2, l2 = c.decode(layer, again, return_lse=True)
+            assert torch.equal(o2, out) and torch.equal(l2, lse)
+        check_decode(c, qr, [501, 21, 1], layer=layer, out=out, lse=lse)
 
 
 def test_streams():

@@ -94,6 +94,7 @@ class Rotary:
             _need(set(sc) <= known and "factor" in sc and (kind != HS_ROTARY_BY_PARTS or "original_context" in sc),
                   f"scaling of kind {name} takes {sorted(known)}")
         _need(magnitude is None or magnitude > 0, "magnitude must be > 0")
+        _need(inv_freq is None or scaling is None, "inv_freq takes the place of the formulas: no scaling beside it")
         cfg = HsRotaryConfig(base, sc.get("factor", 1.0), sc.get("original_context", 0.0), sc.get("low", 1.0),
                              sc.get("high", 32.0), magnitude or 0.0, rot_dim, kind)
         n = max(1, rot_dim // 2)
