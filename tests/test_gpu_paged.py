@@ -311,8 +311,8 @@ def test_decode_ids_scale_strides_and_layers():
     torch = T()
     lengths = [40, 0, 333, 64, 1, 129]
     c, g = make(6, 12, 4, 128, 16, "fp16", "fp16", lengths, layers=3, layer=2, scale=0.3)
-    wide = torch.randn(4, 2 * 12 * 128, generator=g, device="cuda").half()
-    q = wide[:, 12 * 128:].view(4, 12, 128)
+    wide = torch.randn(4, 14 * 128, generator=g, device="cuda").half()
+    q = wide[:, 128:13 * 128].view(4, 12, 128)
     ids = [5, 2, 1, 0]
     check_decode(c, q, lengths, layer=2, scale=0.3, ids=ids)
     ht = torch.randn(12, 4, 128, generator=g, device="cuda").half().transpose(0, 1)
