@@ -885,3 +885,27 @@ def test_the_two_tier_cache_takes_rotated_rows():
     ma, rel = attention_error(as_bits(out[0]), ref)
     assert ma <= MAX_ABS and rel <= REL_L2
     c.close()
+
+
+def test_append_over_more_threads_than_31_bits_count():
+    # one-element accesses of broadcast rows, most of which belong to nobody: 9 million CTAs of 256 threads
+    torch = T()
+    from tiered_kv_cache_int8_gb300 import PagedKVCache, Rotary
+    n, hk, d, page = 140000, 1024, 64, 16
+    assert n * 2 * (hk // 4) // 8 * 256 > 1 << 31
+    c = PagedKVCache(n_layers=1, n_pages=3, page_size=page, max_requests=2, max_pages=2, h_q=hk, h_kv=hk, d=d, rotary=Rotary(2))
+    c.pages.zero_()
+    c.page_table.copy_(torch.tensor([[2, 0], [1, -1]], dtype=torch.int32))
+    c.set_lengths(torch.tensor([15, 3], dtype=torch.int32, device="cuda"))
+    g = torch.Generator(device="cuda").manual_seed(11)
+    k, v = (torch.randn(1, 1, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    c.append(0, k.expand(n, hk, d), v.expand(n, hk, d), tok_offsets=torch.tensor([5, 7, 8], dtype=torch.int32, device="cuda"))
+    assert c.next_lengths.tolist() == [17, 4] and c.lengths.tolist() == [15, 3] and c.device_error() == 0
+    at = {(2, 15): 15, (0, 0): 16, (1, 3): 3}           # (page, slot): position
+    for (p, slot), pos in at.items():
+        want, tol = plain.rotate(k, torch.tensor([pos], device="cuda"), plain.frequencies(2))
+        got = c.pages[0, p, :, :, slot].clone()
+        within(got[0], want[0].expand(hk, d), (tol + 2.0 ** -8 * (want.abs() + tol) + plain.TINY[k.dtype])[0].expand(hk, d), "keys")
+        assert torch.equal(got[1], v[0].expand(hk, d))
+        c.pages[0, p, :, :, slot] = 0
+    assert not c.pages.any()

@@ -20,6 +20,7 @@ namespace {
 
 constexpr int ROT_THREADS = 256;
 constexpr int ROT_AHEAD = 128;    // most bytes of a thread in flight (256: no faster, fewer CTAs an SM)
+constexpr int LENGTH_CTAS = PG_MAX_REQUESTS / ROT_THREADS;   // CTAs that write next_lengths
 
 template <typename T>
 struct Elem;
@@ -297,8 +298,10 @@ __global__ void __launch_bounds__(Shape<T, VEC, INTER>::MAX_THREADS, VEC > 1 ? 4
   int pos = 0;
   Token tok = {0, 1, -1, 0};
   if constexpr (APPEND) {
-    if (p.next_lengths) {
-      for (int i = blockIdx.x * blockDim.x + tid; i < p.n_req; i += gridDim.x * blockDim.x) {
+    // the first CTAs only: blockIdx.x * blockDim.x of all of them may pass 32 bits
+    if (p.next_lengths && blockIdx.x < LENGTH_CTAS) {
+      const int ctas = min(gridDim.x, (unsigned)LENGTH_CTAS);
+      for (int i = blockIdx.x * blockDim.x + tid; i < p.n_req; i += ctas * blockDim.x) {
         const int req = p.req_ids ? p.req_ids[i] : i;
         unsigned err = 0;
         int first;
