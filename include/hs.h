@@ -411,7 +411,8 @@ int hs_indexer_topk_static_error(int32_t device, uint32_t* out);
 #define HS_E4M3 3 /* 8-bit e4m3 pages, with one scale per kv head */
 
 /* A [tokens][heads][d] view of 16- or 32-bit elements: element (t, h, i) is at
- * data + t * token_stride + h * head_stride + i (strides in elements, >= 0); 1 to 4096 heads. */
+ * data + t * token_stride + h * head_stride + i (strides in elements, in [0, 2^40], the last
+ * token and head within 2^46 of the first); 1 to 4096 heads. */
 typedef struct hs_heads {
   void* data;
   int64_t token_stride;

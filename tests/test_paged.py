@@ -244,3 +244,24 @@ def test_binding_structs_follow_the_header(struct, cls):
              "void*": ctypes.c_void_p, "const uint64_t*": ctypes.c_void_p}
     want = [(m[1], ctype[m[0]]) for m in re.findall(r"(const uint64_t\*|void\*|int32_t|int64_t|float|double)\s+(\w+)\s*;", body)]
     assert list(getattr(hs, cls)._fields_) == want
+
+
+@pytest.mark.parametrize("n, ts, h, hs_, taken", [
+    (1 + (1 << 24), 1 << 40, 4, 64, False),        # 2^64 elements, what wraps around to none
+    (1 + (1 << 30), 1 << 33, 4, 64, False), ((1 << 31) - 1, 1 << 40, 1, 0, False), (2, 256, 4096, 1 << 40, False),
+    (2, 1 << 40, 66, 1 << 40, False), (65, 1 << 40, 4, 64, True), (66, 1 << 40, 4, 64, False), (1, 1 << 40, 65, 1 << 40, True)])
+@pytest.mark.parametrize("which", ["in", "out"])
+def test_views_beyond_64_bits_are_refused(L, n, ts, h, hs_, taken, which):
+    # device -1: a call whose arguments pass stops at the device, with another code
+    from tiered_kv_cache_int8_gb300 import hs
+    rot = hs.HsRotary(4096, 64, 0, 0, 1.0)
+    far, near = heads(1 << 50, ts, hs_, h), heads(1 << 12, 64 * h, 64, h)
+    if not taken:
+        near.data = far.data + 2 * ts              # on far's second row, or apart from it only modulo 2^64
+    i, o = (far, near) if which == "in" else (near, far)
+    rc = L.hs_rotary_apply(ctypes.byref(rot), hs.HS_BF16, 64, n, 4096, 1, ctypes.byref(i), ctypes.byref(o), -1, None)
+    if taken:
+        assert rc == hs.HS_ERR_CUDA
+    else:
+        assert rc == hs.HS_ERR_INVALID
+        assert "within 2^46" in L.hs_last_error(None).decode()

@@ -49,6 +49,10 @@ const char* check_view(const hs_heads_t& v, int n_tok, int d, size_t es, bool wr
   if (v.token_stride < 0 || v.head_stride < 0 || v.token_stride > lim || v.head_stride > lim)
     return "a view's strides must be in [0, 2^40]";
   if (reinterpret_cast<uintptr_t>(v.data) % es) return "a view's data is not aligned to its element type";
+  // (so that extents, and bytes behind an address, stay far inside 64 bits)
+  const int64_t reach = (int64_t)1 << 46;
+  if ((v.token_stride && n_tok - 1 > reach / v.token_stride) || (v.head_stride && v.heads - 1 > reach / v.head_stride))
+    return "a view's last token and head must be within 2^46 elements of its first";
   if (written) {
     const bool one_t = n_tok == 1, one_h = v.heads == 1;
     const bool th = (one_h || v.head_stride >= d) &&
