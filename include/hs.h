@@ -476,9 +476,12 @@ typedef struct hs_rotary {
  *   d        : elements of a head, in [2, 1024]
  *   n_tok    : tokens (0: a no-op);  positions: dev int32 [n_tok]
  *   in, out  : n_views (1 or 2) views each; out[i] is in[i] itself (same data and
- *              strides: in place) or memory apart from it.  Output elements must be
- *              distinct, and none of them an element of the other view's input.  Any alignment of the element type; 16-byte aligned views
- *              and strides take the faster loads
+ *              strides: in place) or apart from it, and apart from the other view's
+ *              input and output.  Apart are views whose ranges of bytes do not meet, or
+ *              whose strides show that they share no element (slices of one projection);
+ *              others are refused, as are outputs whose own elements overlap.  Any
+ *              alignment of the element type; 16-byte aligned views and strides take the
+ *              faster loads
  *   device   : CUDA device of the buffers (the current device is left as it was)
  */
 int hs_rotary_apply(const hs_rotary_t* rot, int32_t type, int32_t d, int32_t n_tok, const int32_t* positions,
@@ -541,8 +544,8 @@ void hs_paged_destroy(hs_paged_t* h);
  *   rot         : rotation of k (and q) at the token's position, or NULL for none
  *                 (its transpose field must be 0)
  *   q, q_out    : views of the step's queries and of their rotated values, or both
- *                 NULL; in place or apart as for hs_rotary_apply (no element of q_out
- *                 one of k or v); needs rot
+ *                 NULL; in place or apart, and q_out apart from k and v, as for
+ *                 hs_rotary_apply; needs rot
  *   k, v        : views of the new keys and values (h_kv heads)
  * The row of token j of request r takes position lengths[r] + j.  `lengths` itself is
  * not changed, so every layer of a step is given the same one, and a call that is

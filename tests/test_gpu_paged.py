@@ -909,3 +909,31 @@ def test_append_over_more_threads_than_31_bits_count():
         assert torch.equal(got[1], v[0].expand(hk, d))
         c.pages[0, p, :, :, slot] = 0
     assert not c.pages.any()
+
+
+def test_outputs_over_another_tensor_are_refused():
+    torch = T()
+    from tiered_kv_cache_int8_gb300 import HsError, Rotary
+    n, h, d = 9, 4, 64
+    R = Rotary(d)
+    g = torch.Generator(device="cuda").manual_seed(12)
+    pos = torch.arange(3, 3 + n, dtype=torch.int32, device="cuda")
+    qkv = torch.randn(n, h, 3, d, generator=g, device="cuda").bfloat16()    # queries, keys and values of a head together
+    q, k = qkv[:, :, 0], qkv[:, :, 1]
+    want = R.apply(pos, q, k)
+    before = qkv.clone()
+    for out in ((k, q), (q, q), (torch.empty_like(want[0]),) * 2, (q, q[:, :, :]), (k, torch.empty_like(want[0]))):
+        with pytest.raises(HsError):
+            R.apply(pos, q, k, out=out)
+    with pytest.raises(HsError):
+        R.apply(pos, q, q, out=(q, torch.empty_like(want[0])))
+    assert torch.equal(qkv, before)
+    R.apply(pos, q, k, out=(q, k))
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(qkv[:, :, 2], before[:, :, 2])
+    c, cq, ck, cv, _ = small_step(2)
+    out = ck.repeat(1, 4, 1)
+    with pytest.raises(HsError):
+        c.append(0, out[:, :2], cv, q=cq, q_out=out)
+    with pytest.raises(HsError):
+        c.append(0, ck, out[:, 6:], q=cq, q_out=out)
+    assert c.device_error() == 0 and not c.next_lengths.ne(c.lengths).any()

@@ -265,3 +265,87 @@ def test_views_beyond_64_bits_are_refused(L, n, ts, h, hs_, taken, which):
     else:
         assert rc == hs.HS_ERR_INVALID
         assert "within 2^46" in L.hs_last_error(None).decode()
+
+
+def elements(view, n, d):
+    return {view.data // 2 + t * view.token_stride + h * view.head_stride + i
+            for t in range(n) for h in range(view.heads) for i in range(d)}
+
+
+def apply_two(L, ins, outs, n, d=8):
+    # device -1: a call whose arguments pass stops at the device, with another code than a refusal's
+    from tiered_kv_cache_int8_gb300 import hs
+    rot = hs.HsRotary(4096, d, 0, 0, 1.0)
+    rc = L.hs_rotary_apply(ctypes.byref(rot), hs.HS_BF16, d, n, 4096, len(ins), (hs.HsHeads * len(ins))(*ins),
+                           (hs.HsHeads * len(outs))(*outs), -1, None)
+    assert rc in (hs.HS_ERR_INVALID, hs.HS_ERR_CUDA)
+    return rc == hs.HS_ERR_CUDA
+
+
+@pytest.mark.parametrize("what", ["two_outputs", "swapped", "out0_in1", "out1_in0", "one_input_in_place", "one_row", "shifted"])
+def test_rotary_apply_refuses_outputs_over_the_other_view(L, what):
+    a, b = heads(1 << 12, 32, 8, 4), heads(1 << 16, 32, 8, 4)
+    x, y = heads(1 << 20, 32, 8, 4), heads(1 << 24, 32, 8, 4)
+    assert apply_two(L, (a, b), (x, y), 5) and apply_two(L, (a, b), (a, b), 5) and apply_two(L, (a, a), (x, y), 5)
+    ins, outs = {"two_outputs": ((a, b), (x, x)), "swapped": ((a, b), (b, a)), "out0_in1": ((a, b), (b, y)),
+                 "out1_in0": ((a, b), (x, a)), "one_input_in_place": ((a, a), (a, y)),
+                 "one_row": ((a, heads(1 << 16, 32, 8, 1)), (x, heads(x.data + 4 * 64 + 3 * 16, 32, 8, 1))),   # x's last
+                 "shifted": ((a, b), (x, heads(x.data + 8, 32, 8, 4)))}[what]
+    assert not apply_two(L, ins, outs, 5)
+    assert "overlaps the other" in L.hs_last_error(None).decode()
+
+
+@pytest.mark.parametrize("n", [1, 5])
+@pytest.mark.parametrize("layout", ["projection", "interleaved", "heads_first", "alternate_rows", "heads_first_interleaved"])
+def test_rotary_apply_takes_slices_of_one_buffer_in_place(L, n, layout):
+    # queries of 4 heads of 8 elements and keys of 4 (projection: of 2)
+    q, k = {"projection": (heads(4096, 64, 8, 4), heads(4096 + 64, 64, 8, 2)),
+            "interleaved": (heads(4096, 96, 24, 4), heads(4096 + 16, 96, 24, 4)),         # [n][heads][q, k, v][8]
+            "heads_first": (heads(4096, 8, 8 * n, 4), heads(4096 + 64 * n, 8, 8 * n, 4)),  # [heads][n][8]
+            "alternate_rows": (heads(4096, 64, 8, 4), heads(4096 + 64, 64, 8, 4)),
+            "heads_first_interleaved": (heads(4096, 24, 24 * n, 4), heads(4096 + 32, 24, 24 * n, 4))}[layout]
+    assert not elements(q, n, 8) & elements(k, n, 8)
+    assert apply_two(L, (q, k), (q, k), n) and apply_two(L, (k, q), (k, q), n)
+    away = heads(1 << 20, 32, 8, 4), heads(1 << 24, 8 * k.heads, 8, k.heads)
+    assert apply_two(L, (q, k), away, n) and apply_two(L, (q, k), (q, away[1]), n)
+
+
+def test_no_overlap_passes(L):
+    # small views of any strides: a call that passes has outputs apart from each other and from the other input
+    import random
+    rng = random.Random(7)
+    passed = 0
+    for _ in range(4000):
+        n = rng.randint(1, 4)
+        out = [heads(4096 + 2 * rng.randint(0, 160), rng.choice([0, 4, 8, 12, 16, 24, 40, 48]), rng.choice([0, 4, 8, 12, 20, 32, 48, 96]),
+                     rng.randint(1, 3)) for _ in range(2)]
+        other = heads(4096 + 2 * rng.randint(0, 160), rng.choice([0, 4, 8, 12, 24, 40]), rng.choice([0, 4, 12, 32]), out[1].heads)
+        ins = [out[0], out[1] if rng.random() < 0.5 else other]
+        if apply_two(L, ins, out, n, d=4):
+            passed += 1
+            sets = [elements(v, n, 4) for v in (out[0], out[1], ins[1])]
+            assert all(len(s) == n * v.heads * 4 for s, v in zip(sets, out))
+            assert not sets[0] & sets[1] and not sets[0] & sets[2]
+            if ins[1] is not out[1]:
+                assert not sets[1] & sets[2]
+    assert passed > 100
+
+
+@pytest.mark.parametrize("what", ["fine", "k", "v", "k_row", "v_slice"])
+def test_paged_append_refuses_queries_over_new_rows(L, what):
+    from tiered_kv_cache_int8_gb300 import hs
+    _, h = create(L, device=-1)
+    rot = hs.HsRotary(4096, 128, 0, 0, 1.0)
+    # slices of one projection, rotated in place: 8 + 2 + 2 heads of 128
+    q, k, v = heads(1 << 20, 1536, 128, 8), heads((1 << 20) + 2048, 1536, 128, 2), heads((1 << 20) + 2560, 1536, 128, 2)
+    qo = q
+    if what == "k": qo = heads(k.data, 1024, 128, 8)
+    if what == "v": qo = heads(1 << 24, 1024, 128, 8); v = heads(1 << 24, 256, 128, 2)
+    if what == "k_row": qo = heads(1 << 24, 1024, 128, 8); k = heads((1 << 24) + 7 * 2048 + 1792, 1536, 128, 2)
+    if what == "v_slice": qo = heads(q.data + 256, 1536, 128, 8); q = heads(1 << 24, 1024, 128, 8); v = heads((1 << 20) + 256, 1536, 128, 2)
+    R = ctypes.byref
+    rc = L.hs_paged_append(h, 0, 4, None, 8, None, 4096, 1 << 14, 1 << 15, R(rot), R(q), R(qo), R(k), R(v), None)
+    assert rc == (hs.HS_ERR_CUDA if what == "fine" else hs.HS_ERR_INVALID)
+    if what != "fine":
+        assert "overlaps" in L.hs_last_error(None).decode()
+    L.hs_paged_destroy(h)

@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdio>
 #include <new>
+#include <numeric>
 #include <string>
 
 #include "hs_paged.cuh"
@@ -69,9 +70,25 @@ bool same_view(const hs_heads_t& a, const hs_heads_t& b, int n_tok) {
          (a.heads == 1 || a.head_stride == b.head_stride);
 }
 
+// Whether no element of `a` (n_tok tokens, aligned to its type) is one of `b`: their ranges
+// of bytes do not meet, or neither do the places that they take modulo a stride which both
+// keep to: one token's heads modulo the tokens' stride (slices of one projection), a head of
+// every token modulo the heads' stride, single rows modulo what divides all strides
+// ([tokens][heads][q, k, v][d]).  Views that none of these parts pass as meeting.
 bool apart(const hs_heads_t& a, const hs_heads_t& b, int n_tok, int d, size_t es) {
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.data), b0 = reinterpret_cast<uintptr_t>(b.data);
-  return a0 + (size_t)extent(a, n_tok, d) * es <= b0 || b0 + (size_t)extent(b, n_tok, d) * es <= a0;
+  if (a0 + (size_t)extent(a, n_tok, d) * es <= b0 || b0 + (size_t)extent(b, n_tok, d) * es <= a0) return true;
+  const int64_t delta = (int64_t)(b0 - a0) / (int64_t)es;
+  const int64_t at = n_tok > 1 ? a.token_stride : 0, bt = n_tok > 1 ? b.token_stride : 0;
+  const int64_t ah = a.heads > 1 ? a.head_stride : 0, bh = b.heads > 1 ? b.head_stride : 0;
+  auto distinct = [&](int64_t stride, int64_t a_span, int64_t b_span) {   // of [0, a_span) and [delta, delta + b_span)
+    if (stride == 0) return false;
+    const int64_t r = (delta % stride + stride) % stride;
+    return a_span <= r && r + b_span <= stride;
+  };
+  const int64_t t = std::gcd(at, bt), h = std::gcd(ah, bh);
+  return distinct(t, (a.heads - 1) * ah + d, (b.heads - 1) * bh + d) ||
+         distinct(h, (n_tok - 1) * at + d, (n_tok - 1) * bt + d) || distinct(std::gcd(t, h), d, d);
 }
 
 // whether every row of a view is 16-byte aligned (the stride of a single token or head says nothing)
@@ -234,6 +251,10 @@ int hs_rotary_apply(const hs_rotary_t* rot, int32_t type, int32_t d, int32_t n_t
     wide = wide && wide_view(in[i], n_tok, es) && wide_view(out[i], n_tok, es);
     p.v[i] = row_view(in[i], &out[i], hs::VIEW_ROTATE);
   }
+  // threads of different views run in no order
+  if (n_views == 2 && !(apart(out[0], out[1], n_tok, d, es) && apart(out[0], in[1], n_tok, d, es) &&
+                        apart(out[1], in[0], n_tok, d, es)))
+    return named(HS_ERR_INVALID, me, "an output view overlaps the other output or the other input");
   p.n_views = n_views;
   p.d = d;
   p.n_tok = n_tok;
@@ -339,6 +360,8 @@ int hs_paged_append(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
     if (*why) return named(HS_ERR_INVALID, me, why);
     if (k->heads != c.h_kv || v->heads != c.h_kv) return named(HS_ERR_INVALID, me, "k and v must have h_kv heads");
     if (q && q->heads != c.h_q) return named(HS_ERR_INVALID, me, "q must have h_q heads");
+    if (q && !(apart(*q_out, *k, n_tok, c.d, es) && apart(*q_out, *v, n_tok, c.d, es)))
+      return named(HS_ERR_INVALID, me, "q_out overlaps k or v");
     int n = 0;
     if (q) {
       wide = wide && wide_view(*q, n_tok, es) && wide_view(*q_out, n_tok, es);
