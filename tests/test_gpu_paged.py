@@ -937,3 +937,55 @@ def test_outputs_over_another_tensor_are_refused():
     with pytest.raises(HsError):
         c.append(0, ck, out[:, 6:], q=cq, q_out=out)
     assert c.device_error() == 0 and not c.next_lengths.ne(c.lengths).any()
+
+
+def test_gradients_are_not_dropped_silently():
+    torch = T()
+    from tiered_kv_cache_int8_gb300 import Rotary
+    n, h, d = 6, 2, 64
+    R = Rotary(d)
+    g = torch.Generator(device="cuda").manual_seed(13)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    x, y = (torch.randn(n, h, d, generator=g, device="cuda") for _ in range(2))
+    leaf = x.clone().requires_grad_()
+    want = R.apply(pos, x, y)
+    for args, kw in (((leaf,), {}), ((x, leaf), {}), ((leaf, x), {}), ((x,), dict(out=leaf)), ((x, y), dict(out=(torch.empty_like(x), leaf))),
+                     ((leaf * 2,), {}), ((leaf,), dict(stream=torch.cuda.current_stream()))):
+        with pytest.raises(ValueError):
+            R.apply(pos, *args, **kw)
+    assert torch.equal(leaf.detach(), x)
+    with torch.no_grad():
+        assert torch.equal(R.apply(pos, leaf, y)[0], want[0])
+    with torch.inference_mode():
+        z = x.clone()
+        assert torch.equal(R.apply(pos, z, out=z), want[0])
+    assert torch.equal(R.apply(pos, leaf.detach()), want[0])
+
+    class Rotate(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, t):
+            return R.apply(pos, t)
+
+        @staticmethod
+        def backward(ctx, up):
+            return R.apply(pos, up, transpose=True)
+
+    Rotate.apply(leaf).backward(y)
+    assert torch.equal(leaf.grad, R.apply(pos, y, transpose=True))
+    # a tensor that a backward pass still needs, written in place
+    weight = torch.ones_like(x, requires_grad=True)
+    for write in (lambda t: R.apply(pos, t, out=t), lambda t: R.apply(pos, t, x, out=(t, torch.empty_like(x))),
+                  lambda t: R.apply(pos, x, t, out=(torch.empty_like(x), t))):
+        t = y.clone()
+        loss = (t * weight).sum()
+        write(t)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    c, q, k, v, _ = small_step(5)
+    weight = torch.ones_like(q, requires_grad=True)
+    for write in (lambda t: c.append(0, k, v, q=t, q_out=t), lambda t: c.decode(0, q, out=t)):
+        t = q.clone()
+        loss = (t * weight).sum()
+        write(t)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()

@@ -5,6 +5,10 @@ Every step runs in the library's CUDA kernels.  Calls run on the current stream
 of their device, or on ``stream``; a call's own outputs and workspace are
 allocated on that stream.  ``ValueError`` for tensors of a wrong shape, type or
 device, ``HsError`` for what the library refuses.
+
+No call records a gradient: ``append`` and ``decode`` are for serving, what they return
+has none; ``Rotary.apply`` refuses tensors that require one while gradients are recorded.
+Given outputs count as modified in place (a backward pass that saved one says so).
 """
 from __future__ import annotations
 
@@ -58,6 +62,9 @@ def _ints(name: str, x, device, n: int):
 # the current stream's handle, without building the Stream object where torch offers that
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+_grad_on, _modified = torch.is_grad_enabled, torch.autograd.graph.increment_version
 
 
 def _on_stream(stream, device, tensors, call):
@@ -123,6 +130,10 @@ class Rotary:
         out       : the tensor(s) to write: the inputs themselves (in place) or others
         transpose : the transposed rotation (angles negated): what takes a gradient of
                     the rotated values back; the inverse where magnitude is 1
+
+        Records no gradient, and refuses tensors that require one while gradients are
+        recorded: in a model that trains, call it in an autograd function's forward, and
+        transposed in its backward.
         """
         dev, k = self.device, len(xs)
         if stream is not None:
@@ -132,6 +143,8 @@ class Rotary:
         if k != 1 and k != 2:
             raise ValueError("apply takes one or two tensors")
         x0 = xs[0]
+        if _grad_on() and (x0.requires_grad or (k == 2 and xs[1].requires_grad)):
+            raise ValueError("apply records no gradient of its inputs (without one: torch.no_grad(), or detach)")
         dtype, (n, h, d) = x0.dtype, x0.shape if x0.dim() == 3 else (0, 0, 0)
         if dtype not in _ROTATED:
             raise ValueError(f"no rotation of {dtype}")
@@ -144,6 +157,8 @@ class Rotary:
             y0, y1 = (out, None) if isinstance(out, torch.Tensor) else (*out, None)[:2]
             if y0.shape != x0.shape or (y1 is None) != (k == 1):
                 raise ValueError("out must have the shapes of the inputs")
+            if _grad_on() and (y0.requires_grad or (k == 2 and y1.requires_grad)):
+                raise ValueError("apply records no gradient: out must not require one")
             into = _heads("out", y0, dev, dtype)
         if k == 1:
             views, into = _ONE(*views), _ONE(*into)
@@ -165,6 +180,10 @@ class Rotary:
                                    dev.index, _raw_stream(dev.index))
         if rc:
             _check(rc)
+        if out is not None:
+            _modified(y0)
+            if k == 2:
+                _modified(y1)
         return y0 if k == 1 else (y0, y1)
 
 
@@ -318,6 +337,7 @@ class PagedKVCache:
                 ho = _ONE(q_out.data_ptr(), self.h_q * self.d, self.d, self.h_q, 0)
             else:
                 ho = _ONE(*_heads("q_out", q_out, dev, dtype, self.d, self.h_q))
+                _modified(q_out)
         elif q_out is not None:
             raise ValueError("q_out without q")
         rc = lib().hs_paged_append(self._h, layer, n_req, ids, n, offs, self.page_table.data_ptr(),
@@ -347,6 +367,8 @@ class PagedKVCache:
             out = torch.empty((n, self.h_q, self.d), dtype=dtype, device=dev)
         elif out.shape != q.shape or out.dtype != dtype or out.device != dev or not out.is_contiguous():
             raise ValueError("out must be contiguous, of q's shape, type and device")
+        else:
+            _modified(out)
         if return_lse:
             lse = torch.empty((n, self.h_q), dtype=torch.float32, device=dev)
             lse_ptr = lse.data_ptr()
