@@ -349,3 +349,18 @@ def test_paged_append_refuses_queries_over_new_rows(L, what):
     if what != "fine":
         assert "overlaps" in L.hs_last_error(None).decode()
     L.hs_paged_destroy(h)
+
+
+@pytest.mark.parametrize("name", ["pages", "kv_scale", "page_table", "lengths", "next_lengths"])
+def test_the_cache_keeps_its_tensors(name):
+    # the library holds their addresses, or is given them unchecked: another tensor in their place would be misread
+    import torch
+    from tiered_kv_cache_int8_gb300 import PagedKVCache
+    cache = object.__new__(PagedKVCache)
+    cache._h = None
+    held = torch.ones(3, dtype=torch.int32)
+    setattr(cache, "_" + name, held)
+    with pytest.raises(AttributeError):
+        setattr(cache, name, torch.zeros(1, dtype=torch.int64))
+    setattr(cache, name, getattr(cache, name).__iadd__(1))      # as `cache.lengths += 1` does
+    assert getattr(cache, name) is held and held.tolist() == [2, 2, 2]

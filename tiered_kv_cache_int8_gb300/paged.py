@@ -187,6 +187,14 @@ class Rotary:
         return y0 if k == 1 else (y0, y1)
 
 
+def _kept(name: str):
+    """A tensor attribute that is changed in place only."""
+    def put(self, value):
+        if value is not getattr(self, name):     # (what `cache.lengths += 1` puts back is)
+            raise AttributeError(f"{name[1:]} is written in place, not exchanged for another tensor")
+    return property(lambda self: getattr(self, name), put)
+
+
 class PagedKVCache:
     """A paged cache of keys and values in HBM, its append and its one-token attention.
 
@@ -197,6 +205,9 @@ class PagedKVCache:
     lengths    : int32 [max_requests], positions held before the step
     next_lengths : with the tokens that ``append`` stored; ``decode`` attends to these,
                  and ``commit`` makes them the lengths once every layer is through
+
+    These are written in place (``cache.page_table[r] = ids``, ``cache.lengths.copy_(...)``);
+    the tensors themselves stay the cache's.
 
     Calls that write nothing in common may run at once on different streams.
     """
@@ -228,10 +239,10 @@ class PagedKVCache:
         _check(lib().hs_paged_create(ctypes.byref(self.cfg), pages.data_ptr(),
                                      None if kv_scale is None else kv_scale.data_ptr(), self._error.data_ptr(),
                                      ctypes.byref(self._h)))
-        self.pages, self.kv_scale = pages, kv_scale
-        self.page_table = torch.full((max_requests, max_pages), -1, dtype=torch.int32, device=self.device)
-        self.lengths = torch.zeros(max_requests, dtype=torch.int32, device=self.device)
-        self.next_lengths = torch.zeros(max_requests, dtype=torch.int32, device=self.device)
+        self._pages, self._kv_scale = pages, kv_scale
+        self._page_table = torch.full((max_requests, max_pages), -1, dtype=torch.int32, device=self.device)
+        self._lengths = torch.zeros(max_requests, dtype=torch.int32, device=self.device)
+        self._next_lengths = torch.zeros(max_requests, dtype=torch.int32, device=self.device)
         self._ws_bytes = int(lib().hs_paged_workspace_bytes(self._h))
         self._free = list(range(n_pages - 1, -1, -1))
         self._held: dict[int, list[int]] = {}
@@ -255,10 +266,14 @@ class PagedKVCache:
     def __exit__(self, *a):
         self.close()
 
+    # The library and the calls keep to these tensors' addresses: others are not put in their place.
+    pages, kv_scale, page_table, lengths, next_lengths = map(
+        _kept, ("_pages", "_kv_scale", "_page_table", "_lengths", "_next_lengths"))
+
     def _tensors(self):
         """The cache's own tensors that a call uses."""
         table = None if self.rotary is None else self.rotary._table
-        return self.pages, self.page_table, self.lengths, self.next_lengths, self.kv_scale, self._error, table
+        return self._pages, self._page_table, self._lengths, self._next_lengths, self._kv_scale, self._error, table
 
     # -- pages and lengths -------------------------------------------------------
     def reserve(self, req: int, n_positions: int):
@@ -273,28 +288,28 @@ class PagedKVCache:
         if n > len(self._free):
             raise MemoryError(f"{n} pages wanted, {len(self._free)} free")
         new = [self._free.pop() for _ in range(n)]
-        self.page_table[req, len(have):need] = torch.tensor(new, dtype=torch.int32, device=self.device)
+        self._page_table[req, len(have):need] = torch.tensor(new, dtype=torch.int32, device=self.device)
         have.extend(new)
 
     def release(self, req: int):
         """Takes back the pages of ``req``: its table row is cleared and its lengths are 0."""
         _need(0 <= req < self.max_requests, "request out of range")
         self._free.extend(reversed(self._held.pop(req, [])))
-        self.page_table[req] = -1
-        self.lengths[req] = 0
-        self.next_lengths[req] = 0
+        self._page_table[req] = -1
+        self._lengths[req] = 0
+        self._next_lengths[req] = 0
 
     def free_pages(self) -> int:
         return len(self._free)
 
     def set_lengths(self, lengths):
         """Positions held by every request (int32 [max_requests])."""
-        self.lengths.copy_(lengths)
-        self.next_lengths.copy_(lengths)
+        self._lengths.copy_(lengths)
+        self._next_lengths.copy_(lengths)
 
     def commit(self):
         """The step is through every layer: its tokens count as held."""
-        self.lengths.copy_(self.next_lengths)
+        self._lengths.copy_(self._next_lengths)
 
     # -- the path ------------------------------------------------------------------
     def append(self, layer: int, k, v, q=None, q_out=None, req_ids=None, tok_offsets=None, stream=None):
@@ -340,8 +355,8 @@ class PagedKVCache:
                 _modified(q_out)
         elif q_out is not None:
             raise ValueError("q_out without q")
-        rc = lib().hs_paged_append(self._h, layer, n_req, ids, n, offs, self.page_table.data_ptr(),
-                                   self.lengths.data_ptr(), self.next_lengths.data_ptr(), rot, hq, ho, _ONE(*hk),
+        rc = lib().hs_paged_append(self._h, layer, n_req, ids, n, offs, self._page_table.data_ptr(),
+                                   self._lengths.data_ptr(), self._next_lengths.data_ptr(), rot, hq, ho, _ONE(*hk),
                                    _ONE(*hv), _raw_stream(dev.index))
         if rc:
             _check(rc)
@@ -361,7 +376,7 @@ class PagedKVCache:
         hq = _ONE(*_heads("q", q, dev, dtype, self.d, self.h_q))
         n, lse, lse_ptr = q.shape[0], None, None
         ids = None if req_ids is None else _ints("req_ids", req_ids, dev, n)
-        lens = (self.next_lengths.data_ptr() if lengths is None
+        lens = (self._next_lengths.data_ptr() if lengths is None
                 else _ints("lengths", lengths, dev, self.max_requests))
         if out is None:
             out = torch.empty((n, self.h_q, self.d), dtype=dtype, device=dev)
@@ -373,7 +388,7 @@ class PagedKVCache:
             lse = torch.empty((n, self.h_q), dtype=torch.float32, device=dev)
             lse_ptr = lse.data_ptr()
         ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
-        rc = lib().hs_paged_decode(self._h, layer, n, ids, self.page_table.data_ptr(), lens, hq, out.data_ptr(),
+        rc = lib().hs_paged_decode(self._h, layer, n, ids, self._page_table.data_ptr(), lens, hq, out.data_ptr(),
                                    lse_ptr, ws.data_ptr(), _raw_stream(dev.index))
         if rc:
             _check(rc)
