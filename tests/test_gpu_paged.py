@@ -989,3 +989,16 @@ def test_gradients_are_not_dropped_silently():
         write(t)
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             loss.backward()
+
+
+def test_refusals_on_a_given_stream():
+    # the same errors as on the current stream
+    torch = T()
+    c, q, k, v, _ = small_step(6)
+    s = torch.cuda.Stream()
+    for call in (lambda: c.rotary.apply(c.lengths.cpu(), q, stream=s), lambda: c.rotary.apply(c.lengths, q.cpu(), stream=s),
+                 lambda: c.append(0, k.cpu(), v, stream=s), lambda: c.decode(0, q.cpu(), stream=s),
+                 lambda: c.decode(0, q, lengths=c.lengths.cpu(), stream=s.cuda_stream)):
+        with pytest.raises(ValueError):
+            call()
+    assert torch.cuda.current_stream() != s and c.device_error() == 0

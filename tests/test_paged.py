@@ -364,3 +364,12 @@ def test_the_cache_keeps_its_tensors(name):
         setattr(cache, name, torch.zeros(1, dtype=torch.int64))
     setattr(cache, name, getattr(cache, name).__iadd__(1))      # as `cache.lengths += 1` does
     assert getattr(cache, name) is held and held.tolist() == [2, 2, 2]
+
+
+def test_a_stream_of_another_device_is_refused():
+    import types
+    import torch
+    from tiered_kv_cache_int8_gb300 import paged
+    other = types.SimpleNamespace(cuda_stream=0, device=torch.device("cuda", 1))
+    with pytest.raises(ValueError):
+        paged._on_stream(other, torch.device("cuda", 0), (), lambda: pytest.fail("the call was made"))

@@ -72,9 +72,11 @@ def _on_stream(stream, device, tensors, call):
     stream, and the given tensors are marked as used there."""
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, not on {device}")
     if stream.cuda_stream != _raw_stream(device.index):
         for t in tensors:
-            if t is not None:
+            if t is not None and t.device == device:     # (others are refused by the call)
                 t.record_stream(stream)
     with torch.cuda.stream(stream):
         return call()
