@@ -1002,3 +1002,205 @@ def test_refusals_on_a_given_stream():
         with pytest.raises(ValueError):
             call()
     assert torch.cuda.current_stream() != s and c.device_error() == 0
+
+
+# ---- wide tables: the work is shared out evenly and its pieces joined, however short the contexts are ----------
+
+def widened(c, positions=1040):
+    """The same requests over the same pool with a table of at least `positions` positions (its further columns hold -1)."""
+    from tiered_kv_cache_int8_gb300 import PagedKVCache
+    w = PagedKVCache(n_layers=c.n_layers, n_pages=c.n_pages, page_size=c.page_size, max_requests=c.max_requests,
+                     max_pages=max(c.max_pages, -(-positions // c.page_size)), h_q=c.h_q, h_kv=c.h_kv, d=c.d, dtype=c.dtype,
+                     kv_dtype=c.kv_dtype, softmax_scale=c.cfg.softmax_scale, window=c.cfg.window, rotary=c.rotary,
+                     kv_scale=c.kv_scale, pages=c.pages)
+    w.page_table[:, :c.max_pages].copy_(c.page_table)
+    w.set_lengths(c.lengths)
+    return w
+
+
+RAGGED = [(37 * r) % 90 for r in range(150)]
+RAGGED[3], RAGGED[77], RAGGED[149] = 4000, 1500, 1041
+
+
+@pytest.mark.parametrize("lengths", [[1] * 300, list(range(200)), RAGGED, [0] * 128 + [5], [17] * 129, [0, 1, 15, 16, 17, 65, 130]],
+                         ids=["ones", "rising", "ragged", "mostly empty", "alike", "few"])
+@pytest.mark.parametrize("typ, kv, hq, hk, d", [("bf16", "bf16", 6, 2, 64), ("fp16", "e4m3", 8, 1, 128), ("bf16", "bf16", 20, 1, 256),
+                                                ("fp16", "fp16", 3, 3, 64)])
+def test_wide_tables_of_short_contexts(lengths, typ, kv, hq, hk, d):
+    torch = T()
+    c, g = make(len(lengths), hq, hk, d, 16, typ, kv, lengths, seed=len(lengths) + d)
+    c = widened(c)
+    q = torch.randn(len(lengths), hq, d, generator=g, device="cuda").to(dtype(typ))
+    out, lse = check_decode(c, q, lengths)
+    again, lse2 = c.decode(0, q, return_lse=True)
+    assert torch.equal(out, again) and torch.equal(lse, lse2) and c.device_error() == 0
+
+
+@pytest.mark.parametrize("typ, kv", [("bf16", "bf16"), ("fp16", "e4m3")])
+@pytest.mark.parametrize("window", [1009, 1024, 2000])
+def test_wide_tables_with_a_window(typ, kv, window):
+    torch = T()
+    lengths = [0, 1, 17, window - 1, window, window + 1, 5000, 0, 2500, 40]
+    c, g = make(len(lengths), 8, 4, 64, 32, typ, kv, lengths, window=window)
+    q = torch.randn(len(lengths), 8, 64, generator=g, device="cuda").to(dtype(typ))
+    raw = c.pages.view(torch.uint8) if kv == "e4m3" else c.pages
+    for r, n in enumerate(lengths):
+        pos = torch.arange(max(0, n - window), device="cuda")       # not used, whatever they hold
+        raw[0][c.page_table[r][pos // 32].long(), :, :, pos % 32] = 0x7F if kv == "e4m3" else math.nan
+    check_decode(c, q, lengths, window=window)
+    assert c.device_error() == 0
+
+
+def test_wide_tables_skip_bad_requests():
+    torch = T()
+    from tiered_kv_cache_int8_gb300 import hs
+    R = 140                                    # more than a warp looks through by itself
+    lengths = [(53 * r) % 200 for r in range(R)]
+    lengths[7] = 1300
+    c, g = make(R, 4, 2, 64, 16, "bf16", "bf16", lengths, max_requests=R + 1)
+    c = widened(c)
+    for n in (20, R):                          # few requests, many
+        q = torch.randn(n, 4, 64, generator=g, device="cuda").bfloat16()
+        ids = list(range(n))
+        ids[1], ids[n - 2], ids[9] = R + 1, -1, 7
+        c._error.zero_()
+        out, lse = c.decode(0, q, req_ids=torch.tensor(ids, dtype=torch.int32, device="cuda"), return_lse=True)
+        assert c.device_error() == hs.HS_DEVERR_REQ_RANGE
+        bad = [1, n - 2]
+        fine = [i for i in range(n) if i not in bad]
+        assert (out[bad] == 0).all() and (lse[bad] == -math.inf).all()
+        check_decode(c, q[fine].contiguous(), lengths, ids=[ids[i] for i in fine], out=out[fine], lse=lse[fine])
+        # lengths outside the table
+        other = list(lengths) + [0]
+        other[0], other[5] = -3, c.max_pages * 16 + 1
+        c._error.zero_()
+        out, lse = c.decode(0, q, lengths=torch.tensor(other, dtype=torch.int32, device="cuda"), return_lse=True)
+        assert c.device_error() == hs.HS_DEVERR_CAPACITY
+        assert (out[[0, 5]] == 0).all() and (lse[[0, 5]] == -math.inf).all()
+        fine = [i for i in range(n) if i not in (0, 5)]
+        check_decode(c, q[fine].contiguous(), lengths, ids=fine, out=out[fine], lse=lse[fine])
+
+
+@pytest.mark.parametrize("typ, kv, hq, hk", [("bf16", "bf16", 4, 1), ("fp16", "e4m3", 8, 2)])
+def test_bad_pages_over_whole_shares(typ, kv, hq, hk):
+    # pieces in which nothing is attended, alone and joined with others
+    torch = T()
+    from tiered_kv_cache_int8_gb300 import hs
+    lengths = [60000, 30000, 5000, 64]
+    c, g = make(4, hq, hk, 64, 64, typ, kv, lengths)
+    q = torch.randn(4, hq, 64, generator=g, device="cuda").to(dtype(typ))
+    for bad in ([(0, 200, 600)], [(0, 0, 700), (1, 100, 469)], [(0, 1, 938), (1, 0, 469), (2, 0, 79)], [(r, 0, 938) for r in range(4)]):
+        held = c.page_table.clone()
+        for r, a, b in bad:
+            c.page_table[r, a:b] = c.n_pages + 5 if r % 2 else -1
+        c._error.zero_()
+        out, lse = c.decode(0, q, return_lse=True)
+        assert c.device_error() == hs.HS_DEVERR_PAGE
+        for r in range(4):
+            want, wl, tol, tl = plain.attend(q[r], c.pages[0], c.page_table[r], lengths[r], 0, 1 / 8,
+                                             None if c.kv_scale is None else c.kv_scale[0])
+            within(out[r], want, tol, f"out of request {r}")
+            if torch.isinf(wl).all():
+                assert (lse[r] == -math.inf).all() and (out[r] == 0).all()
+            else:
+                within(lse[r], wl, tl, f"lse of request {r}")
+        c.page_table.copy_(held)
+
+
+def test_only_empty_requests_over_a_used_workspace():
+    # the pieces and chains that an earlier call left behind are not taken up
+    import ctypes
+    torch = T()
+    from tiered_kv_cache_int8_gb300 import hs
+    c, g = make(2, 8, 2, 64, 64, "bf16", "bf16", [40000, 3])
+    q = torch.randn(2, 8, 64, generator=g, device="cuda").bfloat16()
+    ws = torch.full((c._ws_bytes,), 0x7F, dtype=torch.uint8, device="cuda")
+    heads = hs.HsHeads(q.data_ptr(), 8 * 64, 64, 8, 0)
+
+    def run(lengths):
+        lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+        out, lse = torch.full_like(q, 7.0), torch.full((2, 8), 7.0, device="cuda")
+        rc = hs.lib().hs_paged_decode(c._h, 0, 2, None, c.page_table.data_ptr(), lens.data_ptr(), ctypes.byref(heads), out.data_ptr(),
+                                      lse.data_ptr(), ws.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        torch.cuda.synchronize()
+        return out, lse
+
+    for lengths in ([40000, 3], [0, 0], [40000, 3], [3, 0], [0, 3], [39999, 0]):
+        out, lse = run(lengths)
+        check_decode(c, q, lengths, out=out, lse=lse)
+    assert c.device_error() == 0
+
+
+@pytest.mark.parametrize("typ, kv", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3"), ("fp16", "e4m3")])
+@pytest.mark.parametrize("wide", [False, True])
+def test_a_row_that_wins_alone(typ, kv, wide):
+    # large scores that are exact in 32 bits (integers below 2^24 under a power of two); the second best is 200 or more
+    # below, so its weight is 0 and the output is the winner's row
+    torch = T()
+    lengths = [1, 2, 17, 100, 500, 1000, 900]
+    at = [0, 1, 16, 0, 499, 480, 16]                     # the winners' positions
+    c, g = make(len(lengths), 4, 2, 64, 64, typ, kv, lengths, scale=0.125)
+    if kv == "e4m3":
+        c.kv_scale.copy_(2.0 ** torch.randint(-6, 3, c.kv_scale.shape, generator=g, device="cuda").float())
+    if wide:
+        c = widened(c)
+    big = 4096.0
+    q = (torch.randint(0, 2, (len(lengths), 4, 64), generator=g, device="cuda") * 2 - 1) * big
+    q[:, 1::2] = q[:, ::2]                               # the heads of a group look for the same row
+    raw = c.pages.view(torch.uint8) if kv == "e4m3" else c.pages
+    bits = (lambda x: x.to(c.kv_dtype).view(torch.uint8)) if kv == "e4m3" else (lambda x: x.to(c.kv_dtype))
+    for r, n in enumerate(lengths):
+        pos = torch.arange(n, device="cuda")
+        for h in range(2):
+            sign = q[r, 2 * h] / big
+            rows = torch.randint(-1, 2, (n, 64), generator=g, device="cuda").float()
+            rows = rows * torch.where(rows * sign > 0, 0.0, 1.0)              # products of 0 or below
+            rows[at[r]] = 3 * sign                                            # 3 * 4096 * 64
+            raw[0][c.page_table[r][pos // 64].long(), 0, h, pos % 64] = bits(rows)
+    out, lse = c.decode(0, q.to(dtype(typ)), return_lse=True)
+    for r, n in enumerate(lengths):
+        kv_row = c.pages[0, c.page_table[r, at[r] // 64].long(), :, :, at[r] % 64].double()      # [2, hk, d]
+        scales = torch.ones(2, 2, dtype=torch.float64, device="cuda") if kv != "e4m3" else c.kv_scale[0].double()
+        v = (kv_row[1] * scales[1][:, None]).repeat_interleave(2, dim=0)
+        if kv == "e4m3":
+            # the winner's weight is rounded to fp16, its share of the sum is not; then products and the output
+            tol = v.abs() * (2.0 ** -11 + 2.0 ** -20)
+            within(out[r], v, tol + plain.HALF_STEP[dtype(typ)] * (v.abs() + tol) + plain.TINY[dtype(typ)], f"out of request {r}")
+        else:
+            # a weight in two parts is off by 2^-16 at most: the row itself is the nearest value
+            assert torch.equal(out[r].double(), v), f"out of request {r}"
+        s = (3 * big * 64 * 0.125 * scales[0])[:, None].expand(2, 2).reshape(4)
+        within(lse[r], s, s * 2.0 ** -21, f"lse of request {r}")
+    assert c.device_error() == 0
+
+
+@pytest.mark.parametrize("width", [1, 66])
+def test_the_most_requests_with_weights_in_two_parts(width):
+    torch = T()
+    from tiered_kv_cache_int8_gb300 import PagedKVCache
+    R, d, page = 4096, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(21)
+    c = PagedKVCache(n_layers=1, n_pages=R, page_size=page, max_requests=R, max_pages=width, h_q=3, h_kv=1, d=d)
+    c.pages.copy_(filled(c.pages.shape, torch.bfloat16, g, False))
+    c.page_table[:, 0] = torch.randperm(R, generator=g, device="cuda").to(torch.int32)
+    lengths = torch.randint(0, page + 1, (R,), generator=g, device="cuda", dtype=torch.int32)
+    c.set_lengths(lengths)
+    q = torch.randn(R, 3, d, generator=g, device="cuda").bfloat16()
+    out, lse = c.decode(0, q, return_lse=True)
+    kv = c.pages[0][c.page_table[:, 0].long(), :, 0].double()               # [R, 2, page, d]
+    seen = torch.arange(page, device="cuda")[None] < lengths[:, None]
+    s = torch.einsum("rhd,rnd->rhn", q.double(), kv[:, 0]) / math.sqrt(d)
+    s = torch.where(seen[:, None], s, -math.inf)
+    p = torch.nan_to_num(torch.softmax(s, -1))
+    want = torch.einsum("rhn,rnd->rhd", p, kv[:, 1])
+    size = torch.einsum("rhn,rnd->rhd", p, kv[:, 1].abs())
+    # as paged_plain.attend has it, for at most 16 positions: a weight in two parts of 2^-8 each
+    dots = torch.einsum("rhd,rnd->rhn", q.double().abs(), kv[:, 0].abs()).amax(-1, keepdim=True) / math.sqrt(d)
+    e_s = (d + 8) * 2.0 ** -23 * dots + 2.0 ** -22 * dots
+    e_p = 2 * e_s + 2.0 ** -20 + (page + 64) * 2.0 ** -23
+    tol = size * (plain.HALF_STEP[q.dtype] ** 2 + e_p) + 2.0 ** -20 * want.abs()
+    within(out, want, tol + plain.HALF_STEP[q.dtype] * (want.abs() + tol) + plain.TINY[q.dtype], "out")
+    some = lengths > 0
+    within(lse[some], torch.logsumexp(s[some], -1), (e_s + 2.0 ** -20 + (page + 64) * 2.0 ** -24)[some, :, 0] + 2.0 ** -20, "lse")
+    assert (lse[~some] == -math.inf).all() and (out[~some] == 0).all() and c.device_error() == 0
