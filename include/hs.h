@@ -530,7 +530,8 @@ void hs_paged_destroy(hs_paged_t* h);
 
 /*
  * hs_paged_append — store new tokens of each request (stream-ordered, capturable).
- *   req_ids     : dev int32 [n_req] distinct request ids, or NULL for 0 .. n_req-1
+ *   req_ids     : dev int32 [n_req] distinct request ids, or NULL for 0 .. n_req-1 (of one
+ *                 that comes twice, what its positions and next length hold is undefined)
  *   n_tok       : rows of q, q_out, k and v
  *   tok_offsets : dev int32 [n_req + 1], or NULL.  Request i of the call takes rows
  *                 tok_offsets[i] .. tok_offsets[i+1]-1 (none where they are equal); rows
@@ -546,7 +547,8 @@ void hs_paged_destroy(hs_paged_t* h);
  *   q, q_out    : views of the step's queries and of their rotated values, or both
  *                 NULL; in place or apart, and q_out apart from k and v, as for
  *                 hs_rotary_apply; needs rot
- *   k, v        : views of the new keys and values (h_kv heads)
+ *   k, v        : views of the new keys and values (h_kv heads), none of them rows of the
+ *                 pool that the call stores
  * The row of token j of request r takes position lengths[r] + j.  `lengths` itself is
  * not changed, so every layer of a step is given the same one, and a call that is
  * repeated rewrites the same rows.  A request with a bad id (HS_DEVERR_REQ_RANGE), a
@@ -573,13 +575,17 @@ int hs_paged_append(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
  *              order, or apart from it
  *   lse      : dev float [n_req][h_q] or NULL: ln sum_n exp(softmax_scale * q_h . K_n)
  *   workspace: dev, hs_paged_workspace_bytes(h) bytes, 256-byte aligned; its contents
- *              matter only within the call: calls that may overlap need one each
+ *              matter only within the call: calls that may overlap need one each.  It and
+ *              lse lie apart from each other and from every other buffer of the call
  * A length of 0 (a padded row of a batch) gives out = 0, lse = -inf.  So does a request
  * with a bad id (HS_DEVERR_REQ_RANGE) or a length outside [0, max_pages * page_size]
  * (HS_DEVERR_CAPACITY).  Positions on a page whose id is out of range are left out
  * (HS_DEVERR_PAGE).  Rows of a page at and behind the length are never used, whatever
  * they hold.  Scores, the softmax and the sums are in 32 bits; the weights that multiply
- * values are held as two numbers of 16 bits (8-bit pages: as one).
+ * values are held as two numbers of 16 bits (8-bit pages: as one, off by up to 2^-11 of
+ * itself).  Weights are at most 2^8 before the division by their sum: values of HS_BF16
+ * pages up to 2^97 in magnitude cannot overflow the sums, larger ones may, up to 2^120 only
+ * where several positions add up.
  * The result does not depend on which page ids hold a request, and is the same bits
  * from call to call.
  */

@@ -8,9 +8,10 @@
 // Bound: HBM.  A row of keys and values serves the h_q / h_kv query heads of its
 // kv head, a few flops per byte, so the time is the cache's bytes; what the design
 // is after is an even share of them for every SM and enough of them in flight.
-// Measured (GB300, copy rate 6.7 TB/s): 16 requests x 32 K positions, 32/8 heads of
-// 128, bf16: 317 us, 6.8 TB/s (tensor pipe 14 % busy); one request of 200 K: 129 us,
-// 6.5 TB/s; 64 of 17 .. 20 K positions, 8-bit pages: 74 us, 5.5 TB/s.  Around the
+// Measured (GB300; a kernel that only reads as many bytes reaches 7.1 to 7.5 TB/s, a copy
+// 6.7): 16 requests x 32 K positions, 32/8 heads of 128, bf16: 318 to 321 us, 6.7 TB/s
+// (the plain read 288 us; tensor pipe 14 % busy); one request of 200 K: 130 us, 6.4 TB/s
+// (114 us); 64 of 17 .. 20 K positions, 8-bit pages: 75 us, 5.5 TB/s (57 us).  Around the
 // stream of rows stand about 10 us: lengths, page ids and the first rows (4 us), the
 // joining of pieces (1 to 3 us) and the second kernel (3 us): all of the 9 us that one
 // request of 4 K positions takes.
@@ -65,6 +66,11 @@ constexpr int RING_BYTES = 192 * 1024;
 // Units of a segment up to which CTAs take whole ones (see above).  Of 32/8 heads of 128, bf16: one
 // request of 512 positions 7.9 us either way, of 1024 11.0 instead of 8.0, but 16 of 1024 15.2 instead of
 // 18.6 and 128 of them 89 instead of 93; through the API every such call takes 12.4 us instead of 16.3.
+// The gain is the call's, not always the GPU's: 33 requests with a window of 1000 (24/8 heads of 64, fp16)
+// take 12.6 us in a graph, shared they took 11.6.  The rule counts units whatever their bytes, asks for
+// MANY_SEGMENTS, which is fewer than the SMs (64 to 127 segments of 33 to 64 units were not measured), and
+// goes by the table's width or the window, as the host does not know the lengths: a window of 1000 passes
+// (64 units with the one it lies across), one of 1024 does not (66).
 constexpr int WHOLE_UNITS = 32, WHOLE_UNITS_MANY = 64, MANY_SEGMENTS = 64;
 
 template <int D, int NT, int QTYPE, bool E4M3>
@@ -405,7 +411,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
       at.n = pre[at.ri + 1] - pre[at.ri];
     }
     Place is = at;                  // the unit whose copy starts next
-    int to_issue = (int)(w1 - w0), to_do = to_issue;   // (2^40 units at the most, over 1000 warps)
+    int to_issue = (int)(w1 - w0), to_do = to_issue;   // (2^40 units at the most, over 608 warps or more: 2^30.8)
     auto step = [&](Place& x) {
       if (++x.u == x.n) {
         x.u = 0;

@@ -129,7 +129,8 @@ class Rotary:
         """Rotates one or two tensors [tokens, heads, d] (a step's queries and keys) of
         the tokens at ``positions`` (int32 [tokens]); returns the rotated tensor(s).
 
-        out       : the tensor(s) to write: the inputs themselves (in place) or others
+        out       : the tensor(s) to write: the inputs themselves (in place) or others, each
+                    apart from the other output and the other input
         transpose : the transposed rotation (angles negated): what takes a gradient of
                     the rotated values back; the inverse where magnitude is 1
 
@@ -208,10 +209,12 @@ class PagedKVCache:
     next_lengths : with the tokens that ``append`` stored; ``decode`` attends to these,
                  and ``commit`` makes them the lengths once every layer is through
 
-    These are written in place (``cache.page_table[r] = ids``, ``cache.lengths.copy_(...)``);
-    the tensors themselves stay the cache's.
+    These are written in place (``cache.page_table[r] = ids``); the tensors themselves stay
+    the cache's.  Lengths are set by ``set_lengths``: what ``decode`` and ``commit`` take are
+    the next ones.
 
-    Calls that write nothing in common may run at once on different streams.
+    Calls that write nothing in common may run at once on different streams (appends of one
+    step to different layers too: the next lengths they write are the same).
     """
 
     def __init__(self, *, n_layers: int, n_pages: int, page_size: int, max_requests: int, max_pages: int, h_q: int,
@@ -305,7 +308,7 @@ class PagedKVCache:
         return len(self._free)
 
     def set_lengths(self, lengths):
-        """Positions held by every request (int32 [max_requests])."""
+        """Positions held by every request (int32 [max_requests]): its lengths and its next ones."""
         self._lengths.copy_(lengths)
         self._next_lengths.copy_(lengths)
 
@@ -324,6 +327,8 @@ class PagedKVCache:
                       rows outside belong to nobody (their rows of a new q_out are undefined).
                       None: one row per request (with req_ids: the same number for each)
         req_ids     : int32 [requests] distinct ids; None: requests 0, 1, ...
+
+        q_out lies apart from k and v; k, v and q may be slices of one projection.
         """
         dev, dtype = self.device, self.dtype
         if stream is not None:
@@ -368,6 +373,7 @@ class PagedKVCache:
         """Attention of one token per request: q [requests, h_q, d] -> out of its shape
         (and, with return_lse, the float32 [requests, h_q] logarithms of the softmax sums).
 
+        q       : its rows 16-byte aligned; at most max_requests of them
         lengths : int32 [max_requests], positions attended to; None: next_lengths
         out     : where to write (q itself, if it is contiguous: in place)
         """
