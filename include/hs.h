@@ -568,7 +568,7 @@ int hs_paged_append(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
  * (stream-ordered, capturable): with N = lengths[r] and the last min(N, window) positions,
  *   o_h = sum_n softmax_n(softmax_scale * q_h . K_n) V_n,   kv head floor(h * h_kv / h_q).
  *   req_ids  : dev int32 [n_req] request ids (the same one may come twice), or NULL for
- *              0 .. n_req-1
+ *              0 .. n_req-1;  n_req is at most max_requests
  *   lengths  : dev int32 [max_requests], the new token's own position counted
  *   q        : view of [n_req][h_q][d], 16-byte aligned rows
  *   out      : dev [n_req][h_q][d] (type), 16-byte aligned; q's own memory in the same

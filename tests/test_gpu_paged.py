@@ -1204,3 +1204,19 @@ def test_the_most_requests_with_weights_in_two_parts(width):
     some = lengths > 0
     within(lse[some], torch.logsumexp(s[some], -1), (e_s + 2.0 ** -20 + (page + 64) * 2.0 ** -24)[some, :, 0] + 2.0 ** -20, "lse")
     assert (lse[~some] == -math.inf).all() and (out[~some] == 0).all() and c.device_error() == 0
+
+
+def test_rotary_takes_an_output_for_each_input():
+    torch = T()
+    from tiered_kv_cache_int8_gb300 import Rotary
+    R = Rotary(64)
+    pos = torch.arange(4, dtype=torch.int32, device="cuda")
+    x, y = (torch.randn(4, 2, 64, device="cuda") for _ in range(2))
+    a, b, c = (torch.full_like(x, 7.0) for _ in range(3))
+    for args, out in (((x, y), (a, b, c)), ((x, y), (a,)), ((x, y), a), ((x,), (a, b)), ((x,), ()), ((x, y), ())):
+        with pytest.raises(ValueError):
+            R.apply(pos, *args, out=out)
+    assert (a == 7.0).all() and (b == 7.0).all()
+    assert R.apply(pos, x, out=(a,)) is a and torch.equal(a, R.apply(pos, x))
+    got = R.apply(pos, x, y, out=[b, c])
+    assert got[0] is b and got[1] is c and torch.equal(c, R.apply(pos, y))

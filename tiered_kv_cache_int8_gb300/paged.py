@@ -157,9 +157,10 @@ class Rotary:
             y0 = torch.empty((n, h, d), dtype=dtype, device=dev)
             into = (y0.data_ptr(), h * d, d, h, 0)
         else:
-            y0, y1 = (out, None) if isinstance(out, torch.Tensor) else (*out, None)[:2]
-            if y0.shape != x0.shape or (y1 is None) != (k == 1):
-                raise ValueError("out must have the shapes of the inputs")
+            ys = (out,) if isinstance(out, torch.Tensor) else tuple(out)
+            if len(ys) != k or ys[0].shape != x0.shape:
+                raise ValueError("out must be a tensor for each input, of its shape")
+            y0, y1 = ys if k == 2 else (*ys, None)
             if _grad_on() and (y0.requires_grad or (k == 2 and y1.requires_grad)):
                 raise ValueError("apply records no gradient: out must not require one")
             into = _heads("out", y0, dev, dtype)
