@@ -409,6 +409,7 @@ int hs_indexer_topk_static_error(int32_t device, uint32_t* out);
 #define HS_FP16 1
 #define HS_FP32 2   /* hs_rotary_apply only */
 #define HS_E4M3 3 /* 8-bit e4m3 pages, with one scale per kv head */
+#define HS_INT4 4 /* 4-bit pages, with a scale per 16 elements of a row and one per kv head */
 
 /* A [tokens][heads][d] view of 16- or 32-bit elements: element (t, h, i) is at
  * data + t * token_stride + h * head_stride + i (strides in elements, in [0, 2^40], the last
@@ -493,9 +494,20 @@ int hs_rotary_apply(const hs_rotary_t* rot, int32_t type, int32_t d, int32_t n_t
  * n of request r is row n % page_size of page page_table[r][n / page_size].
  * The page size must be 16, 32, 64, 128 or 256; d 64, 128 or 256 (keys and values
  * alike); h_q % h_kv == 0.  Queries, new keys and values and outputs are `type`
- * (HS_BF16 or HS_FP16); pages are the same type or HS_E4M3: then they hold
+ * (HS_BF16 or HS_FP16); pages are the same type, HS_E4M3 or HS_INT4.  HS_E4M3 pages hold
  * value * (1 / kv_scale[layer][0 key, 1 value][kv head]) in 32 bits, rounded once and
  * saturated to +-448.
+ *
+ * HS_INT4 pages hold x = value * (1 / kv_scale) in 4-bit codes: 16 elements b of a row (16 b
+ * .. 16 b + 15) share an e4m3 scale s = max |x| / 7 (rounded to nearest, at most 448), and an
+ * element's code is round(x / s) + 8 (ties to even, the rounded quotient in [-7, 7]; 8 where s
+ * is 0), so that a row stands for (code - 8) * s * kv_scale.  A NaN makes its 16 elements NaN;
+ * infinities saturate, as s does beyond 448 * 7 * kv_scale; 16 elements all below 2^-10 * 7 *
+ * kv_scale become 0.  A layer's pages are bytes [n_pages][2][h_kv][page_size / 16][9 d], the 9 d
+ * of 16 positions i of a head being
+ *   keys  : codes [i][d / 2], then scales [i][d / 16]
+ *   values: codes [d / 32][i][16], then scales [d / 16][i]
+ * with the even element of two in the low half of its byte.
  */
 typedef struct hs_paged_config {
   int32_t n_layers;
@@ -519,14 +531,24 @@ typedef struct hs_paged hs_paged_t;
 /*
  * hs_paged_create — check `cfg` and describe the caller's pool.  Allocates nothing on
  * the device: every buffer is the caller's until hs_paged_destroy (NULL is a no-op).
- *   pages     : dev [n_layers][n_pages][2][h_kv][page_size][d], 16-byte aligned; what it
- *               holds is not read here
- *   kv_scale  : dev float [n_layers][2][h_kv], positive; HS_E4M3 pages only (else NULL)
+ *   pages     : dev [n_layers][n_pages][2][h_kv][page_size][d] (HS_INT4: as bytes, above), 16-byte
+ *               aligned; what it holds is not read here
+ *   kv_scale  : dev float [n_layers][2][h_kv], positive; HS_E4M3 and HS_INT4 pages only (else NULL)
  *   error_word: dev uint32, zeroed by the caller: the calls set HS_DEVERR_* bits in it
  */
 int hs_paged_create(const hs_paged_config_t* cfg, void* pages, const float* kv_scale, uint32_t* error_word,
                     hs_paged_t** out);
 void hs_paged_destroy(hs_paged_t* h);
+
+/*
+ * hs_paged_set_scores — how hs_paged_decode and hs_paged_attend make a query's scores, from the
+ * handle's next call on (host memory only; not while another thread uses the handle).  Without it,
+ * and with 0 and NULL, a score is s = softmax_scale * q_h . K_n; else
+ *   softcap : 0 (none), or in [1e-4, 1e6]:  s becomes softcap * tanh(s / softcap)
+ *   slopes  : NULL, or dev float [h_q], finite, the caller's until the handle is destroyed or given
+ *             others:  s then loses slopes[h] * |p - n|, p the query's position
+ */
+int hs_paged_set_scores(hs_paged_t* h, float softcap, const float* slopes);
 
 /*
  * hs_paged_append — store new tokens of each request (stream-ordered, capturable).
@@ -593,6 +615,49 @@ int64_t hs_paged_workspace_bytes(const hs_paged_t* h);
 int hs_paged_decode(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* req_ids, const int32_t* page_table,
                     const int32_t* lengths, const hs_heads_t* q, void* out, float* lse, void* workspace,
                     void* stream);
+
+/*
+ * hs_paged_attend — attention of a call's new tokens over their requests' cached positions:
+ * prompts, chunks of them, drafted tokens (stream-ordered, capturable).  Called after the append
+ * of the same tokens, with the same req_ids, n_tok, tok_offsets, page_table and lengths: token j of
+ * request r is at position p = lengths[r] + j, of N = lengths[r] + its new tokens, and attends to
+ *   max(0, p - window + 1) <= n < max(p + 1, min(prefix[r], N))        (window 0: from 0)
+ * with the scores of hs_paged_set_scores.
+ *   req_ids, n_tok, tok_offsets, page_table, lengths: as for hs_paged_append
+ *   prefix   : dev int32 [max_requests] or NULL (none): positions that all tokens see, those
+ *              before them too
+ *   q        : view of [n_tok][h_q][d], 16-byte aligned rows
+ *   out      : dev [n_tok][h_q][d] (type), 16-byte aligned; q's own memory in the same order, or
+ *              apart from it
+ *   lse      : dev float [n_tok][h_q] or NULL, as for hs_paged_decode
+ *   workspace: dev, hs_paged_attend_workspace_bytes(h) bytes, as for hs_paged_decode
+ * Rows before the first and from the last offset on belong to no request: neither their out nor
+ * their lse is written.  A request with a bad id (HS_DEVERR_REQ_RANGE), or with a length below 0 or
+ * tokens past max_pages * page_size (HS_DEVERR_CAPACITY), gives out = 0, lse = -inf.  Positions on a
+ * page whose id is out of range are left out (HS_DEVERR_PAGE).  Offsets that decrease or leave
+ * [0, n_tok] (HS_DEVERR_OFFSETS) give their request no tokens.  n_tok * h_q / h_kv is below
+ * 2^31 - 2^16.
+ */
+int64_t hs_paged_attend_workspace_bytes(const hs_paged_t* h);
+int hs_paged_attend(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* req_ids, int32_t n_tok,
+                    const int32_t* tok_offsets, const int32_t* page_table, const int32_t* lengths, const int32_t* prefix,
+                    const hs_heads_t* q, void* out, float* lse, void* workspace, void* stream);
+
+/*
+ * hs_paged_read — rows of the cache as values of `type` (stream-ordered, capturable), for instance
+ * to hand a request to the two-tier cache: out's row t is [2][h_kv][d], the keys (rotated, as they
+ * are stored) and then the values of one position, the row layout of hs_append.
+ *   req_ids, n_tok, tok_offsets, page_table: as for hs_paged_append
+ *   starts : dev int32 [max_requests]: row j of request r is its position starts[r] + j
+ *   out    : dev [n_tok] rows of 2 * h_kv * d elements, token_stride apart, 16-byte aligned
+ * 8-bit and 4-bit rows are the product of code and scales in 32 bits, rounded once.  What a
+ * position holds that no append has stored is undefined.  Rows of no request are not written; those
+ * of a request with a bad id, a start below 0 or positions past max_pages * page_size, and of
+ * positions whose page id is out of range, are 0 (with the error bits of hs_paged_append).
+ */
+int hs_paged_read(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* req_ids, int32_t n_tok,
+                  const int32_t* tok_offsets, const int32_t* page_table, const int32_t* starts, void* out,
+                  int64_t token_stride, void* stream);
 
 /* hs_paged_error — synchronise the device and read the handle's error word
  * (HS_DEVERR_* bits since the caller zeroed it).  HS_ERR_DEVICE (with *out set)

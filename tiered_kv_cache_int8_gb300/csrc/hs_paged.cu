@@ -160,7 +160,8 @@ const char* check_paged(const hs_paged_config_t& c) {
   if (c.h_kv < 1 || c.h_kv > 1024) return "h_kv must be in [1, 1024]";
   if (c.h_q < c.h_kv || c.h_q > 4096 || c.h_q % c.h_kv) return "h_q must be a multiple of h_kv, at most 4096";
   if (c.type != HS_BF16 && c.type != HS_FP16) return "type must be HS_BF16 or HS_FP16";
-  if (c.page_type != c.type && c.page_type != HS_E4M3) return "page_type must be type or HS_E4M3";
+  if (c.page_type != c.type && c.page_type != HS_E4M3 && c.page_type != HS_INT4)
+    return "page_type must be type, HS_E4M3 or HS_INT4";
   if (c.window < 0) return "window must be >= 0";
   if (!(c.softmax_scale >= 0.f) || !std::isfinite(c.softmax_scale)) return "softmax_scale must be finite and >= 0";
   // rows of a layer are addressed with 31 bits
@@ -170,7 +171,52 @@ const char* check_paged(const hs_paged_config_t& c) {
 }
 
 size_t layer_bytes(const hs_paged_config_t& c) {
-  return (size_t)c.n_pages * 2 * c.h_kv * c.page_size * c.d * hs::type_bytes(c.page_type);
+  return (size_t)c.n_pages * 2 * c.h_kv * (c.page_size / hs::PG_UNIT) * hs::unit_bytes(c.d, c.page_type);
+}
+
+// The rows of a call on the paged cache: "" or why its arguments cannot be used.
+const char* check_rows(const hs_paged_config_t& c, int32_t layer, int32_t n_req, int32_t n_tok, const int32_t* tok_offsets) {
+  if (layer < 0 || layer >= c.n_layers) return "layer out of range";
+  if (n_req < 0 || n_req > c.max_requests) return "n_req out of range";
+  if (n_tok < 0) return "n_tok < 0";
+  if (n_req > 0 && !tok_offsets && n_tok % n_req) return "without tok_offsets, n_tok must be a multiple of n_req";
+  return "";
+}
+bool odd_ints(const int32_t* a, const int32_t* b, const int32_t* c, const int32_t* d, const void* e = nullptr) {
+  return (reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(c) |
+          reinterpret_cast<uintptr_t>(d) | reinterpret_cast<uintptr_t>(e)) % 4 != 0;
+}
+
+// what a place in the cache is found with (hs_paged_place.cuh)
+void set_place(hs::RotateParams& p, const hs_paged* h, int32_t layer, int32_t n_req, const int32_t* req_ids, int32_t n_tok,
+               const int32_t* tok_offsets, const int32_t* page_table, const int32_t* lengths) {
+  const hs_paged_config_t& c = h->cfg;
+  p.d = c.d;
+  p.n_tok = n_tok;
+  p.req_ids = req_ids;
+  p.tok_offsets = tok_offsets;
+  p.page_table = page_table;
+  p.lengths = lengths;
+  p.n_req = n_req;
+  p.tok_per_req = tok_offsets ? 0 : n_tok / n_req;
+  p.max_requests = c.max_requests;
+  p.max_pages = c.max_pages;
+  p.n_pages = c.n_pages;
+  p.page_size = c.page_size;
+  p.page_shift = h->page_shift;
+  p.h_kv = c.h_kv;
+  p.pages = static_cast<unsigned char*>(h->pages) + layer_bytes(c) * layer;
+  p.kv_scale = h->kv_scale ? h->kv_scale + (size_t)layer * 2 * c.h_kv : nullptr;
+  p.dev_error = h->dev_error;
+}
+
+// how scores are made: for hs::PagedDecodeParams and hs::PagedAttendParams
+template <typename P>
+void set_scores(P& p, const hs_paged* h) {
+  p.scale_log2 = h->scale_log2;
+  p.cap_in = h->softcap > 0.f ? h->scale / h->softcap : 0.f;
+  p.cap_log2 = h->softcap * 1.4426950408889634f;
+  p.slopes = h->slopes;
 }
 
 }  // namespace
@@ -278,8 +324,8 @@ int hs_paged_create(const hs_paged_config_t* cfg, void* pages, const float* kv_s
   if (const char* why = check_paged(*cfg); *why) return named(HS_ERR_CONFIG, me, why);
   if (!pages || reinterpret_cast<uintptr_t>(pages) % 16)
     return named(HS_ERR_INVALID, me, "pages must be 16-byte aligned and not null");
-  if ((cfg->page_type == HS_E4M3) != (kv_scale != nullptr))
-    return named(HS_ERR_INVALID, me, "kv_scale goes with HS_E4M3 pages, and with them only");
+  if ((cfg->page_type == HS_E4M3 || cfg->page_type == HS_INT4) != (kv_scale != nullptr))
+    return named(HS_ERR_INVALID, me, "kv_scale goes with HS_E4M3 and HS_INT4 pages, and with them only");
   if (reinterpret_cast<uintptr_t>(kv_scale) % 4) return named(HS_ERR_INVALID, me, "kv_scale must be 4-byte aligned");
   if (!error_word || reinterpret_cast<uintptr_t>(error_word) % 4)
     return named(HS_ERR_INVALID, me, "error_word must be 4-byte aligned and not null");
@@ -290,6 +336,7 @@ int hs_paged_create(const hs_paged_config_t* cfg, void* pages, const float* kv_s
   h->kv_scale = kv_scale;
   while ((1 << h->page_shift) < cfg->page_size) ++h->page_shift;
   const float scale = cfg->softmax_scale > 0.f ? cfg->softmax_scale : 1.0f / std::sqrt((float)cfg->d);
+  h->scale = scale;
   h->scale_log2 = scale * 1.4426950408889634f;
   h->dev_error = error_word;
   // a handle is host memory only: without a device the calls' checks still run
@@ -310,8 +357,10 @@ int hs_paged_create(const hs_paged_config_t* cfg, void* pages, const float* kv_s
     // the kernels are loaded here, so that a first call may be a captured one
     DeviceScope dev(cfg->device);
     cudaError_t e = dev.err;
-    if (e == cudaSuccess) e = hs::prepare_paged(cfg->d, cfg->h_q / cfg->h_kv, cfg->type, cfg->page_type);
-    if (e == cudaSuccess) e = hs::prepare_rotate(cfg->type, cfg->page_type, true);
+    if (e == cudaSuccess) e = hs::prepare_paged(cfg->d, cfg->h_q / cfg->h_kv, cfg->type, cfg->page_type, false);
+    if (e == cudaSuccess) e = hs::prepare_attend(cfg->d, cfg->type, cfg->page_type);
+    if (e == cudaSuccess) e = hs::prepare_rows(cfg->d, cfg->type, cfg->page_type);
+    if (e == cudaSuccess && cfg->page_type != HS_INT4) e = hs::prepare_rotate(cfg->type, cfg->page_type, true);
     if (e != cudaSuccess) {
       delete h;
       return fail_cuda(e, "hs_paged_create: kernel set-up");
@@ -323,6 +372,26 @@ int hs_paged_create(const hs_paged_config_t* cfg, void* pages, const float* kv_s
 
 void hs_paged_destroy(hs_paged_t* h) { delete h; }
 
+int hs_paged_set_scores(hs_paged_t* h, float softcap, const float* slopes) {
+  static const char* me = "hs_paged_set_scores";
+  if (!h) return named(HS_ERR_INVALID, me, "null handle");
+  if (!(softcap >= 0.f) || !std::isfinite(softcap)) return named(HS_ERR_CONFIG, me, "softcap must be finite and >= 0");
+  // (its share of the scores, and its own powers of two, are held in 32 bits)
+  if (softcap > 0.f && (softcap < 1e-4f || softcap > 1e6f))
+    return named(HS_ERR_CONFIG, me, "softcap must be 0 or in [1e-4, 1e6]");
+  if (reinterpret_cast<uintptr_t>(slopes) % 4) return named(HS_ERR_INVALID, me, "slopes must be 4-byte aligned");
+  if (h->ctas > 0 && (softcap > 0.f || slopes)) {
+    const hs_paged_config_t& c = h->cfg;
+    DeviceScope dev(c.device);
+    cudaError_t e = dev.err;
+    if (e == cudaSuccess) e = hs::prepare_paged(c.d, c.h_q / c.h_kv, c.type, c.page_type, true);
+    if (e != cudaSuccess) return fail_cuda(e, "hs_paged_set_scores: kernel set-up");
+  }
+  h->softcap = softcap;
+  h->slopes = slopes;
+  return HS_OK;
+}
+
 int hs_paged_append(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* req_ids, int32_t n_tok,
                     const int32_t* tok_offsets, const int32_t* page_table, const int32_t* lengths,
                     int32_t* next_lengths, const hs_rotary_t* rot, const hs_heads_t* q, const hs_heads_t* q_out,
@@ -330,16 +399,10 @@ int hs_paged_append(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
   static const char* me = "hs_paged_append";
   if (!h) return named(HS_ERR_INVALID, me, "null handle");
   const hs_paged_config_t& c = h->cfg;
-  if (layer < 0 || layer >= c.n_layers) return named(HS_ERR_INVALID, me, "layer out of range");
-  if (n_req < 0 || n_req > c.max_requests) return named(HS_ERR_INVALID, me, "n_req out of range");
-  if (n_tok < 0) return named(HS_ERR_INVALID, me, "n_tok < 0");
+  if (const char* why = check_rows(c, layer, n_req, n_tok, tok_offsets); *why) return named(HS_ERR_INVALID, me, why);
   if (n_req == 0) return HS_OK;
-  if (!tok_offsets && n_tok % n_req)
-    return named(HS_ERR_INVALID, me, "without tok_offsets, n_tok must be a multiple of n_req");
   if (!page_table || !lengths) return named(HS_ERR_INVALID, me, "null page_table or lengths");
-  if (((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(lengths) |
-        reinterpret_cast<uintptr_t>(next_lengths) | reinterpret_cast<uintptr_t>(req_ids) |
-        reinterpret_cast<uintptr_t>(tok_offsets)) % 4) != 0)
+  if (odd_ints(page_table, lengths, next_lengths, req_ids, tok_offsets))
     return named(HS_ERR_INVALID, me, "an int32 array is not 4-byte aligned");
   if (next_lengths && next_lengths < lengths + c.max_requests && lengths < next_lengths + c.max_requests)
     return named(HS_ERR_INVALID, me, "next_lengths overlaps lengths");
@@ -351,7 +414,8 @@ int hs_paged_append(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
   }
   const size_t es = hs::type_bytes(c.type);
   hs::RotateParams p = {};
-  bool wide = wide_rotary(rot, c.d, es);
+  const bool four = c.page_type == HS_INT4;        // (its kernel turns elements one by one)
+  bool wide = four || wide_rotary(rot, c.d, es);
   if (n_tok > 0) {
     if (!k || !v) return named(HS_ERR_INVALID, me, "null k or v");
     const char* why = check_view(*k, n_tok, c.d, es, false);
@@ -372,35 +436,48 @@ int hs_paged_append(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
     p.v[n++] = row_view(*v, nullptr, hs::VIEW_VALUES);
     p.n_views = n;
   }
-  p.d = c.d;
-  p.n_tok = n_tok;
   if (rot) {
     p.rot_dim = rot->rot_dim;
     p.magnitude = rot->magnitude;
     p.sign = 1.f;
     p.turns = rot->turns;
   }
-  p.req_ids = req_ids;
-  p.tok_offsets = tok_offsets;
-  p.page_table = page_table;
-  p.lengths = lengths;
+  set_place(p, h, layer, n_req, req_ids, n_tok, tok_offsets, page_table, lengths);
   p.next_lengths = next_lengths;
-  p.n_req = n_req;
-  p.tok_per_req = tok_offsets ? 0 : n_tok / n_req;
-  p.max_requests = c.max_requests;
-  p.max_pages = c.max_pages;
-  p.n_pages = c.n_pages;
-  p.page_size = c.page_size;
-  p.page_shift = h->page_shift;
-  p.h_kv = c.h_kv;
-  p.pages = static_cast<unsigned char*>(h->pages) + layer_bytes(c) * layer;
-  p.kv_scale = h->kv_scale ? h->kv_scale + (size_t)layer * 2 * c.h_kv : nullptr;
-  p.dev_error = h->dev_error;
   DeviceScope dev(c.device);
   if (dev.err != cudaSuccess) return fail_cuda(dev.err, "hs_paged_append: device");
-  const cudaError_t e = hs::launch_rotate(p, c.type, c.page_type, true, rot && rot->interleaved, wide,
-                                          static_cast<cudaStream_t>(stream));
+  const bool interleaved = rot && rot->interleaved;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = four ? hs::launch_append4(p, c.type, interleaved, wide, st)
+                             : hs::launch_rotate(p, c.type, c.page_type, true, interleaved, wide, st);
   return e == cudaSuccess ? HS_OK : fail_cuda(e, "hs_paged_append: launch");
+}
+
+int hs_paged_read(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* req_ids, int32_t n_tok,
+                  const int32_t* tok_offsets, const int32_t* page_table, const int32_t* starts, void* out,
+                  int64_t token_stride, void* stream) {
+  static const char* me = "hs_paged_read";
+  if (!h) return named(HS_ERR_INVALID, me, "null handle");
+  const hs_paged_config_t& c = h->cfg;
+  if (const char* why = check_rows(c, layer, n_req, n_tok, tok_offsets); *why) return named(HS_ERR_INVALID, me, why);
+  if (n_req == 0 || n_tok == 0) return HS_OK;
+  if (!page_table || !starts || !out) return named(HS_ERR_INVALID, me, "null argument");
+  if (odd_ints(page_table, starts, req_ids, tok_offsets))
+    return named(HS_ERR_INVALID, me, "an int32 array is not 4-byte aligned");
+  const int64_t row = (int64_t)2 * c.h_kv * c.d;
+  if (reinterpret_cast<uintptr_t>(out) % 16 || token_stride % 8)
+    return named(HS_ERR_INVALID, me, "out's rows must be 16-byte aligned");
+  if (n_tok > 1 && (token_stride < row || token_stride > ((int64_t)1 << 40) || n_tok - 1 > ((int64_t)1 << 46) / token_stride))
+    return named(HS_ERR_INVALID, me, "out's rows must not overlap, and end within 2^46 elements");
+  hs::RotateParams p = {};
+  set_place(p, h, layer, n_req, req_ids, n_tok, tok_offsets, page_table, starts);
+  p.v[0].out = out;
+  p.v[0].out_ts = token_stride;
+  p.v[0].heads = 2 * c.h_kv;
+  DeviceScope dev(c.device);
+  if (dev.err != cudaSuccess) return fail_cuda(dev.err, "hs_paged_read: device");
+  const cudaError_t e = hs::launch_read(p, c.type, c.page_type, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? HS_OK : fail_cuda(e, "hs_paged_read: launch");
 }
 
 int64_t hs_paged_workspace_bytes(const hs_paged_t* h) {
@@ -456,12 +533,78 @@ int hs_paged_decode(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
   p.type = c.type;
   p.page_type = c.page_type;
   p.grid = h->ctas;
-  p.scale_log2 = h->scale_log2;
+  set_scores(p, h);
   DeviceScope dev(c.device);
   if (dev.err != cudaSuccess) return fail_cuda(dev.err, "hs_paged_decode: device");
   if (h->ctas < 1) return named(HS_ERR_CUDA, me, "the handle was created without its device");
   const cudaError_t e = hs::launch_paged_decode(p, h->maps[layer], static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? HS_OK : fail_cuda(e, "hs_paged_decode: launch");
+}
+
+int64_t hs_paged_attend_workspace_bytes(const hs_paged_t* h) {
+  return h ? hs::attend_workspace_bytes(h->cfg.d, h->ctas) : 0;
+}
+
+int hs_paged_attend(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* req_ids, int32_t n_tok,
+                    const int32_t* tok_offsets, const int32_t* page_table, const int32_t* lengths, const int32_t* prefix,
+                    const hs_heads_t* q, void* out, float* lse, void* workspace, void* stream) {
+  static const char* me = "hs_paged_attend";
+  if (!h) return named(HS_ERR_INVALID, me, "null handle");
+  const hs_paged_config_t& c = h->cfg;
+  if (const char* why = check_rows(c, layer, n_req, n_tok, tok_offsets); *why) return named(HS_ERR_INVALID, me, why);
+  if (n_req == 0 || n_tok == 0) return HS_OK;
+  if (!page_table || !lengths || !q || !out || !workspace) return named(HS_ERR_INVALID, me, "null argument");
+  if (odd_ints(page_table, lengths, req_ids, tok_offsets, lse) || reinterpret_cast<uintptr_t>(prefix) % 4)
+    return named(HS_ERR_INVALID, me, "an int32 or float array is not 4-byte aligned");
+  if (reinterpret_cast<uintptr_t>(out) % 16) return named(HS_ERR_INVALID, me, "out must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return named(HS_ERR_INVALID, me, "workspace must be 256-byte aligned");
+  const size_t es = hs::type_bytes(c.type);
+  if (const char* why = check_view(*q, n_tok, c.d, es, false); *why) return named(HS_ERR_INVALID, me, why);
+  if (q->heads != c.h_q) return named(HS_ERR_INVALID, me, "q must have h_q heads");
+  if (!wide_view(*q, n_tok, es)) return named(HS_ERR_INVALID, me, "q's rows must be 16-byte aligned");
+  hs_heads_t o = {out, (int64_t)c.h_q * c.d, c.d, c.h_q, 0};
+  if (!same_view(*q, o, n_tok) && !apart(*q, o, n_tok, c.d, es))
+    return named(HS_ERR_INVALID, me, "out overlaps q without being the same memory in the same order");
+  // rows of a kv head's group are counted with 31 bits
+  if ((long long)n_tok * (c.h_q / c.h_kv) > 0x7fff0000LL)
+    return named(HS_ERR_INVALID, me, "n_tok * h_q / h_kv must be below 2^31 - 2^16");
+  hs::PagedAttendParams p = {};
+  p.req_ids = req_ids;
+  p.tok_offsets = tok_offsets;
+  p.page_table = page_table;
+  p.lengths = lengths;
+  p.prefix = prefix;
+  p.q = q->data;
+  p.q_ts = q->token_stride;
+  p.q_hs = q->head_stride;
+  p.out = out;
+  p.lse = lse;
+  p.ws = static_cast<float*>(workspace);
+  p.pages = static_cast<const unsigned char*>(h->pages) + layer_bytes(c) * layer;
+  p.kv_scale = h->kv_scale ? h->kv_scale + (size_t)layer * 2 * c.h_kv : nullptr;
+  p.dev_error = h->dev_error;
+  p.n_req = n_req;
+  p.n_tok = n_tok;
+  p.tok_per_req = tok_offsets ? 0 : n_tok / n_req;
+  p.max_requests = c.max_requests;
+  p.max_pages = c.max_pages;
+  p.n_pages = c.n_pages;
+  p.page_size = c.page_size;
+  p.page_shift = h->page_shift;
+  p.h_q = c.h_q;
+  p.h_kv = c.h_kv;
+  p.group = c.h_q / c.h_kv;
+  p.d = c.d;
+  p.window = c.window;
+  p.type = c.type;
+  p.page_type = c.page_type;
+  p.grid = h->ctas;
+  set_scores(p, h);
+  DeviceScope dev(c.device);
+  if (dev.err != cudaSuccess) return fail_cuda(dev.err, "hs_paged_attend: device");
+  if (h->ctas < 1) return named(HS_ERR_CUDA, me, "the handle was created without its device");
+  const cudaError_t e = hs::launch_paged_attend(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? HS_OK : fail_cuda(e, "hs_paged_attend: launch");
 }
 
 int hs_paged_error(hs_paged_t* h, uint32_t* out) {

@@ -4,13 +4,6 @@
 
 namespace hs {
 
-cudaError_t paged_decode_d64(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st);
-cudaError_t paged_decode_d128(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st);
-cudaError_t paged_decode_d256(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st);
-cudaError_t prepare_paged_d64(int group, int type, int page_type);
-cudaError_t prepare_paged_d128(int group, int type, int page_type);
-cudaError_t prepare_paged_d256(int group, int type, int page_type);
-
 namespace {
 
 using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -52,31 +45,38 @@ bool pool_map(const hs_paged_config_t& p, void* pages, CUtensorMap* map) {
 
 }  // namespace
 
+// f(head width, kind of page) as constants
+template <typename F>
+auto by_pages(int d, int page_type, F f) {
+  auto with = [&](auto dd) {
+    const Pages k = pages_kind(page_type);
+    return k == PAGES_INT4   ? f(dd, std::integral_constant<int, PAGES_INT4>{})
+           : k == PAGES_E4M3 ? f(dd, std::integral_constant<int, PAGES_E4M3>{})
+                             : f(dd, std::integral_constant<int, PAGES_SAME>{});
+  };
+  return d == 64    ? with(std::integral_constant<int, 64>{})
+         : d == 128 ? with(std::integral_constant<int, 128>{})
+                    : with(std::integral_constant<int, 256>{});
+}
+
 int64_t paged_workspace_bytes(int d, int group, int page_type, int ctas) {
-  const bool e = page_type == HS_E4M3, two = group > 8;
-  size_t n;
-  if (d == 64)
-    n = e ? (two ? pa::ws_bytes<64, 2, true>(ctas) : pa::ws_bytes<64, 1, true>(ctas))
-          : (two ? pa::ws_bytes<64, 2, false>(ctas) : pa::ws_bytes<64, 1, false>(ctas));
-  else if (d == 128)
-    n = e ? (two ? pa::ws_bytes<128, 2, true>(ctas) : pa::ws_bytes<128, 1, true>(ctas))
-          : (two ? pa::ws_bytes<128, 2, false>(ctas) : pa::ws_bytes<128, 1, false>(ctas));
-  else
-    n = e ? (two ? pa::ws_bytes<256, 2, true>(ctas) : pa::ws_bytes<256, 1, true>(ctas))
-          : (two ? pa::ws_bytes<256, 2, false>(ctas) : pa::ws_bytes<256, 1, false>(ctas));
+  const size_t n = by_pages(d, page_type, [&](auto dd, auto pages) {
+    return group > 8 ? pa::ws_bytes<dd(), 2, pages()>(ctas) : pa::ws_bytes<dd(), 1, pages()>(ctas);
+  });
   return (int64_t)((n + 255) / 256 * 256);
 }
 
 bool paged_maps(hs_paged* h, size_t layer_bytes) {
+  if (h->cfg.page_type == HS_INT4) return true;       // plain copies: units lie together
   for (int l = 0; l < h->cfg.n_layers; ++l)
     if (!pool_map(h->cfg, static_cast<unsigned char*>(h->pages) + layer_bytes * l, &h->maps[l])) return false;
   return true;
 }
 
-cudaError_t prepare_paged(int d, int group, int type, int page_type) {
-  return d == 64    ? prepare_paged_d64(group, type, page_type)
-         : d == 128 ? prepare_paged_d128(group, type, page_type)
-                    : prepare_paged_d256(group, type, page_type);
+cudaError_t prepare_paged(int d, int group, int type, int page_type, bool scores) {
+  return by_pages(d, page_type, [&](auto dd, auto pages) {
+    return scores ? pa::prepare_paged_of<dd(), pages(), true>(group, type) : pa::prepare_paged_of<dd(), pages(), false>(group, type);
+  });
 }
 
 cudaError_t launch_paged_decode(PagedDecodeParams p, const CUtensorMap& map, cudaStream_t st) {
@@ -84,7 +84,10 @@ cudaError_t launch_paged_decode(PagedDecodeParams p, const CUtensorMap& map, cud
   const int units = p.max_pages << (p.page_shift - 4);
   const int most = p.window > 0 ? std::min(units, p.window / pa::UNIT + 2) : units;
   p.whole = most <= (p.n_req * p.h_kv >= pa::MANY_SEGMENTS ? pa::WHOLE_UNITS_MANY : pa::WHOLE_UNITS);
-  return p.d == 64 ? paged_decode_d64(p, map, st) : p.d == 128 ? paged_decode_d128(p, map, st) : paged_decode_d256(p, map, st);
+  const bool scores = p.cap_in != 0.f || p.slopes;
+  return by_pages(p.d, p.page_type, [&](auto dd, auto pages) {
+    return scores ? pa::paged_decode_of<dd(), pages(), true>(p, map, st) : pa::paged_decode_of<dd(), pages(), false>(p, map, st);
+  });
 }
 
 }  // namespace hs

@@ -58,7 +58,7 @@
 namespace hs {
 namespace pa {
 
-constexpr int UNIT = 16;                 // positions
+constexpr int UNIT = PG_UNIT;            // positions
 // what a segment costs on top of its units, in units: about two of them by the warps' ends (64 ragged
 // requests over 8-bit pages: 83, 78 and 76 us with 1, 2 and 4; no change from there up to 12)
 constexpr int SEGMENT_COST = 4;
@@ -73,18 +73,19 @@ constexpr int RING_BYTES = 192 * 1024;
 // (64 units with the one it lies across), one of 1024 does not (66).
 constexpr int WHOLE_UNITS = 32, WHOLE_UNITS_MANY = 64, MANY_SEGMENTS = 64;
 
-template <int D, int NT, int QTYPE, bool E4M3>
+template <int D, int NT, int QTYPE, int PAGES>
 struct Cfg {
+  static constexpr bool E4M3 = PAGES == PAGES_E4M3, INT4 = PAGES == PAGES_INT4;
   static constexpr int ES = E4M3 ? 1 : 2;
   static constexpr int HEADS = 8 * NT;                       // query heads of a pass
   static constexpr int ROW = D * ES < 128 ? D * ES : 128;    // bytes of a row in one swizzled block
   static constexpr int BLOCKS = D * ES / ROW;                // blocks side by side in a row
-  static constexpr int HALF = UNIT * D * ES;                 // bytes of a unit's keys (or values)
+  static constexpr int HALF = INT4 ? 9 * D : UNIT * D * ES;  // bytes of a unit's keys (or values)
   static constexpr int STAGE = 2 * HALF;
   // Eight warps with three stages or six; four where a unit is 16 KB; sixteen where units are
   // small or turning bytes into fp16 takes a warp long (8-bit, d = 128: 128 -> 90 us with the
   // segments' cost), if the registers allow it.
-  static constexpr int WARPS = STAGE >= 16384 ? 4 : STAGE <= 2048 || (E4M3 && D == 128 && NT == 1) ? 16 : 8;
+  static constexpr int WARPS = STAGE >= 16384 ? 4 : STAGE <= 2048 || ((E4M3 || INT4) && D == 128 && NT == 1) ? 16 : 8;
   static constexpr int STAGES = RING_BYTES / (WARPS * STAGE) < 12 ? RING_BYTES / (WARPS * STAGE) : 12;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int PROW = D + 4;                         // floats of a piece's head row (bank spread)
@@ -169,6 +170,59 @@ __device__ __forceinline__ void e4m3x4_to_half2(uint32_t four, uint32_t& lo, uin
       : "r"(four));
 }
 
+// two e4m3 values (low byte first) as fp16: exact
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint16_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(two));
+  return r;
+}
+
+// Rows of 4 bits, as fp16: eight codes c of a word become (c - 8) s, exactly.  c | 0x6400 is the fp16
+// 1024 + c, and 0x6400 | 16 c (a nibble higher) is 1024 + 16 c: one fused multiply-add takes the offset
+// and brings the scale in, with both products' operands in 11 bits (129 s, 9 s: s has 4).  Pairs of the
+// result are codes (0, 4), (1, 5), (2, 6), (3, 7) of the word.  Scales are taken 2^-6 as large
+// (1032 * 448 is beyond fp16); whoever uses the values puts INT4_SHIFT back.
+constexpr float INT4_SHIFT = 64.f;
+struct Int4Scale {
+  uint32_t s, off, s16, off16;        // s, -1032 s, s / 16, -72 s
+};
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ Int4Scale int4_scale(uint32_t two) {
+  Int4Scale x;
+  x.s = hmul2(two, 0x24002400u);      // 2^-6
+  x.off = hmul2(x.s, 0xe408e408u);    // -1032
+  x.s16 = hmul2(x.s, 0x2c002c00u);    // 1 / 16
+  x.off16 = hmul2(x.s, 0xd480d480u);  // -72
+  return x;
+}
+__device__ __forceinline__ void int4x8_to_half2(uint32_t w, const Int4Scale& x, uint32_t (&r)[4]) {
+  const uint32_t v = w >> 8;
+  r[0] = hfma2((w & 0x000f000fu) | 0x64006400u, x.s, x.off);
+  r[1] = hfma2((w & 0x00f000f0u) | 0x64006400u, x.s16, x.off16);
+  r[2] = hfma2((v & 0x000f000fu) | 0x64006400u, x.s, x.off);
+  r[3] = hfma2((v & 0x00f000f0u) | 0x64006400u, x.s16, x.off16);
+}
+// the w-th word (of eight codes) that lane t of a row's four holds: 16 bytes at a time, side by side
+template <int D>
+__device__ __forceinline__ int int4_word(int t, int w) {
+  return D == 64 ? 2 * t + w : (w / 4) * 16 + 4 * t + w % 4;
+}
+
+// what a value's sum is multiplied with at the end
+template <int PAGES>
+__device__ __forceinline__ float value_scale(const PagedDecodeParams& p, int kvh) {
+  return PAGES == PAGES_SAME ? 1.f : p.kv_scale[p.h_kv + kvh] * (PAGES == PAGES_INT4 ? INT4_SHIFT : 1.f);
+}
+
 // L2 policy of the pool's rows: read once by a call, they leave first (the whole of L2
 // then serves queries, pieces and the next kernels: 43.3 -> 40.8 us for a step of 64
 // requests of heads of 256); where several passes read them, as any other data.
@@ -193,6 +247,18 @@ __device__ __forceinline__ float pow2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+constexpr float LOG2_E = 1.4426950408889634f;
+
+// tanh to about 2^-20 of itself: near zero by its series (five terms: 2^-22 of itself at 0.3),
+// elsewhere 1 - 2 / (e^2|x| + 1)
+__device__ __forceinline__ float tanh32(float x) {
+  const float a = fabsf(x), y = x * x;
+  float near = fmaf(y, fmaf(y, fmaf(y, fmaf(y, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f) * x;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(pow2(a * (2.f * LOG2_E)) + 1.f));
+  return a < 0.3f ? near : copysignf(fmaf(-2.f, r, 1.f), x);
 }
 
 // The softmax's reference m.  Weights are 2^(s - m) with m near the running maximum, not
@@ -278,11 +344,12 @@ struct Place {   // a unit of the sequence
   int ri, hc, u, n;
 };
 
-template <int D, int NT, int QTYPE, bool E4M3>
-__global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
+template <int D, int NT, int QTYPE, int PAGES, bool SCORES>
+__global__ void __launch_bounds__(Cfg<D, NT, QTYPE, PAGES>::THREADS, 1)
     paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ CUtensorMap map) {
-  using C = Cfg<D, NT, QTYPE, E4M3>;
-  constexpr bool BF16 = QTYPE == HS_BF16 && !E4M3;   // type of the products
+  using C = Cfg<D, NT, QTYPE, PAGES>;
+  constexpr bool E4M3 = C::E4M3, INT4 = C::INT4, SCALED = E4M3 || INT4;
+  constexpr bool BF16 = QTYPE == HS_BF16 && !SCALED;   // type of the products
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::SM_BARS);
@@ -462,7 +529,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
       bad = (bad & ~(1u << stage)) | ((unsigned)i_bad << stage);
       if (lane == 0) {
         mbar_arrive_expect_tx(&bar[stage], C::STAGE);
-        tma_unit(ring_s + stage * C::STAGE, &map, i_row, smem_addr(&bar[stage]), policy);
+        if constexpr (INT4) {                       // a unit's keys lie together, and its values
+          const unsigned char* k = p.pages + (long long)(i_row >> 4) * C::HALF;
+          unsigned char* to = smem + C::SM_RING + ((size_t)warp * C::STAGES + stage) * C::STAGE;
+          bulk_g2s_hint(to, k, C::HALF, &bar[stage], policy);
+          bulk_g2s_hint(to + C::HALF, k + ((long long)p.h_kv << (p.page_shift - 4)) * C::HALF, C::HALF, &bar[stage], policy);
+        } else {
+          tma_unit(ring_s + stage * C::STAGE, &map, i_row, smem_addr(&bar[stage]), policy);
+        }
       }
       i_row += UNIT;
       --i_left;
@@ -476,7 +550,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
       return (uint32_t)(row * C::ROW + ((piece ^ sw) << 4));
     };
     const uint32_t k_at = place(lane & 15, lane >> 4);
-    const uint32_t v_at = C::HALF + (E4M3 ? k_at : place((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1));
+    const uint32_t v_at = C::HALF + (INT4 ? (lane >> 4) * 256 + (lane & 15) * 16
+                                     : E4M3 ? k_at : place((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1));
     // piece 2 i + b of a row: b is in the lane's place, 2 i changes bits that the place's xor keeps apart
     auto piece2 = [&](uint32_t base, int i) {
       constexpr int PER = C::ROW / 32;              // pairs of pieces in a block
@@ -484,7 +559,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
     };
 
     uint32_t qf[NT][D / 16][2];
-    float fac[NT][2];                               // scores to powers of two, by head
+    float fac[NT][2];                               // scores to powers of two (or shares of the cap), by head
+    [[maybe_unused]] float slope[NT][2];            // of the distance, to powers of two
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
     int first = 0, len = 0, unit0 = 0, from = 0;
     bool fresh = true, alive = true;
@@ -498,22 +574,30 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
         request_units(p, at.ri, &unit0, &first, &len, &req, &err);
         from = at.u;
         const int kvh = at.hc / chunks, chunk = at.hc - kvh * chunks;
-        const float ks = E4M3 ? p.kv_scale[kvh] : 1.f;
+        const float ks = E4M3 ? p.kv_scale[kvh] : INT4 ? p.kv_scale[kvh] * INT4_SHIFT : 1.f;
+        const float to_score = SCORES && p.cap_in != 0.f ? p.cap_in : p.scale_log2;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const int hg = chunk * C::HEADS + nt * 8 + g;        // head within the group
           const bool have = hg < p.group;
           const uint16_t* qrow = static_cast<const uint16_t*>(p.q) + at.ri * p.q_ts + (kvh * p.group + (have ? hg : 0)) * p.q_hs;
-          if constexpr (E4M3) {
-            // columns 4t .. 4t+3 of each 16: the order in which the key bytes come
+          if constexpr (SCALED) {
+            // columns 4t .. 4t+3 of each 16, or pairs of the lane's eights: the order in which the keys come
             float x[D / 16][4], mx = 0.f;
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              const uint2 w = *reinterpret_cast<const uint2*>(qrow + c * 16 + t * 4);
-              const float2 a = unpack2<QTYPE>(w.x), b = unpack2<QTYPE>(w.y);
-              x[c][0] = a.x; x[c][1] = a.y; x[c][2] = b.x; x[c][3] = b.y;
+            for (int c = 0; c < D / 16; c += INT4 ? 2 : 1) {
+              if constexpr (INT4) {
+                const uint4 w = *reinterpret_cast<const uint4*>(qrow + int4_word<D>(t, c / 2) * 8);
+                const float2 a = unpack2<QTYPE>(w.x), b = unpack2<QTYPE>(w.y), d = unpack2<QTYPE>(w.z), f = unpack2<QTYPE>(w.w);
+                x[c][0] = a.x; x[c][1] = d.x; x[c][2] = a.y; x[c][3] = d.y;
+                x[c + 1][0] = b.x; x[c + 1][1] = f.x; x[c + 1][2] = b.y; x[c + 1][3] = f.y;
+              } else {
+                const uint2 w = *reinterpret_cast<const uint2*>(qrow + c * 16 + t * 4);
+                const float2 a = unpack2<QTYPE>(w.x), b = unpack2<QTYPE>(w.y);
+                x[c][0] = a.x; x[c][1] = a.y; x[c][2] = b.x; x[c][3] = b.y;
+              }
 #pragma unroll
-              for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(x[c][e]));
+              for (int e = 0; e < (INT4 ? 8 : 4); ++e) mx = fmaxf(mx, fabsf(x[c + (e >> 2)][e & 3]));
             }
             mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 2));
@@ -528,7 +612,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int ee = __shfl_sync(FULL_MASK, e2, (2 * t + e) << 2);
-              fac[nt][e] = p.scale_log2 * ks * exp2f((float)(ee / 2)) * exp2f((float)(ee - ee / 2));
+              fac[nt][e] = to_score * ks * exp2f((float)(ee / 2)) * exp2f((float)(ee - ee / 2));
             }
           } else {
 #pragma unroll
@@ -538,7 +622,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
                 const uint32_t w = *reinterpret_cast<const uint32_t*>(qrow + c * 16 + e * 8 + t * 2);
                 qf[nt][c][e] = have ? w : 0u;
               }
-            fac[nt][0] = fac[nt][1] = p.scale_log2;
+            fac[nt][0] = fac[nt][1] = to_score;
+          }
+          if constexpr (SCORES) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int hs = chunk * C::HEADS + nt * 8 + 2 * t + e;
+              slope[nt][e] = p.slopes && hs < p.group ? p.slopes[kvh * p.group + hs] * LOG2_E : 0.f;
+            }
           }
           m[nt][0] = m[nt][1] = -INFINITY;
           l[nt][0] = l[nt][1] = 0.f;
@@ -568,7 +659,48 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
-        if constexpr (E4M3) {
+        if constexpr (INT4) {
+          const unsigned char* unit = smem + C::SM_RING + ((size_t)warp * C::STAGES + stage) * C::STAGE;
+          constexpr int WORDS = D / 32;             // of eight codes, of a lane and row
+          uint32_t w[2][WORDS];
+          uint16_t sb[2][WORDS > 4 ? 2 : 1];        // the scales of the lane's blocks
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const unsigned char* row = unit + (g + 8 * r) * (D / 2);
+            const unsigned char* srow = unit + 8 * D + (g + 8 * r) * (D / 16);
+            if constexpr (D == 64) {
+              const uint2 v = *reinterpret_cast<const uint2*>(row + t * 8);
+              w[r][0] = v.x; w[r][1] = v.y;
+              sb[r][0] = srow[t];
+            } else {
+#pragma unroll
+              for (int i = 0; i < WORDS / 4; ++i) {
+                const uint4 v = *reinterpret_cast<const uint4*>(row + i * 64 + t * 16);
+                w[r][4 * i] = v.x; w[r][4 * i + 1] = v.y; w[r][4 * i + 2] = v.z; w[r][4 * i + 3] = v.w;
+                sb[r][i] = *reinterpret_cast<const uint16_t*>(srow + i * 8 + 2 * t);
+              }
+            }
+          }
+          Int4Scale sc[2];
+#pragma unroll
+          for (int i = 0; i < WORDS; ++i) {
+            uint32_t a[2][4];                       // by row: pairs of the word's eight
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              if (D == 64 ? i == 0 : i % 2 == 0) {
+                const uint32_t two = e4m3x2_to_half2(sb[r][i / 4]);
+                sc[r] = int4_scale(__byte_perm(two, 0, D == 64 || i % 4 == 0 ? 0x1010 : 0x3232));
+              }
+              int4x8_to_half2(w[r][i], sc[r], a[r]);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t f[4] = {a[0][2 * c], a[1][2 * c], a[0][2 * c + 1], a[1][2 * c + 1]};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816<false>(c ? s2[nt] : s[nt], f, qf[nt][2 * i + c][0], qf[nt][2 * i + c][1]);
+            }
+          }
+        } else if constexpr (E4M3) {
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             uint32_t r[4];
@@ -598,6 +730,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
         const bool in0 = !part || (g >= lo && g < hi), in1 = !part || (g + 8 >= lo && g + 8 < hi);
         if (part) {
           // the others may hold anything: their values become 0 (a weight of 0 would leave a NaN one)
+          if constexpr (INT4) {                     // (with a scale of 0, whatever their codes)
+            unsigned char* sv = smem + C::SM_RING + ((size_t)warp * C::STAGES + stage) * C::STAGE + C::HALF + 8 * D;
+            for (int e = lane; e < D; e += 32)
+              if ((e & 15) < lo || (e & 15) >= hi) sv[e] = 0;
+          } else
           for (int e = lane; e < UNIT * C::BLOCKS * (C::ROW / 16); e += 32) {
             const int row = (e / (C::ROW / 16)) % UNIT;
             if (row < lo || row >= hi)
@@ -612,8 +749,18 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            s[nt][e] = in0 ? (s[nt][e] + s2[nt][e]) * fac[nt][e] : -INFINITY;
-            s[nt][e + 2] = in1 ? (s[nt][e + 2] + s2[nt][e + 2]) * fac[nt][e] : -INFINITY;
+            s[nt][e] = (s[nt][e] + s2[nt][e]) * fac[nt][e];
+            s[nt][e + 2] = (s[nt][e + 2] + s2[nt][e + 2]) * fac[nt][e];
+            if constexpr (SCORES) {
+              if (p.cap_in != 0.f) {
+                s[nt][e] = p.cap_log2 * tanh32(s[nt][e]);
+                s[nt][e + 2] = p.cap_log2 * tanh32(s[nt][e + 2]);
+              }
+              s[nt][e] += slope[nt][e] * (float)(pos + g - (len - 1));
+              s[nt][e + 2] += slope[nt][e] * (float)(pos + g + 8 - (len - 1));
+            }
+            s[nt][e] = in0 ? s[nt][e] : -INFINITY;
+            s[nt][e + 2] = in1 ? s[nt][e + 2] : -INFINITY;
             grows = grows || fmaxf(s[nt][e], s[nt][e + 2]) > m[nt][e] + SLACK;
           }
         if (__any_sync(FULL_MASK, grows)) {
@@ -641,7 +788,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
         // rounding (relative error of a step over wide heads 0.0021 with one, 0.0017 with two and with
         // 32-bit weights; the second takes 1.3 % of the time).  8-bit values, themselves 2^-4 off, get
         // one fp16, and the tensor pipe's time back.
-        constexpr int PARTS = E4M3 ? 1 : 2;
+        constexpr int PARTS = SCALED ? 1 : 2;
         constexpr int WTYPE = BF16 ? HS_BF16 : HS_FP16;
         uint32_t pf[NT][PARTS][2];
 #pragma unroll
@@ -664,7 +811,29 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
           }
         }
         // ---- O^T += V^T P^T
-        if constexpr (E4M3) {
+        if constexpr (INT4) {
+          const unsigned char* sv = smem + C::SM_RING + ((size_t)warp * C::STAGES + stage) * C::STAGE + C::HALF + 8 * D;
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) {
+            uint32_t r[4];                          // [32 elements of the 64][positions 0-7, 8-15]
+            ldsm4_trans(r, st + v_at + i * 512);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint32_t a[2][4];                     // by positions: the four elements of a lane
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint16_t two = *reinterpret_cast<const uint16_t*>(sv + ((2 * i + q) * 2 + (g >> 2)) * 16 + h * 8 + 2 * t);
+                int4x8_to_half2(r[2 * q + h], int4_scale(e4m3x2_to_half2(two)), a[h]);
+              }
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const uint32_t f[4] = {a[0][2 * c], a[0][2 * c + 1], a[1][2 * c], a[1][2 * c + 1]};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[nt][4 * i + 2 * q + c], f, pf[nt][0][0], pf[nt][0][1]);
+              }
+            }
+          }
+        } else if constexpr (E4M3) {
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             uint32_t r[4];
@@ -717,10 +886,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
             x += __shfl_xor_sync(FULL_MASK, x, 16);
             l[nt][e] = x;
           }
-        // an accumulator's row 0 / 1 of the pair: elements of the 16
-        const int d0 = E4M3 ? 2 * g : g, d1 = E4M3 ? 2 * g + 1 : g + 8;
+        // an accumulator's row 0 / 1 of the pair: elements of the 16 (4-bit pages: of the 32)
+        const int d0 = INT4 ? 4 * g : E4M3 ? 2 * g : g, d1 = INT4 ? 4 * g + 1 : E4M3 ? 2 * g + 1 : g + 8;
+        auto first_of = [](int c) { return INT4 ? (c >> 1) * 32 + (c & 1) * 2 : c * 16; };
         if (from == 0 && ends) {
-          const float vs = E4M3 ? p.kv_scale[p.h_kv + kvh] : 1.f;
+          const float vs = value_scale<PAGES>(p, kvh);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -733,8 +903,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c) {
                   const uint32_t two = pack2<QTYPE>(o[nt][c][e] * inv, o[nt][c][e + 2] * inv);
-                  row[c * 16 + d0] = (uint16_t)two;
-                  row[c * 16 + d1] = (uint16_t)(two >> 16);
+                  row[first_of(c) + d0] = (uint16_t)two;
+                  row[first_of(c) + d1] = (uint16_t)(two >> 16);
                 }
                 if (p.lse && g == 0) p.lse[h] = log_sum<BF16>(m[nt][e], l[nt][e]);
               }
@@ -750,8 +920,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
               const int h = nt * 8 + 2 * t + e;
 #pragma unroll
               for (int c = 0; c < D / 16; ++c) {
-                dst[h * C::PROW + c * 16 + d0] = o[nt][c][e];
-                dst[h * C::PROW + c * 16 + d1] = o[nt][c][e + 2];
+                dst[h * C::PROW + first_of(c) + d0] = o[nt][c][e];
+                dst[h * C::PROW + first_of(c) + d1] = o[nt][c][e + 2];
               }
               if (g == 0) {
                 dst[C::HEADS * C::PROW + h] = m[nt][e];
@@ -838,7 +1008,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
         }
         if (from == 0 && to == n) {
           const long long row = (long long)ri * p.h_q + kvh * p.group + hg;
-          const float inv = inverse(ll) * (E4M3 ? p.kv_scale[p.h_kv + kvh] : 1.f);
+          const float inv = inverse(ll) * value_scale<PAGES>(p, kvh);
 #pragma unroll
           for (int e = 0; e < VW; ++e) acc[e] *= inv;
           store_lane<QTYPE, VW>(p.out, row * D + lane * VW, acc);
@@ -872,10 +1042,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, QTYPE, E4M3>::THREADS, 1)
 // row; the warps' sums are added in a fixed order.
 constexpr int JOIN_WARPS = 8;
 
-template <int D, int NT, int QTYPE, bool E4M3>
+template <int D, int NT, int QTYPE, int PAGES>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
-  using C = Cfg<D, NT, QTYPE, E4M3>;
-  constexpr bool BF16 = QTYPE == HS_BF16 && !E4M3;
+  using C = Cfg<D, NT, QTYPE, PAGES>;
+  constexpr bool BF16 = QTYPE == HS_BF16 && PAGES == PAGES_SAME;
   constexpr int VW = D / 32, PER = PG_MAX_CTAS / 32;
   __shared__ float s_o[JOIN_WARPS][D];
   griddep_wait();
@@ -943,45 +1113,56 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_join_kernel(const __gri
     for (int e = 0; e < VW; ++e) acc[e] += y[e];
   }
   const long long row = (long long)ch.ri * p.h_q + kvh * p.group + hg;
-  const float inv = inverse(ll) * (E4M3 ? p.kv_scale[p.h_kv + kvh] : 1.f);
+  const float inv = inverse(ll) * value_scale<PAGES>(p, kvh);
 #pragma unroll
   for (int e = 0; e < VW; ++e) acc[e] *= inv;
   store_lane<QTYPE, VW>(p.out, row * D + lane * VW, acc);
   if (p.lse && lane == 0) p.lse[row] = log_sum<BF16>(mm, ll);
 }
 
-template <int D, int NT, int QTYPE, bool E4M3>
+template <int D, int NT, int QTYPE, int PAGES, bool SCORES>
 struct Kernels {
-  using C = Cfg<D, NT, QTYPE, E4M3>;
+  using C = Cfg<D, NT, QTYPE, PAGES>;
   static cudaError_t prepare() {
     cudaFuncAttributes fa;
-    const cudaError_t e = cudaFuncGetAttributes(&fa, paged_join_kernel<D, NT, QTYPE, E4M3>);
-    return e != cudaSuccess ? e : allow_smem(paged_decode_kernel<D, NT, QTYPE, E4M3>, C::smem(PG_MAX_REQUESTS));
+    const cudaError_t e = cudaFuncGetAttributes(&fa, paged_join_kernel<D, NT, QTYPE, PAGES>);
+    return e != cudaSuccess ? e : allow_smem(paged_decode_kernel<D, NT, QTYPE, PAGES, SCORES>, C::smem(PG_MAX_REQUESTS));
   }
   static cudaError_t launch(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st) {
-    const cudaError_t e = launch_pdl(paged_decode_kernel<D, NT, QTYPE, E4M3>, dim3(p.grid), dim3(C::THREADS),
+    const cudaError_t e = launch_pdl(paged_decode_kernel<D, NT, QTYPE, PAGES, SCORES>, dim3(p.grid), dim3(C::THREADS),
                                      C::smem(p.n_req), st, p, map);
     if (e != cudaSuccess || p.whole) return e;
-    return launch_pdl(paged_join_kernel<D, NT, QTYPE, E4M3>, dim3(p.grid, C::HEADS), dim3(32 * JOIN_WARPS), 0, st, p);
+    return launch_pdl(paged_join_kernel<D, NT, QTYPE, PAGES>, dim3(p.grid, C::HEADS), dim3(32 * JOIN_WARPS), 0, st, p);
   }
 };
 
 // f(kernels) for a configuration.  Query heads of a pass: up to 8 or 16 of a kv head's; more
 // are taken in several passes over its rows.
-template <int D, int NT, typename F>
-cudaError_t by_type(int type, int page_type, F f) {
-  const bool e = page_type == HS_E4M3;
-  if (type == HS_BF16) return e ? f(Kernels<D, NT, HS_BF16, true>{}) : f(Kernels<D, NT, HS_BF16, false>{});
-  return e ? f(Kernels<D, NT, HS_FP16, true>{}) : f(Kernels<D, NT, HS_FP16, false>{});
-}
-template <int D, typename F>
-cudaError_t by_group(int group, int type, int page_type, F f) {
-  return group <= 8 ? by_type<D, 1>(type, page_type, f) : by_type<D, 2>(type, page_type, f);
+template <int D, int PAGES, bool SCORES, typename F>
+cudaError_t by_group(int group, int type, F f) {
+  if (type == HS_BF16)
+    return group <= 8 ? f(Kernels<D, 1, HS_BF16, PAGES, SCORES>{}) : f(Kernels<D, 2, HS_BF16, PAGES, SCORES>{});
+  return group <= 8 ? f(Kernels<D, 1, HS_FP16, PAGES, SCORES>{}) : f(Kernels<D, 2, HS_FP16, PAGES, SCORES>{});
 }
 
-template <int D, int NT, bool E4M3>
+// The kernels of one head width and kind of page are compiled together (hs_paged_attention_*.cu).
+template <int D, int PAGES, bool SCORES>
+cudaError_t paged_decode_of(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st);
+template <int D, int PAGES, bool SCORES>
+cudaError_t prepare_paged_of(int group, int type);
+#define HS_PAGED_DECODE_OF(D, PAGES, SCORES)                                                                  \
+  template <>                                                                                                 \
+  cudaError_t paged_decode_of<D, PAGES, SCORES>(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st) { \
+    return by_group<D, PAGES, SCORES>(p.group, p.type, [&](auto k) { return k.launch(p, map, st); });         \
+  }                                                                                                           \
+  template <>                                                                                                 \
+  cudaError_t prepare_paged_of<D, PAGES, SCORES>(int group, int type) {                                       \
+    return by_group<D, PAGES, SCORES>(group, type, [](auto k) { return k.prepare(); });                       \
+  }
+
+template <int D, int NT, int PAGES>
 size_t ws_bytes(int grid) {
-  using C = Cfg<D, NT, HS_BF16, E4M3>;
+  using C = Cfg<D, NT, HS_BF16, PAGES>;
   return ws_chain(C::PIECE, grid, C::WARPS) * 4 + (size_t)grid * sizeof(Chain);
 }
 

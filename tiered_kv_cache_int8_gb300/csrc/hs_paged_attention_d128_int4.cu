@@ -1,0 +1,11 @@
+// The paged attention kernels for heads of 128: 4-bit pages.
+#include "hs_paged_attention.cuh"
+
+namespace hs {
+namespace pa {
+
+HS_PAGED_DECODE_OF(128, PAGES_INT4, false)
+HS_PAGED_DECODE_OF(128, PAGES_INT4, true)
+
+}  // namespace pa
+}  // namespace hs

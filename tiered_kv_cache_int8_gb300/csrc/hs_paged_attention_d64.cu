@@ -1,14 +1,11 @@
-// The paged attention kernels for heads of 64 elements.
+// The paged attention kernels for heads of 64: 16-bit and 8-bit pages.
 #include "hs_paged_attention.cuh"
 
 namespace hs {
+namespace pa {
 
-cudaError_t paged_decode_d64(const PagedDecodeParams& p, const CUtensorMap& map, cudaStream_t st) {
-  return pa::by_group<64>(p.group, p.type, p.page_type, [&](auto k) { return k.launch(p, map, st); });
-}
+HS_PAGED_DECODE_OF(64, PAGES_SAME, false)
+HS_PAGED_DECODE_OF(64, PAGES_E4M3, false)
 
-cudaError_t prepare_paged_d64(int group, int type, int page_type) {
-  return pa::by_group<64>(group, type, page_type, [](auto k) { return k.prepare(); });
-}
-
+}  // namespace pa
 }  // namespace hs

@@ -30,7 +30,7 @@ HS_DEVERR_NO_LEAD = 0x20
 HS_DEVERR_PAGE = 0x40
 HS_DEVERR_OFFSETS = 0x80
 
-HS_BF16, HS_FP16, HS_FP32, HS_E4M3 = 0, 1, 2, 3
+HS_BF16, HS_FP16, HS_FP32, HS_E4M3, HS_INT4 = 0, 1, 2, 3, 4
 HS_ROTARY_PLAIN, HS_ROTARY_LINEAR, HS_ROTARY_NTK, HS_ROTARY_BY_PARTS = 0, 1, 2, 3
 
 HS_K_APPEND, HS_K_SELECT, HS_K_ATTENTION, HS_K_COUNT = 0, 1, 2, 3
@@ -47,7 +47,8 @@ EXPORTED = ("hs_create", "hs_destroy", "hs_append", "hs_decode_layer", "hs_stats
             "hs_status_string", "hs_row_elems", "hs_indexer_topk_static",
             "hs_indexer_topk_static_error", "hs_rotary_table", "hs_rotary_apply", "hs_paged_create",
             "hs_paged_destroy", "hs_paged_append", "hs_paged_workspace_bytes", "hs_paged_decode",
-            "hs_paged_error")
+            "hs_paged_error", "hs_paged_set_scores", "hs_paged_attend_workspace_bytes", "hs_paged_attend",
+            "hs_paged_read")
 
 
 class HsConfig(ctypes.Structure):
@@ -155,6 +156,14 @@ def lib():
         L.hs_paged_workspace_bytes.restype = ctypes.c_int64
         L.hs_paged_decode.argtypes = [VP, I32, I32, VP, VP, VP, VP, VP, VP, VP, VP]
         L.hs_paged_decode.restype = ctypes.c_int
+        L.hs_paged_set_scores.argtypes = [VP, ctypes.c_float, VP]
+        L.hs_paged_set_scores.restype = ctypes.c_int
+        L.hs_paged_attend_workspace_bytes.argtypes = [VP]
+        L.hs_paged_attend_workspace_bytes.restype = ctypes.c_int64
+        L.hs_paged_attend.argtypes = [VP, I32, I32, VP, I32, VP, VP, VP, VP, VP, VP, VP, VP, VP]
+        L.hs_paged_attend.restype = ctypes.c_int
+        L.hs_paged_read.argtypes = [VP, I32, I32, VP, I32, VP, VP, VP, VP, ctypes.c_int64, VP]
+        L.hs_paged_read.restype = ctypes.c_int
         L.hs_paged_error.argtypes = [VP, P(ctypes.c_uint32)]
         L.hs_paged_error.restype = ctypes.c_int
         _LIB = L

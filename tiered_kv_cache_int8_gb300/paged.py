@@ -6,8 +6,8 @@ of their device, or on ``stream``; a call's own outputs and workspace are
 allocated on that stream.  ``ValueError`` for tensors of a wrong shape, type or
 device, ``HsError`` for what the library refuses.
 
-No call records a gradient: ``append`` and ``decode`` are for serving, what they return
-has none; ``Rotary.apply`` refuses tensors that require one while gradients are recorded.
+No call records a gradient: ``append``, ``attend``, ``decode`` and ``read`` are for serving, what
+they return has none; ``Rotary.apply`` refuses tensors that require one while gradients are recorded.
 Given outputs count as modified in place (a backward pass that saved one says so).
 """
 from __future__ import annotations
@@ -17,10 +17,12 @@ import struct
 
 import torch
 
-from .hs import (HS_BF16, HS_E4M3, HS_ERR_DEVICE, HS_FP16, HS_FP32, HS_OK, HS_ROTARY_BY_PARTS, HS_ROTARY_LINEAR,
-                 HS_ROTARY_NTK, HS_ROTARY_PLAIN, HsError, HsHeads, HsPagedConfig, HsRotary, HsRotaryConfig, lib)
+from .hs import (HS_BF16, HS_E4M3, HS_ERR_DEVICE, HS_FP16, HS_FP32, HS_INT4, HS_OK, HS_ROTARY_BY_PARTS,
+                 HS_ROTARY_LINEAR, HS_ROTARY_NTK, HS_ROTARY_PLAIN, HsError, HsHeads, HsPagedConfig, HsRotary,
+                 HsRotaryConfig, lib)
 
-TYPES = {torch.bfloat16: HS_BF16, torch.float16: HS_FP16, torch.float32: HS_FP32, torch.float8_e4m3fn: HS_E4M3}
+TYPES = {torch.bfloat16: HS_BF16, torch.float16: HS_FP16, torch.float32: HS_FP32, torch.float8_e4m3fn: HS_E4M3,
+         "int4": HS_INT4}    # (no torch type holds 4-bit codes: such pages are bytes)
 _ROTATED = {torch.bfloat16: HS_BF16, torch.float16: HS_FP16, torch.float32: HS_FP32}
 # one and two hs_heads_t in a row (packed: a ctypes structure of each costs a small call much of its time)
 _ONE, _TWO = struct.Struct("Pqqii").pack, struct.Struct("PqqiiPqqii").pack
@@ -200,9 +202,15 @@ def _kept(name: str):
 
 
 class PagedKVCache:
-    """A paged cache of keys and values in HBM, its append and its one-token attention.
+    """A paged cache of keys and values in HBM, its append, the attention of a prompt's
+    tokens and of one token, and its rows as values.
 
-    pages      : [n_layers, n_pages, 2, h_kv, page_size, d] (given, or allocated here)
+    kv_dtype   : of the pages: dtype, torch.float8_e4m3fn or "int4"; the last two with kv_scale,
+                 float32 [n_layers, 2 (keys, values), h_kv]: what a stored 1 stands for
+    pages      : [n_layers, n_pages, 2, h_kv, page_size, d] (given, or allocated here); "int4":
+                 bytes [n_layers, n_pages, 2, h_kv, page_size // 16, 9 * d] (include/hs.h has their order)
+    softcap    : scores become softcap * tanh(score / softcap); 0: they stay
+    slopes     : float32 [h_q]: a score then loses slopes[h] per position of distance
     page_table : int32 [max_requests, max_pages], page ids of each request (-1: none);
                  written by ``reserve`` / ``release``, or by the caller, who then hands
                  out the pages
@@ -220,9 +228,10 @@ class PagedKVCache:
 
     def __init__(self, *, n_layers: int, n_pages: int, page_size: int, max_requests: int, max_pages: int, h_q: int,
                  h_kv: int, d: int, dtype=torch.bfloat16, kv_dtype=None, softmax_scale: float = 0.0, window: int = 0,
-                 rotary: Rotary | None = None, kv_scale=None, pages=None, device: int = 0):
+                 rotary: Rotary | None = None, kv_scale=None, pages=None, device: int = 0, softcap: float = 0.0,
+                 slopes=None):
         kv_dtype = kv_dtype or dtype
-        _need(dtype in TYPES and kv_dtype in TYPES, f"no cache of {kv_dtype} for {dtype}")
+        _need(dtype in TYPES and kv_dtype in TYPES and dtype != "int4", f"no cache of {kv_dtype} for {dtype}")
         self._h = ctypes.c_void_p()
         self.device = torch.device("cuda", device)
         self.cfg = HsPagedConfig(n_layers, n_pages, page_size, max_requests, max_pages, h_q, h_kv, d, TYPES[dtype],
@@ -231,25 +240,38 @@ class PagedKVCache:
         self.n_layers, self.n_pages, self.page_size, self.max_pages = n_layers, n_pages, page_size, max_pages
         self.max_requests, self.h_q, self.h_kv, self.d = max_requests, h_q, h_kv, d
         _need(rotary is None or rotary.device == self.device, "the rotation is on another device")
-        shape = (n_layers, n_pages, 2, h_kv, page_size, d)
+        four = kv_dtype == "int4"
+        shape = (n_layers, n_pages, 2, h_kv, *((page_size // 16, 9 * d) if four else (page_size, d)))
+        held = torch.uint8 if four else kv_dtype
+        if slopes is not None:
+            _need(tuple(slopes.shape) == (h_q,) and slopes.dtype == torch.float32 and slopes.device == self.device,
+                  f"slopes must be float32 [h_q] on {self.device}")
+            slopes = slopes.contiguous()
         if kv_scale is not None:
             _need(tuple(kv_scale.shape) == (n_layers, 2, h_kv) and kv_scale.dtype == torch.float32
                   and kv_scale.device == self.device, f"kv_scale must be float32 [n_layers, 2, h_kv] on {self.device}")
             kv_scale = kv_scale.contiguous()
         if pages is not None:
-            _need(tuple(pages.shape) == shape and pages.dtype == kv_dtype and pages.device == self.device
-                  and pages.is_contiguous(), f"pages must be a contiguous {kv_dtype} tensor {list(shape)} on {self.device}")
+            _need(tuple(pages.shape) == shape and pages.dtype == held and pages.device == self.device
+                  and pages.is_contiguous(), f"pages must be a contiguous {held} tensor {list(shape)} on {self.device}")
         else:   # what a bad configuration makes of this is refused by the library below
-            pages = torch.empty([max(0, s) for s in shape], dtype=kv_dtype, device=self.device)
+            pages = torch.empty([max(0, s) for s in shape], dtype=held, device=self.device)
         self._error = torch.zeros(4, dtype=torch.int32, device=self.device)
         _check(lib().hs_paged_create(ctypes.byref(self.cfg), pages.data_ptr(),
                                      None if kv_scale is None else kv_scale.data_ptr(), self._error.data_ptr(),
                                      ctypes.byref(self._h)))
-        self._pages, self._kv_scale = pages, kv_scale
+        self._pages, self._kv_scale, self._slopes, self.softcap = pages, kv_scale, slopes, float(softcap)
+        if softcap or slopes is not None:
+            try:
+                _check(lib().hs_paged_set_scores(self._h, softcap, None if slopes is None else slopes.data_ptr()))
+            except HsError:
+                self.close()
+                raise
         self._page_table = torch.full((max_requests, max_pages), -1, dtype=torch.int32, device=self.device)
         self._lengths = torch.zeros(max_requests, dtype=torch.int32, device=self.device)
         self._next_lengths = torch.zeros(max_requests, dtype=torch.int32, device=self.device)
         self._ws_bytes = int(lib().hs_paged_workspace_bytes(self._h))
+        self._attend_bytes = int(lib().hs_paged_attend_workspace_bytes(self._h))
         self._free = list(range(n_pages - 1, -1, -1))
         self._held: dict[int, list[int]] = {}
         torch.cuda.current_stream(self.device).synchronize()
@@ -273,13 +295,14 @@ class PagedKVCache:
         self.close()
 
     # The library and the calls keep to these tensors' addresses: others are not put in their place.
-    pages, kv_scale, page_table, lengths, next_lengths = map(
-        _kept, ("_pages", "_kv_scale", "_page_table", "_lengths", "_next_lengths"))
+    pages, kv_scale, page_table, lengths, next_lengths, slopes = map(
+        _kept, ("_pages", "_kv_scale", "_page_table", "_lengths", "_next_lengths", "_slopes"))
 
     def _tensors(self):
         """The cache's own tensors that a call uses."""
         table = None if self.rotary is None else self.rotary._table
-        return self._pages, self._page_table, self._lengths, self._next_lengths, self._kv_scale, self._error, table
+        return (self._pages, self._page_table, self._lengths, self._next_lengths, self._kv_scale, self._error, table,
+                self._slopes)
 
     # -- pages and lengths -------------------------------------------------------
     def reserve(self, req: int, n_positions: int):
@@ -336,17 +359,11 @@ class PagedKVCache:
             return _on_stream(stream, dev, (k, v, q, q_out, req_ids, tok_offsets, *self._tensors()),
                               lambda: self.append(layer, k, v, q, q_out, req_ids, tok_offsets))
         hk, hv = _heads("k", k, dev, dtype, self.d, self.h_kv), _heads("v", v, dev, dtype, self.d, self.h_kv)
-        n_req = n = k.shape[0]
+        n = k.shape[0]
         if v.shape[0] != n:
             raise ValueError("k and v have different numbers of rows")
-        ids = offs = hq = ho = rot = None
-        if req_ids is not None:
-            n_req = req_ids.shape[0]
-            ids = _ints("req_ids", req_ids, dev, n_req)
-        if tok_offsets is not None:
-            if req_ids is None:
-                n_req = tok_offsets.shape[0] - 1
-            offs = _ints("tok_offsets", tok_offsets, dev, n_req + 1)
+        n_req, ids, offs = self._requests(n, req_ids, tok_offsets)
+        hq = ho = rot = None
         if self.rotary is not None:
             rot = self.rotary._plan[0]
         if q is not None:
@@ -369,6 +386,89 @@ class PagedKVCache:
         if rc:
             _check(rc)
         return q_out
+
+    def attend(self, layer: int, q, req_ids=None, tok_offsets=None, prefix=None, lengths=None, out=None,
+               return_lse: bool = False, stream=None):
+        """Attention of a step's new tokens over their requests' positions, themselves among
+        them: q [tokens, h_q, d] (as ``append`` returned it) -> out of its shape (and, with
+        return_lse, the float32 [tokens, h_q] logarithms of the softmax sums).  Called after the
+        append of the same tokens and before ``commit``, with its req_ids and tok_offsets.
+
+        A token sees its own position and those before it (``window`` of them at most).
+
+        prefix  : int32 [max_requests]: of request r, positions below prefix[r] are seen by every
+                  token of the call, also by those before them
+        lengths : int32 [max_requests], positions held before the step; None: the cache's
+        q       : its rows 16-byte aligned
+        out     : where to write (q itself, if it is contiguous: in place); rows of no request
+                  stay as they are (of a new out: are undefined)
+        """
+        dev, dtype = self.device, self.dtype
+        if stream is not None:
+            return _on_stream(stream, dev, (q, req_ids, tok_offsets, prefix, lengths, out, *self._tensors()),
+                              lambda: self.attend(layer, q, req_ids, tok_offsets, prefix, lengths, out, return_lse))
+        hq = _ONE(*_heads("q", q, dev, dtype, self.d, self.h_q))
+        n, lse, lse_ptr = q.shape[0], None, None
+        n_req, ids, offs = self._requests(n, req_ids, tok_offsets)
+        lens = self._lengths.data_ptr() if lengths is None else _ints("lengths", lengths, dev, self.max_requests)
+        pre = None if prefix is None else _ints("prefix", prefix, dev, self.max_requests)
+        if out is None:
+            out = torch.empty((n, self.h_q, self.d), dtype=dtype, device=dev)
+        elif out.shape != q.shape or out.dtype != dtype or out.device != dev or not out.is_contiguous():
+            raise ValueError("out must be contiguous, of q's shape, type and device")
+        else:
+            _modified(out)
+        if return_lse:
+            lse = torch.empty((n, self.h_q), dtype=torch.float32, device=dev)
+            lse_ptr = lse.data_ptr()
+        ws = torch.empty(self._attend_bytes, dtype=torch.uint8, device=dev)
+        rc = lib().hs_paged_attend(self._h, layer, n_req, ids, n, offs, self._page_table.data_ptr(), lens, pre, hq,
+                                   out.data_ptr(), lse_ptr, ws.data_ptr(), _raw_stream(dev.index))
+        if rc:
+            _check(rc)
+        return (out, lse) if return_lse else out
+
+    def _requests(self, n: int, req_ids, tok_offsets) -> tuple:
+        """Requests of a call with n rows, and the addresses of their ids and offsets."""
+        n_req, ids, offs = n, None, None
+        if req_ids is not None:
+            n_req = req_ids.shape[0]
+            ids = _ints("req_ids", req_ids, self.device, n_req)
+        if tok_offsets is not None:
+            if req_ids is None:
+                n_req = tok_offsets.shape[0] - 1
+            offs = _ints("tok_offsets", tok_offsets, self.device, n_req + 1)
+        return n_req, ids, offs
+
+    def read(self, layer: int, n_tok: int, req_ids=None, tok_offsets=None, starts=None, out=None, stream=None):
+        """Rows of the cache as values: [n_tok, 2 (keys, values), h_kv, d] of the cache's type, row j
+        of request r its position starts[r] + j; flattened, a row is one that ``HiSparseCache.append``
+        takes.  Requests, ids and offsets as for ``append``; rows of no request stay as they are (of
+        a new out: are undefined).
+
+        starts : int32 [max_requests]; None: lengths, so that the step's new rows are read
+        out    : where to write: its last three dimensions dense, its rows 16-byte aligned
+        """
+        dev, dtype = self.device, self.dtype
+        if stream is not None:
+            return _on_stream(stream, dev, (req_ids, tok_offsets, starts, out, *self._tensors()),
+                              lambda: self.read(layer, n_tok, req_ids, tok_offsets, starts, out))
+        if not 0 <= n_tok <= _MOST:
+            raise ValueError("n_tok must be in [0, 2^31 - 1]")
+        n_req, ids, offs = self._requests(n_tok, req_ids, tok_offsets)
+        begin = self._lengths.data_ptr() if starts is None else _ints("starts", starts, dev, self.max_requests)
+        shape = (n_tok, 2, self.h_kv, self.d)
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=dev)
+        elif out.shape != shape or out.dtype != dtype or out.device != dev or (n_tok and not out[0].is_contiguous()):
+            raise ValueError(f"out must be {list(shape)} {dtype} on {dev}, its last three dimensions dense")
+        else:
+            _modified(out)
+        rc = lib().hs_paged_read(self._h, layer, n_req, ids, n_tok, offs, self._page_table.data_ptr(), begin,
+                                 out.data_ptr(), out.stride(0), _raw_stream(dev.index))
+        if rc:
+            _check(rc)
+        return out
 
     def decode(self, layer: int, q, req_ids=None, lengths=None, out=None, return_lse: bool = False, stream=None):
         """Attention of one token per request: q [requests, h_q, d] -> out of its shape
