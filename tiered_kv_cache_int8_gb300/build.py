@@ -21,7 +21,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["hs_api.cu", "hs_append.cu", "hs_score.cu", "hs_select.cu", "hs_attention.cu", "hs_attention_mla.cu",
            "hs_static.cu", "hs_rotary.cu", "hs_paged.cu", "hs_paged_rows.cu", "hs_paged_attention.cu",
            *(f"hs_paged_attention_d{d}{kind}.cu" for d in (64, 128, 256) for kind in ("", "_scores", "_int4")),
-           "hs_paged_attend.cu"]
+           "hs_paged_attend.cu", *(f"hs_paged_attend_d{d}.cu" for d in (64, 128, 256))]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 

@@ -345,7 +345,7 @@ int hs_paged_create(const hs_paged_config_t* cfg, void* pages, const float* kv_s
     h->ctas = 0;
   } else {
     h->ctas = std::min(h->ctas, hs::PG_MAX_CTAS);
-    h->maps.reset(new (std::nothrow) CUtensorMap[cfg->n_layers]);
+    h->maps.reset(new (std::nothrow) CUtensorMap[(size_t)cfg->n_layers * 2]());
     if (!h->maps) {
       delete h;
       return named(HS_ERR_OOM, me, "out of host memory");
@@ -465,7 +465,7 @@ int hs_paged_read(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* re
   if (odd_ints(page_table, starts, req_ids, tok_offsets))
     return named(HS_ERR_INVALID, me, "an int32 array is not 4-byte aligned");
   const int64_t row = (int64_t)2 * c.h_kv * c.d;
-  if (reinterpret_cast<uintptr_t>(out) % 16 || token_stride % 8)
+  if (reinterpret_cast<uintptr_t>(out) % 16 || (n_tok > 1 && token_stride % 8))
     return named(HS_ERR_INVALID, me, "out's rows must be 16-byte aligned");
   if (n_tok > 1 && (token_stride < row || token_stride > ((int64_t)1 << 40) || n_tok - 1 > ((int64_t)1 << 46) / token_stride))
     return named(HS_ERR_INVALID, me, "out's rows must not overlap, and end within 2^46 elements");
@@ -603,7 +603,7 @@ int hs_paged_attend(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
   DeviceScope dev(c.device);
   if (dev.err != cudaSuccess) return fail_cuda(dev.err, "hs_paged_attend: device");
   if (h->ctas < 1) return named(HS_ERR_CUDA, me, "the handle was created without its device");
-  const cudaError_t e = hs::launch_paged_attend(p, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = hs::launch_paged_attend(p, h->maps[(size_t)c.n_layers + layer], static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? HS_OK : fail_cuda(e, "hs_paged_attend: launch");
 }
 

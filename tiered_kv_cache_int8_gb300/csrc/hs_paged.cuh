@@ -17,7 +17,8 @@ struct hs_paged {
   void* pages = nullptr;
   const float* kv_scale = nullptr;
   unsigned int* dev_error = nullptr;
-  std::unique_ptr<CUtensorMap[]> maps;   // of each layer's pool; null without a device
+  std::unique_ptr<CUtensorMap[]> maps;   // of each layer's pool, for one-token attention and, behind
+                                         // those, for prompts; null without a device
   int ctas = 0;                          // of the attention kernel; 0 without a device
   int page_shift = 0;
   float scale = 0.f, scale_log2 = 0.f;
@@ -127,7 +128,8 @@ struct PagedAttendParams {
 cudaError_t launch_append4(const RotateParams& p, int type, bool interleaved, bool wide, cudaStream_t st);
 cudaError_t launch_read(const RotateParams& p, int type, int page_type, cudaStream_t st);
 cudaError_t prepare_rows(int d, int type, int page_type);
-cudaError_t launch_paged_attend(const PagedAttendParams& p, cudaStream_t st);
+cudaError_t launch_paged_attend(const PagedAttendParams& p, const CUtensorMap& map, cudaStream_t st);
+int attend_box_rows(int d, int page_size);   // of a copy of 16-bit pages
 cudaError_t prepare_attend(int d, int type, int page_type);
 int64_t attend_workspace_bytes(int d, int ctas);
 cudaError_t launch_rotate(const RotateParams& p, int type, int page_type, bool append, bool interleaved,

@@ -43,6 +43,18 @@ bool pool_map(const hs_paged_config_t& p, void* pages, CUtensorMap* map) {
   return r == CUDA_SUCCESS;
 }
 
+// The pool as rows of 64-element blocks: a copy brings some rows of one block.
+bool rows_map(const hs_paged_config_t& p, void* pages, CUtensorMap* map) {
+  const Encode encode = encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {64, (cuuint64_t)p.n_pages * 2 * p.h_kv * p.page_size, (cuuint64_t)(p.d / 64)};
+  const cuuint64_t strides[2] = {(cuuint64_t)p.d * 2, 128};
+  const cuuint32_t box[3] = {64, (cuuint32_t)attend_box_rows(p.d, p.page_size), 1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, pages, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 // f(head width, kind of page) as constants
@@ -68,8 +80,12 @@ int64_t paged_workspace_bytes(int d, int group, int page_type, int ctas) {
 
 bool paged_maps(hs_paged* h, size_t layer_bytes) {
   if (h->cfg.page_type == HS_INT4) return true;       // plain copies: units lie together
-  for (int l = 0; l < h->cfg.n_layers; ++l)
-    if (!pool_map(h->cfg, static_cast<unsigned char*>(h->pages) + layer_bytes * l, &h->maps[l])) return false;
+  const bool rows = h->cfg.page_type == h->cfg.type;  // (8-bit rows are turned into fp16 on the way to prompts)
+  for (int l = 0; l < h->cfg.n_layers; ++l) {
+    unsigned char* pages = static_cast<unsigned char*>(h->pages) + layer_bytes * l;
+    if (!pool_map(h->cfg, pages, &h->maps[l])) return false;
+    if (rows && !rows_map(h->cfg, pages, &h->maps[(size_t)h->cfg.n_layers + l])) return false;
+  }
   return true;
 }
 
