@@ -26,11 +26,9 @@ struct Cfg {
   static constexpr int STAGES = D == 64 ? 8 : 5;
   static constexpr int SOFT = 4 * NQ;                          // softmax warps
   static constexpr int W_MMA = SOFT, W_LOAD = SOFT + 1, W_FIX = SOFT + 2, W_Q = SOFT + 3, W_CONV = SOFT + 4;
+  static constexpr int Q0 = CONV ? W_LOAD : W_Q, Q_WARPS = W_Q - Q0 + 1;   // warps that bring queries
   static constexpr int WARPS = SOFT + 4 + (CONV ? 4 : 0);
   static constexpr int THREADS = 32 * WARPS;
-  // registers of a thread at launch, of the softmax warps, of the others: the shares add up to the launch's
-  static constexpr int REGS_SOFT = NQ == 1 ? 0 : CONV ? 168 : 208;
-  static constexpr int REGS_REST = NQ == 1 ? 0 : 88;
   // columns of TMEM
   // two buffers of scores, two of weights, the sums.  Products of one shape run in the order of their
   // issue, so that at d = 128, where both products are 128 x 128, weights may lie over the scores they came
@@ -44,15 +42,18 @@ struct Cfg {
   static constexpr int SM_META = SM_RING + STAGES * STAGE;
   static constexpr size_t SMEM = 1024 + SM_META + sizeof(int) * 256;
   static constexpr int PIECE = ROWS * D + 2 * ROWS;            // floats of a piece: o [d / 4][row][4], m, l
-  static constexpr int SEGMENT_COST = 2;                       // of a segment on top of its tiles, in tiles
+  // of a segment on top of its tiles, in tiles: queries, the first scores, output (6 us; a tile takes 1.6 us
+  // at d = 128, 1 us at 64 and, of 64 positions, at 256)
+  static constexpr int SEGMENT_COST = D == 128 ? 4 : 6;
 };
 
 struct Meta {
   uint64_t full[8], empty[8], vok[8];
-  uint64_t q_full, q_empty, s_full[2], p_ready[2], o_done[2], drain;
+  uint64_t q_full, q_empty, s_full[2], p_ready[2][2], o_done[2], drain;
   uint32_t tmem;
   int abort;
-  int begin[6];                  // place of the share's first tile: request, block, head, tile; 1: there is one
+  int begin[7];                  // of the share: request, block, head, first tile; 1: there is one; what lies of the
+                                 // segment before it; cost of a segment on top of its tiles
   unsigned char bad[8];          // of a tile: its units of 16 positions on pages out of range
   signed char q_exp[2][256];     // power of two that a row of queries was divided by
 };
@@ -68,17 +69,27 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+// The products' warp runs as one, so that operands are uniform registers, and `one` (of its lanes) issues.
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+__device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t one) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+               "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)), "r"(one)
                : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, uint32_t one) {
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+               "r"((uint32_t)add), "r"(one)
+               : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t one) {
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+               "r"((uint32_t)add), "r"(one)
                : "memory");
 }
 #define HS_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
@@ -101,12 +112,80 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* r) {
 #undef HS_S8
 // (and no use of what was loaded moves before it)
 template <int N>
-__device__ __forceinline__ void tmem_wait_load(uint32_t (&r)[N]) {
+__device__ __forceinline__ void tmem_wait_load(uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_load8(uint32_t* r, uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+               "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+               : "memory");
+}
+
+// ---- two 32-bit numbers at a time
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 two(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 apart(F2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// tanh(x) / x as a polynomial of x^2, the one with the least relative error on its range (found by
+// exchange): 5.4e-7 for |x| <= 1/2, 5.9e-7 for |x| <= 1.  Six or eight products a score, where e^2x and its
+// reciprocal would cost two special functions and as many (a tile of 128 scores a thread: 8000 cycles).
+template <int N>
+__device__ __forceinline__ F2 capped2(F2 s, F2 mul, float cap) {
+  constexpr float K4[4] = {0.99999946f, -0.33326318f, 0.13190297f, -0.044402229f};
+  constexpr float K6[6] = {0.99999941f, -0.33329042f, 0.13281434f, -0.051605674f, 0.016743115f, -0.0030670604f};
+  auto k = [&](int i) {
+    const float c = (N == 4 ? K4[i] : K6[i]) * cap;
+    return two(c, c);
+  };
+  const F2 x = mul2(s, mul), y = mul2(x, x);
+  F2 r = fma2(y, k(N - 1), k(N - 2));
+#pragma unroll
+  for (int i = N - 3; i >= 0; --i) r = fma2(r, y, k(i));
+  return mul2(r, x);
+}
 
 // Shared-memory operand of 128-byte rows under the 128-byte swizzle, eight rows 1024 bytes apart.
 // `lead`: bytes between blocks of 64 elements along a row where rows are not the contraction's
@@ -118,12 +197,6 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
 __device__ __forceinline__ constexpr uint32_t product(bool bf16, int n, bool values) {
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((values ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
          ((128u >> 4) << 24);
-}
-
-template <int A>
-__device__ __forceinline__ void setmaxnreg() {   // (to A registers: whether that is more or fewer, the caller knows)
-  if constexpr (A >= 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(A));
-  else if constexpr (A > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(A));
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -223,11 +296,12 @@ struct Walk {
   const PagedAttendParams& p;
   int i, blk, head;
   long long left;               // cost that the share has left, from the segment's begin on
+  int seg;                      // cost of a segment on top of its tiles
   int from, to;                 // tiles of the piece
   Request r;
   Block b;
   unsigned err = 0;
-  __device__ Walk(const PagedAttendParams& p_, const int* begin, long long left_) : p(p_), left(left_) {
+  __device__ Walk(const PagedAttendParams& p_, const int* begin, long long left_) : p(p_), left(left_), seg(begin[6]) {
     i = begin[0];
     blk = begin[1];
     head = begin[2];
@@ -240,7 +314,7 @@ struct Walk {
     left += begin[5];
     r = request_of(p, i, &err);
     b = block_of<C>(p, r, blk);
-    to = (int)min((long long)b.tiles, left - C::SEGMENT_COST);
+    to = (int)min((long long)b.tiles, left - seg);
   }
   // whether there is a piece (empty ones are passed over)
   __device__ bool piece() {
@@ -251,7 +325,7 @@ struct Walk {
     return false;
   }
   __device__ void next() {
-    left -= b.tiles + C::SEGMENT_COST;
+    left -= b.tiles + seg;
     from = 0;
     if (left <= 0) return;
     if (++head == p.h_kv) {
@@ -269,7 +343,7 @@ struct Walk {
       }
       b = block_of<C>(p, r, blk);
     }
-    to = (int)min((long long)b.tiles, left - C::SEGMENT_COST);
+    to = (int)min((long long)b.tiles, left - seg);
   }
 };
 
@@ -298,11 +372,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(&M.empty[s], 1);
       mbar_init(&M.vok[s], 1);
     }
-    mbar_init(&M.q_full, 1);
+    mbar_init(&M.q_full, C::Q_WARPS);
     mbar_init(&M.q_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&M.s_full[s], 1);
-      mbar_init(&M.p_ready[s], 4);
+      mbar_init(&M.p_ready[0][s], 4);
+      mbar_init(&M.p_ready[1][s], 4);
       mbar_init(&M.o_done[s], 1);
     }
     mbar_init(&M.drain, 1);
@@ -316,10 +391,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   // ---- the share: blocks before each request, then the cost of a thread's blocks, then the place of its begin
   long long share, mine;
+  int seg;
   {
     int* pre = reinterpret_cast<int*>(smem + C::SM_RING);               // n_req + 1
-    long long* part = reinterpret_cast<long long*>(smem);               // a sum per thread
-    int* scan = reinterpret_cast<int*>(smem + 8 * C::THREADS);
+    long long* part = reinterpret_cast<long long*>(smem);               // a sum per warp
+    int* scan = reinterpret_cast<int*>(smem + 8 * C::WARPS);
     unsigned err = 0;
     const int per = (p.n_req + C::THREADS - 1) / C::THREADS;
     const int i0 = min(p.n_req, tid * per), i1 = min(p.n_req, i0 + per);
@@ -356,27 +432,39 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (!f(i, r, b - pre[i])) return;
       }
     };
-    long long cost = 0;
+    long long cost = 0;                          // tiles of the thread's blocks, for one head
     each([&](int, const Request& r, int blk) {
-      cost += (long long)(block_of<C>(p, r, blk).tiles + C::SEGMENT_COST) * p.h_kv;
+      cost += block_of<C>(p, r, blk).tiles;
       return true;
     });
-    part[tid] = cost;
+    long long before = cost, total = 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(FULL_MASK, before, o);
+      if (lane >= o) before += x;
+    }
+    if (lane == 31) part[warp] = before;
     __syncthreads();
-    long long before = 0, total = 0;
-    for (int t = 0; t < C::THREADS; ++t) {
+    before -= cost;
+#pragma unroll
+    for (int t = 0; t < C::WARPS; ++t) {
       const long long x = part[t];
-      if (t < tid) before += x;
+      if (t < warp) before += x;
       total += x;
     }
-    share = (total + gridDim.x - 1) / gridDim.x;
-    if (share < C::SEGMENT_COST + 1) share = C::SEGMENT_COST + 1;
+    // where a share is a few tiles, every CTA starts a segment anyway
+    seg = (int)min((long long)C::SEGMENT_COST, total * p.h_kv / gridDim.x);
+    total = (total + (long long)all * seg) * p.h_kv;
+    before = (before + (long long)b0 * seg) * p.h_kv;
+    cost = (cost + (long long)(b1 - b0) * seg) * p.h_kv;
+    share = max((total + gridDim.x - 1) / gridDim.x, (long long)seg + 1);
     const long long x0 = min(total, blockIdx.x * share), x1 = min(total, x0 + share);
     mine = x1 - x0;
+    if (tid == 0) M.begin[6] = seg;
     if (mine > 0 && x0 >= before && x0 < before + cost) {
       long long x = x0 - before;
       each([&](int i, const Request& r, int blk) {
-        const int one = block_of<C>(p, r, blk).tiles + C::SEGMENT_COST;
+        const int one = block_of<C>(p, r, blk).tiles + seg;
         if (x >= (long long)one * p.h_kv) {
           x -= (long long)one * p.h_kv;
           return true;
@@ -385,8 +473,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         M.begin[0] = i;
         M.begin[1] = blk;
         M.begin[2] = head;
-        M.begin[3] = max(0, rest - C::SEGMENT_COST);
-        M.begin[5] = rest;                       // cost of the segment before the share
+        M.begin[3] = max(0, rest - seg);
+        M.begin[5] = rest;
         M.begin[4] = 1;
         return false;
       });
@@ -403,7 +491,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   if (warp < C::SOFT) {
     // ================= softmax: a thread per row =================
-    setmaxnreg<C::REGS_SOFT>();
     const int slot = NQ == 2 ? warp >> 2 : 0, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t t_o = lanes + C::T_O + slot * D;
@@ -422,7 +509,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int pos = w.r.len + tok;
         const int hi = max(pos + 1, w.r.all), lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
         const bool shaped = p.cap_in != 0.f || p.slopes;
-        const float slope = p.slopes ? p.slopes[h] * LOG2_E : 0.f;
+        const float slope = p.slopes ? p.slopes[h] * LOG2_E : 0.f;   // to powers of two
         float mul = p.cap_in != 0.f ? p.cap_in : p.scale_log2;
         if (C::CONV) mul *= p.kv_scale[w.head] * (C::PAGES == PAGES_INT4 ? pa::INT4_SHIFT : 1.f);
         float m = -INFINITY, l = 0.f;
@@ -445,39 +532,116 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             mul *= exp2f((float)(e / 2)) * exp2f((float)(e - e / 2));
           }
           const uint32_t t_s = lanes + C::T_S + buf * KT;
-          uint32_t s[KT];
-#pragma unroll
-          for (int c = 0; c < KT; c += 32) tmem_load32(s + c, t_s + c);
-          tmem_wait_load(s);
-          auto S = [&](int c) { return __uint_as_float(s[c]); };
           const int n0 = w.b.start + (w.from + j) * KT;
-          float to2 = mul;                        // what makes powers of two of S
-          if (shaped) {
-            to2 = 1.f;
-            if (p.cap_in != 0.f) {
-#pragma unroll
-              for (int c = 0; c < KT; ++c) s[c] = __float_as_uint(p.cap_log2 * pa::tanh32(S(c) * mul));
-            } else {
-#pragma unroll
-              for (int c = 0; c < KT; ++c) s[c] = __float_as_uint(S(c) * mul);
-            }
-            if (p.slopes) {
-              const float far = (float)(n0 - pos);
-#pragma unroll
-              for (int c = 0; c < KT; ++c) s[c] = __float_as_uint(fmaf(-slope, fabsf(far + (float)c), S(c)));
-            }
-          }
+          const float to2 = shaped ? 1.f : mul;    // what makes powers of two of S
           const unsigned bad = M.bad[(tile_no + j) & 7];
-          if (__any_sync(FULL_MASK, lo > n0 || hi < n0 + KT) || bad) {
-            const int c0 = lo - n0, c1 = hi - n0;
+          const bool part = __any_sync(FULL_MASK, lo > n0 || hi < n0 + KT) || bad;
+          float top[2] = {-INFINITY, -INFINITY};
+          // 32 scores from column c0 on: cap, bias, masks (what they become goes back to its place), the largest.
+          auto shape = [&](auto capped, auto biased, auto masked, uint32_t (&s)[32], int c0) {
+            auto S = [&](int c) -> float { return __uint_as_float(s[c]); };
+            if constexpr (decltype(capped)::value) {
+              float most[2] = {0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < KT; ++c)
-              if (c < c0 || c >= c1 || (bad >> (c / 16) & 1)) s[c] = 0xff800000u;
+              for (int c = 0; c < 32; c += 2) most[c >> 1 & 1] = max3(most[c >> 1 & 1], fabsf(S(c)), fabsf(S(c + 1)));
+              // (votes of their own: a lane must not pass one over)
+              const float far = fmaxf(most[0], most[1]) * fabsf(mul);
+              const bool over_half = __any_sync(FULL_MASK, mine_row && !(far <= 0.5f));
+              const bool over_one = __any_sync(FULL_MASK, mine_row && !(far <= 1.f));
+              auto all = [&](auto n) {
+                const F2 by = two(mul, mul);
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                  const float2 z = apart(capped2<decltype(n)::value>(two(S(c), S(c + 1)), by, p.cap_log2));
+                  s[c] = __float_as_uint(z.x);
+                  s[c + 1] = __float_as_uint(z.y);
+                }
+              };
+              if (!over_half) {
+                all(std::integral_constant<int, 4>{});
+              } else if (!over_one) {
+                all(std::integral_constant<int, 6>{});
+              } else {
+#pragma unroll 1
+                for (int c = 0; c < 32; c += 8) {          // (few instructions: columns by way of their place)
+                  uint32_t z[8];
+                  tmem_load8(z, t_s + c0 + c);
+                  tmem_wait_load<8>(z);
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) z[e] = __float_as_uint(p.cap_log2 * pa::tanh32(__uint_as_float(z[e]) * mul));
+                  tmem_store8(t_s + c0 + c, z);
+                }
+                tmem_wait_store();
+                tmem_load32(s, t_s + c0);
+                tmem_wait_load<32>(s);
+              }
+            }
+            if constexpr (decltype(biased)::value) {
+              const float far = (float)(n0 + c0 - pos), by = decltype(capped)::value ? 1.f : mul;
+              const F2 by2 = two(by, by);
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                const float2 z = decltype(capped)::value ? make_float2(S(c), S(c + 1)) : apart(mul2(two(S(c), S(c + 1)), by2));
+                s[c] = __float_as_uint(fmaf(-slope, fabsf(far + (float)c), z.x));
+                s[c + 1] = __float_as_uint(fmaf(-slope, fabsf(far + (float)(c + 1)), z.y));
+              }
+            }
+            if constexpr (decltype(masked)::value) {
+              const int from = lo - n0 - c0, to = hi - n0 - c0;
+              const unsigned off = bad >> (c0 / 16);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (c < from || c >= to || (off >> (c / 16) & 1)) s[c] = 0xff800000u;
+            }
+            tmem_store32(t_s + c0, s);
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) top[c >> 1 & 1] = max3(top[c >> 1 & 1], S(c), S(c + 1));
+          };
+          // Twice over the scores, 32 at a time and the next 32 on their way: held in registers between, they
+          // would take code of thousands of instructions, which warps of different phases then wait for
+          uint32_t x[32], y[32];
+          auto each = [&](auto capped, auto biased, auto masked) {
+            tmem_load32(x, t_s);
+#pragma unroll 1
+            for (int c = 0; c < KT; c += 64) {
+              tmem_wait_load<32>(x);
+              tmem_load32(y, t_s + c + 32);
+              shape(capped, biased, masked, x, c);
+              tmem_wait_load<32>(y);
+              if (c + 64 < KT) tmem_load32(x, t_s + c + 64);
+              shape(capped, biased, masked, y, c + 32);
+            }
+            tmem_wait_store();
+          };
+          constexpr std::true_type yes{};
+          constexpr std::false_type no{};
+          if (shaped) {
+            if (p.cap_in == 0.f) {
+              if (part) each(no, yes, yes); else each(no, yes, no);
+            } else if (p.slopes) {
+              if (part) each(yes, yes, yes); else each(yes, yes, no);
+            } else {
+              if (part) each(yes, no, yes); else each(yes, no, no);
+            }
+          } else if (part) {
+            each(no, no, yes);
+          } else {
+            constexpr int HELD = C::CONV ? 64 : KT;
+#pragma unroll
+            for (int c0 = 0; c0 < KT; c0 += HELD) {
+              uint32_t s[HELD];
+              float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int c = 0; c < HELD; c += 32) tmem_load32(s + c, t_s + c0 + c);
+              tmem_wait_load<HELD>(s);
+#pragma unroll
+              for (int c = 0; c < HELD; c += 2) t[c >> 1 & 3] = max3(t[c >> 1 & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+              top[0] = max3(top[0], t[0], t[1]);
+              top[1] = max3(top[1], t[2], t[3]);
+            }
           }
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < KT; ++c) top[c & 3] = fmaxf(top[c & 3], S(c));
-          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * to2;
+          tmem_load32(x, t_s);
+          const float mx = fmaxf(top[0], top[1]) * to2;
           if (__any_sync(FULL_MASK, mine_row && mx > m + SLACK)) {    // (a row behind the last may hold anything)
             const float n = fmaxf(m, mx);
             const float keep = pow2(m - (n == -INFINITY ? 0.f : n));
@@ -489,7 +653,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
                 tmem_load32(o, t_o + c);
-                tmem_wait_load(o);
+                tmem_wait_load<32>(o);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
                 tmem_store32(t_o + c, o);
@@ -497,21 +661,36 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
           }
           const float base = (m == -INFINITY ? 0.f : m) - (C::BF16 ? 0.f : FP16_SHIFT);
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          F2 sum[2] = {two(0.f, 0.f), two(0.f, 0.f)};
+          const F2 to2s = two(to2, to2), less = two(-base, -base);
+          const uint32_t t_p = lanes + C::T_P + buf * C::P_STEP;
+          auto weights = [&](uint32_t (&s)[32], int c0) {
 #pragma unroll
-          for (int c = 0; c < KT; c += 2) {
-            const float a = pow2(fmaf(S(c), to2, -base)), b = pow2(fmaf(S(c + 1), to2, -base));
-            sum[c & 2] += a;
-            sum[(c & 2) + 1] += b;
-            s[c / 2] = pa::pack2<C::BF16 ? HS_BF16 : HS_FP16>(a, b);
+            for (int c = 0; c < 32; c += 2) {
+              const float2 z = apart(fma2(two(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), to2s, less));
+              const float a = pow2(z.x), b = pow2(z.y);
+              sum[c >> 1 & 1] = add2(sum[c >> 1 & 1], two(a, b));
+              s[c / 2] = pa::pack2<C::BF16 ? HS_BF16 : HS_FP16>(a, b);
+            }
+            tmem_store16(t_p + c0 / 2, s);
+            if (KT == 64 || c0 & 32) {             // a half of the tile: the product with the values starts on the first
+              tmem_wait_store();
+              fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&M.p_ready[KT == 64 ? c0 / 32 : c0 / 64][buf]);
+            }
+          };
+#pragma unroll 1
+          for (int c = 0; c < KT; c += 64) {
+            tmem_wait_load<32>(x);
+            tmem_load32(y, t_s + c + 32);
+            weights(x, c);
+            tmem_wait_load<32>(y);
+            if (c + 64 < KT) tmem_load32(x, t_s + c + 64);
+            weights(y, c + 32);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-#pragma unroll
-          for (int c = 0; c < KT / 2; c += 32) tmem_store32(lanes + C::T_P + buf * C::P_STEP + c, s + c);
-          tmem_wait_store();
-          fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&M.p_ready[buf]);
+          const float2 both = apart(add2(sum[0], sum[1]));
+          l += both.x + both.y;
         }
         tile_no += tiles;
         // ---- the piece's rows
@@ -521,29 +700,47 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const long long orow = (long long)(w.r.first + tok) * p.h_q + h;
         float* ws = p.ws + ws_piece<C>(blockIdx.x, w.from == 0);
         if (slot * 128 < w.b.rows) {
+          long long row4[4];                       // of the lane's four
+#pragma unroll
+          for (int k = 0; k < 4; ++k) row4[k] = __shfl_sync(FULL_MASK, mine_row ? orow : -1, (lane & ~3) + k);
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
             if (count > 0) {
               tmem_load32(o, t_o + c);
-              tmem_wait_load(o);
+              tmem_wait_load<32>(o);
             } else {
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = 0;
             }
-            if (mine_row) {
-              if (whole) {
-                uint16_t* dst = static_cast<uint16_t*>(p.out) + orow * D + c;
+            if (whole) {
+              // four lanes hand each other 16-byte parts, so that together they store 64 bytes of a row (a lane
+              // storing its own row touches 32 lines at a time)
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                  uint4 v;
-                  v.x = pa::pack2<C::QTYPE>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                  v.y = pa::pack2<C::QTYPE>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                  v.z = pa::pack2<C::QTYPE>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                  v.w = pa::pack2<C::QTYPE>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                  *reinterpret_cast<uint4*>(dst + e) = v;
+              for (int e = 0; e < 16; ++e)
+                o[e] = pa::pack2<C::QTYPE>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+#pragma unroll
+              for (int x = 1; x < 4; x <<= 1) {
+                const bool up = lane & x;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if (k & x) continue;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    uint32_t& a = o[k * 4 + e];
+                    uint32_t& b = o[(k | x) * 4 + e];
+                    const uint32_t got = __shfl_xor_sync(FULL_MASK, up ? a : b, x);
+                    if (up) a = got; else b = got;
+                  }
                 }
-              } else {
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (row4[k] >= 0)
+                  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row4[k] * D + c + (lane & 3) * 8) =
+                      make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            } else {
+              if (mine_row) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
                   *reinterpret_cast<uint4*>(ws + ((size_t)((c + e) / 4) * C::ROWS + slot * 128 + row) * 4) =
@@ -561,7 +758,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
         }
         if (w.from == 0 && !whole) {               // goes on in other CTAs: to the one with the segment's end
-          const long long end = blockIdx.x * share + mine - w.left + w.b.tiles + C::SEGMENT_COST - 1;
+          const long long end = blockIdx.x * share + mine - w.left + w.b.tiles + seg - 1;
           chain = Chain{w.i, w.blk, w.head, (int)(end / share)};
         }
         fence_before();                            // (these reads before what the next piece's products write)
@@ -570,14 +767,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     run();
     if (tid == 0) reinterpret_cast<Chain*>(p.ws + ws_chain<C>(gridDim.x))[blockIdx.x] = chain;
   } else {
-    setmaxnreg<C::REGS_REST>();
     if (warp == C::W_MMA) {
-      // ================= products: one thread =================
+      // ================= products =================
       auto run = [&] {
-        const uint32_t qk = product(C::BF16, KT, false), pv = product(C::BF16, D, true);
+        constexpr uint32_t qk = product(C::BF16, KT, false), pv = product(C::BF16, D, true);
+        const uint32_t one = elect();
         uint32_t stage = 0, phase = 0, p_used[2] = {0, 0}, q_no = 0;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-          const bool ok = wait_for(bar, parity, abort, err);
+          const bool ok = __all_sync(FULL_MASK, wait_for(bar, parity, abort, err));
           fence_after();
           return ok;
         };
@@ -592,19 +789,25 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           return s;
         };
         auto keys = [&](int s, int tile_slot, int buf) {     // S = Q K^T
-          const uint32_t q = smem_s + tile_slot * C::QB, k = ring_s + s * C::STAGE;
+          const uint64_t q = operand(smem_s + tile_slot * C::QB, 16), k = operand(ring_s + s * C::STAGE, 16);
 #pragma unroll
           for (int c = 0; c < D / 16; ++c)
-            mma_ss(tmem + C::T_S + buf * KT, operand(q + (c / 4) * (128 * 128) + (c % 4) * 32, 16),
-                   operand(k + (c / 4) * (KT * 128) + (c % 4) * 32, 16), qk, c > 0);
-          mma_commit(&M.s_full[buf]);
+            mma_ss(tmem + C::T_S + buf * KT, q + (((c / 4) * (128 * 128) + (c % 4) * 32) >> 4),
+                   k + (((c / 4) * (KT * 128) + (c % 4) * 32) >> 4), qk, c > 0, one);
+          mma_commit(&M.s_full[buf], one);
         };
         auto values = [&](int s, int tile_slot, int buf, bool add) {   // O += P V
-          const uint32_t v = ring_s + s * C::STAGE;
+          const uint64_t v = operand(ring_s + s * C::STAGE, KT * 128);
 #pragma unroll
-          for (int c = 0; c < KT / 16; ++c)
-            mma_ts(tmem + C::T_O + tile_slot * D, tmem + C::T_P + buf * C::P_STEP + c * 8, operand(v + c * 2048, KT * 128), pv, add || c > 0);
-          mma_commit(&M.o_done[buf]);
+          for (int h = 0; h < 2; ++h) {
+            if (!wait(&M.p_ready[h][buf], p_used[buf] & 1)) return false;
+#pragma unroll
+            for (int c = h * (KT / 32); c < (h + 1) * (KT / 32); ++c)
+              mma_ts(tmem + C::T_O + tile_slot * D, tmem + C::T_P + buf * C::P_STEP + c * 8, v + (c * 2048 >> 4), pv, add || c > 0, one);
+          }
+          ++p_used[buf];
+          mma_commit(&M.o_done[buf], one);
+          return true;
         };
         Walk<C> w(p, M.begin, mine);
         for (; w.piece(); w.next(), ++q_no) {
@@ -623,8 +826,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
             for (int x = 0; x < NQ; ++x)
               if (j < count[x]) keys(s, x, NQ == 2 ? x : j);
-            mma_commit(&M.empty[s]);
-            if (j == tiles - 1) mma_commit(&M.q_empty);
+            mma_commit(&M.empty[s], one);
+            if (j == tiles - 1) mma_commit(&M.q_empty, one);
           }
           for (int j = 0; j < tiles; ++j) {
             const uint32_t v = at(1, &ph);
@@ -637,20 +840,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int x = 0; x < NQ; ++x) {
               if (j >= count[x]) continue;
               const int buf = NQ == 2 ? x : j & 1;
-              if (!wait(&M.p_ready[buf], p_used[buf] & 1)) return;
-              ++p_used[buf];
-              values(v, x, buf, j > 0);
+              if (!values(v, x, buf, j > 0)) return;
               if (more && j + AHEAD < count[x]) {
                 if (!have && !wait(&M.full[k], kph)) return;
                 have = true;
                 keys(k, x, buf);
               }
             }
-            mma_commit(&M.empty[v]);
+            mma_commit(&M.empty[v], one);
             if (more) {
               if (!have && !wait(&M.full[k], kph)) return;
-              mma_commit(&M.empty[k]);
-              if (j + AHEAD == tiles - 1) mma_commit(&M.q_empty);
+              mma_commit(&M.empty[k], one);
+              if (j + AHEAD == tiles - 1) mma_commit(&M.q_empty, one);
             }
             stage += 2;
             if (stage >= C::STAGES) {
@@ -660,11 +861,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
         }
       };
-      if (lane == 0) {
-        run();
-        mma_commit(&M.drain);                     // every product is through before TMEM is freed
-        mbar_wait_bounded(&M.drain, 0);
-      }
+      run();
+      mma_commit(&M.drain, elect());                 // every product is through before TMEM is freed
+      mbar_wait_bounded(&M.drain, 0);
     } else if (warp == C::W_LOAD && !C::CONV) {
       // ================= pages by TMA =================
       uint32_t stage = 0, phase = 0, tile_no = 0;
@@ -751,53 +950,59 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
       };
       run();
-    } else if (warp == C::W_Q) {
+    } else if (warp >= C::Q0 && warp <= C::W_Q) {
       // ================= queries =================
       auto run = [&] {
         uint32_t no = 0;
-        constexpr int PER = D / 8, TOGETHER = 32 / PER ? 32 / PER : 1;    // 16-byte parts of a row, rows at a time
+        constexpr int PER = D / 8, TOGETHER = 32 / PER;       // 16-byte parts of a row, rows at a time
+        constexpr int STEP = TOGETHER * C::Q_WARPS;
+        const int c = lane % PER, r0 = (warp - C::Q0) * TOGETHER + lane / PER;
+        unsigned char* to = smem + (c / 8) * (128 * 128);
+        auto dst_of = [&](int r) { return to + (r / 128) * C::QB + (r % 128) * 128 + (((c % 8) ^ (r & 7)) << 4); };
         Walk<C> w(p, M.begin, mine);
         for (; w.piece(); w.next(), ++no) {
           if (!__all_sync(FULL_MASK, wait_for(&M.q_empty, (no & 1) ^ 1, abort, err))) return;
-          const int row0 = w.blk * C::ROWS, c = lane % PER;
-          const uint16_t* q = static_cast<const uint16_t*>(p.q) + (long long)w.r.first * p.q_ts + (long long)w.head * p.group * p.q_hs;
-          auto dst_of = [&](int r) {
-            return smem + (r / 128) * C::QB + (c / 8) * (128 * 128) + (r % 128) * 128 + (((c % 8) ^ (r & 7)) << 4);
-          };
-          if constexpr (!C::CONV) {
-            for (int r = lane / PER; r < w.b.rows; r += TOGETHER) {
-              const int tok = (row0 + r) / p.group, g = row0 + r - tok * p.group;
-              cp_async_16(dst_of(r), q + tok * p.q_ts + g * p.q_hs + c * 8);
-            }
-            cp_async_wait_all();
-          } else {
-            // as fp16, a row under a power of two that brings its largest into [1, 2)
-            for (int rb = 0; rb < w.b.rows; rb += TOGETHER) {
+          const int row0 = w.blk * C::ROWS;
+          const uint16_t* q = static_cast<const uint16_t*>(p.q) + (long long)w.r.first * p.q_ts + (long long)w.head * p.group * p.q_hs + c * 8;
+          // rows of a block from its first token on: below 2^13, so a product in 32 bits divides them
+          const int tok0 = row0 / p.group, g0 = row0 - tok0 * p.group;
+          const float one = 1.0f / p.group;
+          q += tok0 * p.q_ts;
+#pragma unroll 8
+          for (int r = r0; r < w.b.rows; r += STEP) {
+            const int tok = (int)(((float)(g0 + r) + 0.5f) * one), g = g0 + r - tok * p.group;
+            cp_async_16(dst_of(r), q + tok * p.q_ts + g * p.q_hs);
+          }
+          cp_async_wait_all();
+          if constexpr (C::CONV) {
+            // 16 bits of another range become fp16: a row under a power of two that brings its largest into [1, 2)
+#pragma unroll 2
+            for (int rb = (warp - C::Q0) * TOGETHER; rb < w.b.rows; rb += STEP) {
               const int r = rb + lane / PER;
               const bool in = r < w.b.rows;
-              const int tok = (row0 + (in ? r : 0)) / p.group, g = row0 + (in ? r : 0) - tok * p.group;
-              const uint4 u = in ? *reinterpret_cast<const uint4*>(q + tok * p.q_ts + g * p.q_hs + c * 8) : make_uint4(0, 0, 0, 0);
-              const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
-              float x[8], mx = 0.f;
+              if constexpr (C::QTYPE == HS_BF16) {
+                uint4* at = reinterpret_cast<uint4*>(dst_of(in ? r : 0));
+                const uint4 u = in ? *at : make_uint4(0, 0, 0, 0);
+                const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+                float x[8], mx = 0.f;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 v = pa::unpack2<C::QTYPE>(uw[e]);
-                x[2 * e] = v.x;
-                x[2 * e + 1] = v.y;
-                mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
-              }
+                for (int e = 0; e < 4; ++e) {
+                  const float2 v = pa::unpack2<C::QTYPE>(uw[e]);
+                  x[2 * e] = v.x;
+                  x[2 * e + 1] = v.y;
+                  mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
+                }
 #pragma unroll
-              for (int o = PER / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, o));
-              const int e2 = mx > 0.f && mx < INFINITY ? max(-126, min(126, ilogbf(mx))) : 0;
-              const float down = exp2f((float)(-e2 / 2)), down2 = exp2f((float)(-e2 - (-e2 / 2)));
-              uint4 y;
-              y.x = pa::pack2<HS_FP16>(x[0] * down * down2, x[1] * down * down2);
-              y.y = pa::pack2<HS_FP16>(x[2] * down * down2, x[3] * down * down2);
-              y.z = pa::pack2<HS_FP16>(x[4] * down * down2, x[5] * down * down2);
-              y.w = pa::pack2<HS_FP16>(x[6] * down * down2, x[7] * down * down2);
-              if (in) {
-                *reinterpret_cast<uint4*>(dst_of(r)) = y;
-                if (c == 0) M.q_exp[no & 1][r] = (signed char)e2;
+                for (int o = PER / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, o));
+                const int e2 = mx > 0.f && mx < INFINITY ? max(-126, min(126, ilogbf(mx))) : 0;
+                const float down = exp2f((float)(-e2));
+                if (in) {
+                  *at = make_uint4(pa::pack2<HS_FP16>(x[0] * down, x[1] * down), pa::pack2<HS_FP16>(x[2] * down, x[3] * down),
+                                   pa::pack2<HS_FP16>(x[4] * down, x[5] * down), pa::pack2<HS_FP16>(x[6] * down, x[7] * down));
+                  if (c == 0) M.q_exp[no & 1][r] = (signed char)e2;
+                }
+              } else if (in && c == 0) {
+                M.q_exp[no & 1][r] = 0;
               }
             }
           }
@@ -815,87 +1020,105 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         constexpr int EL = C::PAGES == PAGES_INT4 ? 32 : 16;       // elements of 16 bytes of codes
         constexpr int PER = D / EL, STEP = 128 / PER, N = KT / STEP;   // parts of a row, rows at a time, parts of a thread
         const int part = ct % PER, r0 = ct / PER;
+        struct Raw {
+          uint4 codes[N];
+          uint32_t scales[N];
+        };
+        struct Pages {
+          int at[N];             // of the thread's rows; -1: none
+          int unit;              // of the unit that the lane looks after: its page is out of range
+        };
         Walk<C> w(p, M.begin, mine);
         for (; w.piece(); w.next()) {
           const int32_t* table = p.page_table + (long long)w.r.req * p.max_pages;
-          for (int j = w.from; j < w.to; ++j, ++tile_no) {
+          auto pages_of = [&](int j) {
+            Pages g;
             const int n0 = w.b.start + j * KT;
-            if (warp == C::W_CONV) {
-              const int n = n0 + lane * 16;
-              const bool want = lane < KT / 16 && n < w.b.hi;
-              const int page = want ? table[n >> p.page_shift] : 0;
-              const unsigned bits = __ballot_sync(FULL_MASK, page < 0 || page >= p.n_pages);
-              if (lane == 0) {
-                M.bad[tile_no & 7] = (unsigned char)bits;
-                if (bits) set_error(err, HS_DEVERR_PAGE);
-              }
-            }
-            int pages[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) {
               const int n = n0 + r0 + i * STEP;
-              pages[i] = n >= w.b.lo && n < w.b.hi ? table[n >> p.page_shift] : -1;
-              if (pages[i] >= p.n_pages) pages[i] = -1;
+              g.at[i] = n >= w.b.lo && n < w.b.hi ? table[n >> p.page_shift] : -1;
             }
+            const int n = n0 + lane * 16;
+            const int id = lane < KT / 16 && n < w.b.hi ? table[n >> p.page_shift] : 0;
+            g.unit = id < 0 || id >= p.n_pages;
+            return g;
+          };
+          auto load = [&](const Pages& g, int j, int which) {
+            Raw x;
 #pragma unroll
-            for (int which = 0; which < 2; ++which) {
-              uint4 raw[N];
-              uint32_t sc[N];
-#pragma unroll
-              for (int i = 0; i < N; ++i) {
-                const int n = n0 + r0 + i * STEP;
-                raw[i] = make_uint4(0, 0, 0, 0);
-                sc[i] = 0;
-                if (pages[i] >= 0) {
-                  const long long at = ((((long long)pages[i] * 2 + which) * p.h_kv + w.head) << p.page_shift) + (n & (p.page_size - 1));
-                  if constexpr (C::PAGES == PAGES_E4M3) {
-                    raw[i] = *reinterpret_cast<const uint4*>(p.pages + at * D + part * 16);
-                  } else {
-                    const unsigned char* u = p.pages + (at >> 4) * (9 * D);
-                    const int k = n & 15;
-                    raw[i] = *reinterpret_cast<const uint4*>(u + (which ? part * 256 + k * 16 : k * (D / 2) + part * 16));
-                    const unsigned char* b = u + 8 * D + (which ? part * 32 + k : k * (D / 16) + part * 2);
-                    sc[i] = b[0] | (uint32_t)b[which ? 16 : 1] << 8;
-                  }
-                }
-              }
-              if (!__all_sync(FULL_MASK, wait_for(&M.empty[stage], phase ^ 1, abort, err))) return;
-              unsigned char* to = smem + C::SM_RING + stage * C::STAGE;
-#pragma unroll
-              for (int i = 0; i < N; ++i) {
-                const int r = r0 + i * STEP;
-                auto put = [&](int e, uint4 v) {    // elements e .. e + 7
-                  *reinterpret_cast<uint4*>(to + (e / 64) * (KT * 128) + r * 128 + (((e / 8 % 8) ^ (r & 7)) << 4)) = v;
-                };
-                const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            for (int i = 0; i < N; ++i) {
+              const int n = w.b.start + j * KT + r0 + i * STEP;
+              x.codes[i] = make_uint4(0, 0, 0, 0);
+              x.scales[i] = 0;
+              if (g.at[i] >= 0 && g.at[i] < p.n_pages) {
+                const long long at = ((((long long)g.at[i] * 2 + which) * p.h_kv + w.head) << p.page_shift) + (n & (p.page_size - 1));
                 if constexpr (C::PAGES == PAGES_E4M3) {
-#pragma unroll
-                  for (int k = 0; k < 2; ++k) {
-                    uint4 v;
-                    pa::e4m3x4_to_half2(x[2 * k], v.x, v.y);
-                    pa::e4m3x4_to_half2(x[2 * k + 1], v.z, v.w);
-                    put(part * 16 + k * 8, v);
-                  }
+                  x.codes[i] = *reinterpret_cast<const uint4*>(p.pages + at * D + part * 16);
                 } else {
-                  const uint32_t two = pa::e4m3x2_to_half2((uint16_t)sc[i]);
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const pa::Int4Scale s4 = pa::int4_scale(__byte_perm(two, 0, k < 2 ? 0x1010 : 0x3232));
-                    uint32_t a[4];                  // pairs (0, 4), (1, 5), (2, 6), (3, 7)
-                    pa::int4x8_to_half2(x[k], s4, a);
-                    put(part * 32 + k * 8, make_uint4(__byte_perm(a[0], a[1], 0x5410), __byte_perm(a[2], a[3], 0x5410),
-                                                      __byte_perm(a[0], a[1], 0x7632), __byte_perm(a[2], a[3], 0x7632)));
-                  }
+                  const unsigned char* u = p.pages + (at >> 4) * (9 * D);
+                  const int k = n & 15;
+                  x.codes[i] = *reinterpret_cast<const uint4*>(u + (which ? part * 256 + k * 16 : k * (D / 2) + part * 16));
+                  const unsigned char* b = u + 8 * D + (which ? part * 32 + k : k * (D / 16) + part * 2);
+                  x.scales[i] = b[0] | (uint32_t)b[which ? 16 : 1] << 8;
                 }
               }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&M.full[stage]);
-              if (++stage == C::STAGES) {
-                stage = 0;
-                phase ^= 1;
+            }
+            return x;
+          };
+          auto store = [&](const Raw& raw) {
+            if (!__all_sync(FULL_MASK, wait_for(&M.empty[stage], phase ^ 1, abort, err))) return false;
+            unsigned char* to = smem + C::SM_RING + stage * C::STAGE;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              const int r = r0 + i * STEP;
+              auto put = [&](int e, uint4 v) {      // elements e .. e + 7
+                *reinterpret_cast<uint4*>(to + (e / 64) * (KT * 128) + r * 128 + (((e / 8 % 8) ^ (r & 7)) << 4)) = v;
+              };
+              const uint32_t x[4] = {raw.codes[i].x, raw.codes[i].y, raw.codes[i].z, raw.codes[i].w};
+              if constexpr (C::PAGES == PAGES_E4M3) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  uint4 v;
+                  pa::e4m3x4_to_half2(x[2 * k], v.x, v.y);
+                  pa::e4m3x4_to_half2(x[2 * k + 1], v.z, v.w);
+                  put(part * 16 + k * 8, v);
+                }
+              } else {
+                const uint32_t two = pa::e4m3x2_to_half2((uint16_t)raw.scales[i]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const pa::Int4Scale s4 = pa::int4_scale(__byte_perm(two, 0, k < 2 ? 0x1010 : 0x3232));
+                  uint32_t a[4];                    // pairs (0, 4), (1, 5), (2, 6), (3, 7)
+                  pa::int4x8_to_half2(x[k], s4, a);
+                  put(part * 32 + k * 8, make_uint4(__byte_perm(a[0], a[1], 0x5410), __byte_perm(a[2], a[3], 0x5410),
+                                                    __byte_perm(a[0], a[1], 0x7632), __byte_perm(a[2], a[3], 0x7632)));
+                }
               }
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&M.full[stage]);
+            if (++stage == C::STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
+            return true;
+          };
+          // what comes next is on its way while this is turned (one after the other a tile took 4 us)
+          Pages g = pages_of(w.from);
+          Raw keys = load(g, w.from, 0);
+          for (int j = w.from; j < w.to; ++j, ++tile_no) {
+            const unsigned bits = __ballot_sync(FULL_MASK, g.unit);
+            if (ct == 0) {
+              M.bad[tile_no & 7] = (unsigned char)bits;
+              if (bits) set_error(err, HS_DEVERR_PAGE);
+            }
+            const Raw values = load(g, j, 1);
+            if (j + 1 < w.to) g = pages_of(j + 1);
+            if (!store(keys)) return;
+            if (j + 1 < w.to) keys = load(g, j + 1, 0);
+            if (!store(values)) return;
           }
         }
       };
@@ -927,6 +1150,7 @@ constexpr int JOIN_WARPS = 8;
 template <typename C>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_attend_join_kernel(const __grid_constant__ PagedAttendParams p) {
   __shared__ float4 s_o[JOIN_WARPS][8][32];
+  __shared__ float s_m[JOIN_WARPS][32], s_l[JOIN_WARPS][32];
   griddep_wait();
   griddep_launch_dependents();
   const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -939,40 +1163,49 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_attend_join_kernel(cons
   if ((int)blockIdx.y * 32 >= b.rows) return;
   const bool in = row < b.rows;
   const int n = ch.last - cta + 1, c0 = blockIdx.z * 8;
-  auto piece = [&](int j) { return p.ws + ws_piece<C>(cta + j, j == 0); };
-  float mm = -INFINITY;
-  for (int j = 0; j < n; ++j) mm = fmaxf(mm, in ? piece(j)[C::ROWS * C::D + row] : -INFINITY);
-  const float base = mm == -INFINITY ? 0.f : mm;
-  float ll = 0.f;
-  for (int j = 0; j < n; ++j)
-    if (in) ll += exp2f(piece(j)[C::ROWS * C::D + row] - base) * piece(j)[C::ROWS * C::D + C::ROWS + row];
+  float m = -INFINITY, l = 0.f;
   float4 acc[8];
 #pragma unroll
   for (int c = 0; c < 8; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
   for (int j = warp; j < n; j += JOIN_WARPS) {
-    if (!in) break;
-    const float* at = piece(j);
-    const float w = exp2f(at[C::ROWS * C::D + row] - base);
+    const float* at = p.ws + ws_piece<C>(cta + j, j == 0);
+    float4 x[8];
+    const float pm = in ? at[C::ROWS * C::D + row] : -INFINITY, pl = in ? at[C::ROWS * C::D + C::ROWS + row] : 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      x[c] = in ? *reinterpret_cast<const float4*>(at + ((size_t)(c0 + c) * C::ROWS + row) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float mm = fmaxf(m, pm), base = mm == -INFINITY ? 0.f : mm;
+    const float keep = exp2f(m - base), w = exp2f(pm - base);
+    m = mm;
+    l = l * keep + pl * w;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const float4 x = *reinterpret_cast<const float4*>(at + ((size_t)(c0 + c) * C::ROWS + row) * 4);
-      acc[c].x += w * x.x;
-      acc[c].y += w * x.y;
-      acc[c].z += w * x.z;
-      acc[c].w += w * x.w;
+      acc[c].x = acc[c].x * keep + x[c].x * w;
+      acc[c].y = acc[c].y * keep + x[c].y * w;
+      acc[c].z = acc[c].z * keep + x[c].z * w;
+      acc[c].w = acc[c].w * keep + x[c].w * w;
     }
   }
+  s_m[warp][lane] = m;
+  s_l[warp][lane] = l;
 #pragma unroll
   for (int c = 0; c < 8; ++c) s_o[warp][c][lane] = acc[c];
   __syncthreads();
-  float4 o = s_o[0][warp][lane];
+  float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-  for (int k = 1; k < JOIN_WARPS; ++k) {
+  for (int k = 0; k < JOIN_WARPS; ++k) mm = fmaxf(mm, s_m[k][lane]);
+  const float base = mm == -INFINITY ? 0.f : mm;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < JOIN_WARPS; ++k) {
+    const float w = exp2f(s_m[k][lane] - base);
     const float4 x = s_o[k][warp][lane];
-    o.x += x.x;
-    o.y += x.y;
-    o.z += x.z;
-    o.w += x.w;
+    ll += w * s_l[k][lane];
+    o.x += w * x.x;
+    o.y += w * x.y;
+    o.z += w * x.z;
+    o.w += w * x.w;
   }
   if (!in) return;
   const int rr = ch.blk * C::ROWS + row, tok = rr / p.group, h = ch.head * p.group + rr - tok * p.group;
@@ -988,11 +1221,7 @@ struct Kernels {
   static cudaError_t prepare() {
     cudaFuncAttributes fa;
     cudaError_t e = cudaFuncGetAttributes(&fa, paged_attend_join_kernel<C>);
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, paged_attend_kernel<C>);
     if (e != cudaSuccess) return e;
-    // the softmax warps would wait for ever for registers that the launch did not bring
-    if (C::REGS_SOFT && fa.numRegs * C::WARPS < C::REGS_SOFT * C::SOFT + C::REGS_REST * (C::WARPS - C::SOFT))
-      return cudaErrorInvalidConfiguration;
     return allow_smem(paged_attend_kernel<C>, C::SMEM);
   }
   static cudaError_t launch(const PagedAttendParams& p, const CUtensorMap& map, cudaStream_t st) {
