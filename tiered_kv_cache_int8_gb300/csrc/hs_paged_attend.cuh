@@ -23,10 +23,16 @@ struct Cfg {
   static constexpr int BLK = D / 64;                           // 128-byte blocks of a row
   static constexpr int QB = 128 * D * 2;                       // bytes of a tile's queries
   static constexpr int STAGE = KT * D * 2;
-  static constexpr int STAGES = D == 64 ? 8 : 5;
+  static constexpr int STAGES = D == 64 ? 8 : CONV ? 4 : 5;
+  // 8- and 4-bit pages: what a tile's keys or values (8 bits: half of them) take there, and places for that
+  static constexpr bool INT4 = PAGES == PAGES_INT4;
+  static constexpr int UNIT_BYTES = INT4 ? 9 * D : 16 * D;
+  static constexpr int PARTS = CONV && !INT4 ? 2 : 1, RAW_ROWS = KT / PARTS;
+  static constexpr int RAW = CONV ? RAW_ROWS / PG_UNIT * UNIT_BYTES : 0;
+  static constexpr int RAWS = CONV ? (INT4 ? 3 : 4) : 0;
   static constexpr int SOFT = 4 * NQ;                          // softmax warps
   static constexpr int W_MMA = SOFT, W_LOAD = SOFT + 1, W_FIX = SOFT + 2, W_Q = SOFT + 3, W_CONV = SOFT + 4;
-  static constexpr int Q0 = CONV ? W_LOAD : W_Q, Q_WARPS = W_Q - Q0 + 1;   // warps that bring queries
+  static constexpr int Q0 = CONV ? W_FIX : W_Q, Q_WARPS = W_Q - Q0 + 1;   // warps that bring queries
   static constexpr int WARPS = SOFT + 4 + (CONV ? 4 : 0);
   static constexpr int THREADS = 32 * WARPS;
   // columns of TMEM
@@ -39,7 +45,8 @@ struct Cfg {
   static constexpr int T_O = D == 128 ? 2 * KT : 3 * KT;
   static constexpr int TCOLS = 512;
   static constexpr int SM_RING = NQ * QB;
-  static constexpr int SM_META = SM_RING + STAGES * STAGE;
+  static constexpr int SM_RAW = SM_RING + STAGES * STAGE;
+  static constexpr int SM_META = (SM_RAW + RAWS * RAW + 1023) / 1024 * 1024;
   static constexpr size_t SMEM = 1024 + SM_META + sizeof(int) * 256;
   static constexpr int PIECE = ROWS * D + 2 * ROWS;            // floats of a piece: o [d / 4][row][4], m, l
   // of a segment on top of its tiles, in tiles: queries, the first scores, output (6 us; a tile takes 1.6 us
@@ -48,7 +55,7 @@ struct Cfg {
 };
 
 struct Meta {
-  uint64_t full[8], empty[8], vok[8];
+  uint64_t full[8], empty[8], ready[8], raw_full[6], raw_empty[6];
   uint64_t q_full, q_empty, s_full[2], p_ready[2][2], o_done[2], drain;
   uint32_t tmem;
   int abort;
@@ -369,8 +376,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&M.full[s], C::CONV ? 4 : 1);
-      mbar_init(&M.empty[s], 1);
-      mbar_init(&M.vok[s], 1);
+      mbar_init(&M.empty[s], C::CONV ? 1 : 2);
+      mbar_init(&M.ready[s], 1);
+    }
+    for (int s = 0; s < C::RAWS; ++s) {
+      mbar_init(&M.raw_full[s], 1);
+      mbar_init(&M.raw_empty[s], 4);
     }
     mbar_init(&M.q_full, C::Q_WARPS);
     mbar_init(&M.q_empty, 1);
@@ -537,13 +548,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const unsigned bad = M.bad[(tile_no + j) & 7];
           const bool part = __any_sync(FULL_MASK, lo > n0 || hi < n0 + KT) || bad;
           float top[2] = {-INFINITY, -INFINITY};
-          // 32 scores from column c0 on: cap, bias, masks (what they become goes back to its place), the largest.
-          auto shape = [&](auto capped, auto biased, auto masked, uint32_t (&s)[32], int c0) {
+          // 64 scores from column c0 on: cap, bias, masks (what they become goes back to its place), the largest.
+          auto shape = [&](auto capped, auto biased, auto masked, uint32_t (&s)[64], int c0) {
             auto S = [&](int c) -> float { return __uint_as_float(s[c]); };
+            const int from = lo - n0 - c0, to = hi - n0 - c0;
+            const unsigned off = bad >> (c0 / 16);
+            auto unseen = [&](int c) { return c < from || c >= to || (off >> (c / 16) & 1); };
             if constexpr (decltype(capped)::value) {
+              if constexpr (decltype(masked)::value) {     // (what hidden columns hold decides nothing)
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                  if (unseen(c)) s[c] = 0;
+              }
               float most[2] = {0.f, 0.f};
 #pragma unroll
-              for (int c = 0; c < 32; c += 2) most[c >> 1 & 1] = max3(most[c >> 1 & 1], fabsf(S(c)), fabsf(S(c + 1)));
+              for (int c = 0; c < 64; c += 2) most[c >> 1 & 1] = max3(most[c >> 1 & 1], fabsf(S(c)), fabsf(S(c + 1)));
               // (votes of their own: a lane must not pass one over)
               const float far = fmaxf(most[0], most[1]) * fabsf(mul);
               const bool over_half = __any_sync(FULL_MASK, mine_row && !(far <= 0.5f));
@@ -551,7 +570,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               auto all = [&](auto n) {
                 const F2 by = two(mul, mul);
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) {
+                for (int c = 0; c < 64; c += 2) {
                   const float2 z = apart(capped2<decltype(n)::value>(two(S(c), S(c + 1)), by, p.cap_log2));
                   s[c] = __float_as_uint(z.x);
                   s[c + 1] = __float_as_uint(z.y);
@@ -563,7 +582,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 all(std::integral_constant<int, 6>{});
               } else {
 #pragma unroll 1
-                for (int c = 0; c < 32; c += 8) {          // (few instructions: columns by way of their place)
+                for (int c = 0; c < 64; c += 8) {          // (few instructions: columns by way of their place)
                   uint32_t z[8];
                   tmem_load8(z, t_s + c0 + c);
                   tmem_wait_load<8>(z);
@@ -573,43 +592,41 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 tmem_wait_store();
                 tmem_load32(s, t_s + c0);
-                tmem_wait_load<32>(s);
+                tmem_load32(s + 32, t_s + c0 + 32);
+                tmem_wait_load<64>(s);
               }
             }
             if constexpr (decltype(biased)::value) {
               const float far = (float)(n0 + c0 - pos), by = decltype(capped)::value ? 1.f : mul;
               const F2 by2 = two(by, by);
 #pragma unroll
-              for (int c = 0; c < 32; c += 2) {
+              for (int c = 0; c < 64; c += 2) {
                 const float2 z = decltype(capped)::value ? make_float2(S(c), S(c + 1)) : apart(mul2(two(S(c), S(c + 1)), by2));
                 s[c] = __float_as_uint(fmaf(-slope, fabsf(far + (float)c), z.x));
                 s[c + 1] = __float_as_uint(fmaf(-slope, fabsf(far + (float)(c + 1)), z.y));
               }
             }
             if constexpr (decltype(masked)::value) {
-              const int from = lo - n0 - c0, to = hi - n0 - c0;
-              const unsigned off = bad >> (c0 / 16);
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (c < from || c >= to || (off >> (c / 16) & 1)) s[c] = 0xff800000u;
+              for (int c = 0; c < 64; ++c)
+                if (unseen(c)) s[c] = 0xff800000u;
             }
             tmem_store32(t_s + c0, s);
+            tmem_store32(t_s + c0 + 32, s + 32);
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) top[c >> 1 & 1] = max3(top[c >> 1 & 1], S(c), S(c + 1));
+            for (int c = 0; c < 64; c += 2) top[c >> 1 & 1] = max3(top[c >> 1 & 1], S(c), S(c + 1));
           };
-          // Twice over the scores, 32 at a time and the next 32 on their way: held in registers between, they
-          // would take code of thousands of instructions, which warps of different phases then wait for
+          // Twice over the scores, by loops: held in registers between, they would take code of thousands of
+          // instructions, which warps of different phases then wait for
           uint32_t x[32], y[32];
           auto each = [&](auto capped, auto biased, auto masked) {
-            tmem_load32(x, t_s);
 #pragma unroll 1
             for (int c = 0; c < KT; c += 64) {
-              tmem_wait_load<32>(x);
-              tmem_load32(y, t_s + c + 32);
-              shape(capped, biased, masked, x, c);
-              tmem_wait_load<32>(y);
-              if (c + 64 < KT) tmem_load32(x, t_s + c + 64);
-              shape(capped, biased, masked, y, c + 32);
+              uint32_t s[64];
+              tmem_load32(s, t_s + c);
+              tmem_load32(s + 32, t_s + c + 32);
+              tmem_wait_load<64>(s);
+              shape(capped, biased, masked, s, c);
             }
             tmem_wait_store();
           };
@@ -700,6 +717,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const long long orow = (long long)(w.r.first + tok) * p.h_q + h;
         float* ws = p.ws + ws_piece<C>(blockIdx.x, w.from == 0);
         if (slot * 128 < w.b.rows) {
+          // where an element of 32 is (4-bit pages: eight are in the order of their codes)
+          auto column = [](int e) { return C::INT4 ? (e & ~7) + (e & 3) * 2 + (e >> 2 & 1) : e; };
           long long row4[4];                       // of the lane's four
 #pragma unroll
           for (int k = 0; k < 4; ++k) row4[k] = __shfl_sync(FULL_MASK, mine_row ? orow : -1, (lane & ~3) + k);
@@ -717,8 +736,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               // four lanes hand each other 16-byte parts, so that together they store 64 bytes of a row (a lane
               // storing its own row touches 32 lines at a time)
 #pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+              uint32_t y[16];
+#pragma unroll
               for (int e = 0; e < 16; ++e)
-                o[e] = pa::pack2<C::QTYPE>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                y[e] = pa::pack2<C::QTYPE>(__uint_as_float(o[column(2 * e)]), __uint_as_float(o[column(2 * e + 1)]));
 #pragma unroll
               for (int x = 1; x < 4; x <<= 1) {
                 const bool up = lane & x;
@@ -727,8 +749,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                   if (k & x) continue;
 #pragma unroll
                   for (int e = 0; e < 4; ++e) {
-                    uint32_t& a = o[k * 4 + e];
-                    uint32_t& b = o[(k | x) * 4 + e];
+                    uint32_t& a = y[k * 4 + e];
+                    uint32_t& b = y[(k | x) * 4 + e];
                     const uint32_t got = __shfl_xor_sync(FULL_MASK, up ? a : b, x);
                     if (up) a = got; else b = got;
                   }
@@ -738,13 +760,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               for (int k = 0; k < 4; ++k)
                 if (row4[k] >= 0)
                   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row4[k] * D + c + (lane & 3) * 8) =
-                      make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                      make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
             } else {
               if (mine_row) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
                   *reinterpret_cast<uint4*>(ws + ((size_t)((c + e) / 4) * C::ROWS + slot * 128 + row) * 4) =
-                      make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                      make_uint4(o[column(e)], o[column(e + 1)], o[column(e + 2)], o[column(e + 3)]);
               }
             }
           }
@@ -831,7 +853,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           for (int j = 0; j < tiles; ++j) {
             const uint32_t v = at(1, &ph);
-            if (!wait(C::CONV ? &M.full[v] : &M.vok[v], ph)) return;
+            if (!wait(C::CONV ? &M.full[v] : &M.ready[v], ph)) return;
             const bool more = j + AHEAD < tiles;
             bool have = false;
             uint32_t kph;
@@ -864,58 +886,63 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       run();
       mma_commit(&M.drain, elect());                 // every product is through before TMEM is freed
       mbar_wait_bounded(&M.drain, 0);
-    } else if (warp == C::W_LOAD && !C::CONV) {
-      // ================= pages by TMA =================
-      uint32_t stage = 0, phase = 0, tile_no = 0;
-      uint32_t flying[2] = {0, 0};                // stages with copies that nobody may have waited for, by phase
+    } else if (warp == C::W_LOAD) {
+      // ================= pages, by TMA: into the ring, or to be turned into fp16 on the way there =================
+      constexpr int PLACES = C::CONV ? C::RAWS : C::STAGES;
+      uint64_t* full = C::CONV ? M.raw_full : M.full;
+      uint64_t* empty = C::CONV ? M.raw_empty : M.empty;
+      uint32_t stage = 0, phase = 0, tile_no = 0, copied = 0;
       auto run = [&] {
         Walk<C> w(p, M.begin, mine);
-        const int rows = min(p.page_size, KT), boxes = KT / rows * C::BLK;
+        // a lane's copy: rows of one page (and block of 64 elements), or a unit of 16
+        const int rows = C::CONV ? PG_UNIT : min(p.page_size, KT), boxes = KT / rows * (C::CONV ? 1 : C::BLK);
         for (; w.piece(); w.next()) {
           const int32_t* table = p.page_table + (long long)w.r.req * p.max_pages;
           for (int j = w.from; j < w.to; ++j, ++tile_no) {
             const int n0 = w.b.start + j * KT;
-            const int u = lane / C::BLK, n = n0 + u * rows;
+            const int u = C::CONV ? lane : lane / C::BLK, n = n0 + u * rows;
             const bool want = lane < boxes && n < w.b.hi;
-            int page = want ? table[n >> p.page_shift] : 0;
+            const int page = want ? table[n >> p.page_shift] : 0;
             const bool off = want && (page < 0 || page >= p.n_pages);
-            if (__any_sync(FULL_MASK, off)) {
-              // the bad units, of 16 positions
-              unsigned bits = off ? ((1u << (rows / 16)) - 1) << (u * (rows / 16)) : 0u;
-              bits = __reduce_or_sync(FULL_MASK, bits);
-              if (lane == 0) {
-                set_error(err, HS_DEVERR_PAGE);
-                M.bad[tile_no & 7] = (unsigned char)bits;
-              }
-            } else if (lane == 0) {
-              M.bad[tile_no & 7] = 0;
+            // the bad units, of 16 positions
+            const unsigned bits = __reduce_or_sync(FULL_MASK, off ? ((1u << (rows / 16)) - 1) << (u * (rows / 16)) : 0u);
+            if (lane == 0) {
+              if (bits) set_error(err, HS_DEVERR_PAGE);
+              M.bad[tile_no & 7] = (unsigned char)bits;
             }
             const bool copy = want && !off;
-            const int copies = __popc(__ballot_sync(FULL_MASK, copy));
             const int in_page = n & (p.page_size - 1);
 #pragma unroll
-            for (int which = 0; which < 2; ++which) {
-              if (!__all_sync(FULL_MASK, wait_for(&M.empty[stage], phase ^ 1, abort, err))) return;
-              if (lane == 0) mbar_arrive_expect_tx(&M.full[stage], copies * rows * 128);
-              __syncwarp();
-              if (copy)
-                tma_rows(ring_s + stage * C::STAGE + (lane % C::BLK) * (KT * 128) + u * rows * 128, &map,
-                         ((page * 2 + which) * p.h_kv + w.head) * p.page_size + in_page, lane % C::BLK, &M.full[stage]);
-              flying[phase] |= 1u << stage;
-              flying[phase ^ 1] &= ~(1u << stage);
-              if (++stage == C::STAGES) {
-                stage = 0;
-                phase ^= 1;
+            for (int which = 0; which < 2; ++which)
+#pragma unroll
+              for (int part = 0; part < C::PARTS; ++part) {
+                const bool now = copy && (C::PARTS == 1 || u / (C::RAW_ROWS / 16) == part);
+                const int copies = __popc(__ballot_sync(FULL_MASK, now));
+                if (!__all_sync(FULL_MASK, wait_for(&empty[stage], phase ^ 1, abort, err))) return;
+                if (lane == 0) mbar_arrive_expect_tx(&full[stage], copies * (C::CONV ? C::UNIT_BYTES : rows * 128));
+                __syncwarp();
+                if (now) {
+                  const int row = ((page * 2 + which) * p.h_kv + w.head) * p.page_size + in_page;
+                  if constexpr (C::CONV)
+                    bulk_g2s(smem + C::SM_RAW + stage * C::RAW + u % (C::RAW_ROWS / 16) * C::UNIT_BYTES,
+                             p.pages + (long long)(row >> 4) * C::UNIT_BYTES, C::UNIT_BYTES, &full[stage]);
+                  else
+                    tma_rows(ring_s + stage * C::STAGE + (lane % C::BLK) * (KT * 128) + u * rows * 128, &map, row, lane % C::BLK,
+                             &full[stage]);
+                }
+                ++copied;
+                if (++stage == PLACES) {
+                  stage = 0;
+                  phase ^= 1;
+                }
               }
-            }
           }
         }
       };
       run();
       if (*abort)                                  // copies in flight land before the shared memory goes
-        for (int s = 0; s < C::STAGES; ++s)
-          for (int ph = 0; ph < 2; ++ph)
-            if (flying[ph] >> s & 1) mbar_wait_bounded(&M.full[s], ph);
+        for (uint32_t k = copied < PLACES ? 0 : copied - PLACES; k < copied; ++k)
+          mbar_wait_bounded(&full[k % PLACES], (k / PLACES) & 1);
     } else if (warp == C::W_FIX && !C::CONV) {
       // ================= values of positions that no row sees become 0 =================
       auto run = [&] {
@@ -923,9 +950,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         Walk<C> w(p, M.begin, mine);
         for (; w.piece(); w.next())
           for (int j = w.from; j < w.to; ++j, ++tile_no) {
-            // keys are passed on as they are (a stage holds keys in one round and values in the next)
+            // Every stage is waited for here, in order, and refilled once this warp has passed it too, so that no
+            // wait is for a phase behind the next (copies land in any order) or before the last
             if (!__all_sync(FULL_MASK, wait_for(&M.full[stage], phase, abort, err))) return;
-            if (lane == 0) mbar_arrive(&M.vok[stage]);
+            if (lane == 0) {
+              mbar_arrive(&M.ready[stage]);
+              mbar_arrive(&M.empty[stage]);
+            }
             if (++stage == C::STAGES) {
               stage = 0;
               phase ^= 1;
@@ -942,7 +973,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               fence_proxy_async_smem();
               __syncwarp();
             }
-            if (lane == 0) mbar_arrive(&M.vok[stage]);
+            if (lane == 0) {
+              mbar_arrive(&M.ready[stage]);
+              mbar_arrive(&M.empty[stage]);
+            }
             if (++stage == C::STAGES) {
               stage = 0;
               phase ^= 1;
@@ -976,7 +1010,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           cp_async_wait_all();
           if constexpr (C::CONV) {
             // 16 bits of another range become fp16: a row under a power of two that brings its largest into [1, 2)
-#pragma unroll 2
+#pragma unroll 4
             for (int rb = (warp - C::Q0) * TOGETHER; rb < w.b.rows; rb += STEP) {
               const int r = rb + lane / PER;
               const bool in = r < w.b.rows;
@@ -984,25 +1018,38 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 uint4* at = reinterpret_cast<uint4*>(dst_of(in ? r : 0));
                 const uint4 u = in ? *at : make_uint4(0, 0, 0, 0);
                 const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
-                float x[8], mx = 0.f;
+                // the largest of a row as whole numbers: bits without a sign order as values do (a NaN above all)
+                uint32_t mx = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx = __vmaxu2(mx, uw[e] & 0x7fff7fffu);
+#pragma unroll
+                for (int o = PER / 2; o; o >>= 1) mx = __vmaxu2(mx, __shfl_xor_sync(FULL_MASK, mx, o));
+                const int bits = max(mx & 0xffff, mx >> 16), field = bits >> 7;     // exponent of bf16
+                const int e2 = field == 0 || field == 255 ? 0 : max(-126, min(126, field - 127));
+                const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
+                float x[8];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  const float2 v = pa::unpack2<C::QTYPE>(uw[e]);
-                  x[2 * e] = v.x;
-                  x[2 * e + 1] = v.y;
-                  mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
+                  x[2 * e] = bf16lo(uw[e]);
+                  x[2 * e + 1] = bf16hi(uw[e]);
                 }
-#pragma unroll
-                for (int o = PER / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, o));
-                const int e2 = mx > 0.f && mx < INFINITY ? max(-126, min(126, ilogbf(mx))) : 0;
-                const float down = exp2f((float)(-e2));
                 if (in) {
-                  *at = make_uint4(pa::pack2<HS_FP16>(x[0] * down, x[1] * down), pa::pack2<HS_FP16>(x[2] * down, x[3] * down),
-                                   pa::pack2<HS_FP16>(x[4] * down, x[5] * down), pa::pack2<HS_FP16>(x[6] * down, x[7] * down));
+                  // (4-bit pages: elements of eight in the order in which their codes are turned)
+                  auto pair = [&](int i) {
+                    const int e = C::INT4 ? i : 2 * i, f = C::INT4 ? i + 4 : 2 * i + 1;
+                    return pa::pack2<HS_FP16>(x[e] * down, x[f] * down);
+                  };
+                  *at = make_uint4(pair(0), pair(1), pair(2), pair(3));
                   if (c == 0) M.q_exp[no & 1][r] = (signed char)e2;
                 }
-              } else if (in && c == 0) {
-                M.q_exp[no & 1][r] = 0;
+              } else if (in) {
+                if constexpr (C::INT4) {
+                  uint4* at = reinterpret_cast<uint4*>(dst_of(r));
+                  const uint4 u = *at;
+                  *at = make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632), __byte_perm(u.y, u.w, 0x5410),
+                                   __byte_perm(u.y, u.w, 0x7632));
+                }
+                if (c == 0) M.q_exp[no & 1][r] = 0;
               }
             }
           }
@@ -1015,112 +1062,82 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     } else if (C::CONV && warp >= C::W_CONV) {
       // ================= 8-bit and 4-bit pages, turned into fp16 =================
       auto run = [&] {
-        uint32_t stage = 0, phase = 0, tile_no = 0;
+        uint32_t stage = 0, phase = 0, place = 0, place_phase = 0, tile_no = 0;
         const int ct = tid - 32 * C::W_CONV;
-        constexpr int EL = C::PAGES == PAGES_INT4 ? 32 : 16;       // elements of 16 bytes of codes
-        constexpr int PER = D / EL, STEP = 128 / PER, N = KT / STEP;   // parts of a row, rows at a time, parts of a thread
+        constexpr int EL = C::INT4 ? 32 : 16;                      // elements of 16 bytes of codes
+        constexpr int PER = D / EL, STEP = 128 / PER, N = C::RAW_ROWS / STEP;   // parts of a row, rows at a time, parts of a thread
         const int part = ct % PER, r0 = ct / PER;
-        struct Raw {
-          uint4 codes[N];
-          uint32_t scales[N];
-        };
-        struct Pages {
-          int at[N];             // of the thread's rows; -1: none
-          int unit;              // of the unit that the lane looks after: its page is out of range
-        };
+        // where the thread's rows go: the swizzle of their 16-byte pieces is the same for all of them
+        static_assert(STEP % 8 == 0, "");
+        unsigned char* const to0 = smem + C::SM_RING + part * EL / 64 * (KT * 128) + r0 * 128;
+        const int piece0 = part * EL / 8 % 8, sw = r0 & 7;
         Walk<C> w(p, M.begin, mine);
-        for (; w.piece(); w.next()) {
-          const int32_t* table = p.page_table + (long long)w.r.req * p.max_pages;
-          auto pages_of = [&](int j) {
-            Pages g;
-            const int n0 = w.b.start + j * KT;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const int n = n0 + r0 + i * STEP;
-              g.at[i] = n >= w.b.lo && n < w.b.hi ? table[n >> p.page_shift] : -1;
-            }
-            const int n = n0 + lane * 16;
-            const int id = lane < KT / 16 && n < w.b.hi ? table[n >> p.page_shift] : 0;
-            g.unit = id < 0 || id >= p.n_pages;
-            return g;
-          };
-          auto load = [&](const Pages& g, int j, int which) {
-            Raw x;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const int n = w.b.start + j * KT + r0 + i * STEP;
-              x.codes[i] = make_uint4(0, 0, 0, 0);
-              x.scales[i] = 0;
-              if (g.at[i] >= 0 && g.at[i] < p.n_pages) {
-                const long long at = ((((long long)g.at[i] * 2 + which) * p.h_kv + w.head) << p.page_shift) + (n & (p.page_size - 1));
-                if constexpr (C::PAGES == PAGES_E4M3) {
-                  x.codes[i] = *reinterpret_cast<const uint4*>(p.pages + at * D + part * 16);
-                } else {
-                  const unsigned char* u = p.pages + (at >> 4) * (9 * D);
-                  const int k = n & 15;
-                  x.codes[i] = *reinterpret_cast<const uint4*>(u + (which ? part * 256 + k * 16 : k * (D / 2) + part * 16));
-                  const unsigned char* b = u + 8 * D + (which ? part * 32 + k : k * (D / 16) + part * 2);
-                  x.scales[i] = b[0] | (uint32_t)b[which ? 16 : 1] << 8;
-                }
-              }
-            }
-            return x;
-          };
-          auto store = [&](const Raw& raw) {
-            if (!__all_sync(FULL_MASK, wait_for(&M.empty[stage], phase ^ 1, abort, err))) return false;
-            unsigned char* to = smem + C::SM_RING + stage * C::STAGE;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const int r = r0 + i * STEP;
-              auto put = [&](int e, uint4 v) {      // elements e .. e + 7
-                *reinterpret_cast<uint4*>(to + (e / 64) * (KT * 128) + r * 128 + (((e / 8 % 8) ^ (r & 7)) << 4)) = v;
-              };
-              const uint32_t x[4] = {raw.codes[i].x, raw.codes[i].y, raw.codes[i].z, raw.codes[i].w};
-              if constexpr (C::PAGES == PAGES_E4M3) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  uint4 v;
-                  pa::e4m3x4_to_half2(x[2 * k], v.x, v.y);
-                  pa::e4m3x4_to_half2(x[2 * k + 1], v.z, v.w);
-                  put(part * 16 + k * 8, v);
-                }
-              } else {
-                const uint32_t two = pa::e4m3x2_to_half2((uint16_t)raw.scales[i]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const pa::Int4Scale s4 = pa::int4_scale(__byte_perm(two, 0, k < 2 ? 0x1010 : 0x3232));
-                  uint32_t a[4];                    // pairs (0, 4), (1, 5), (2, 6), (3, 7)
-                  pa::int4x8_to_half2(x[k], s4, a);
-                  put(part * 32 + k * 8, make_uint4(__byte_perm(a[0], a[1], 0x5410), __byte_perm(a[2], a[3], 0x5410),
-                                                    __byte_perm(a[0], a[1], 0x7632), __byte_perm(a[2], a[3], 0x7632)));
-                }
-              }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&M.full[stage]);
-            if (++stage == C::STAGES) {
-              stage = 0;
-              phase ^= 1;
-            }
-            return true;
-          };
-          // what comes next is on its way while this is turned (one after the other a tile took 4 us)
-          Pages g = pages_of(w.from);
-          Raw keys = load(g, w.from, 0);
+        for (; w.piece(); w.next())
           for (int j = w.from; j < w.to; ++j, ++tile_no) {
-            const unsigned bits = __ballot_sync(FULL_MASK, g.unit);
-            if (ct == 0) {
-              M.bad[tile_no & 7] = (unsigned char)bits;
-              if (bits) set_error(err, HS_DEVERR_PAGE);
+            const int n0 = w.b.start + j * KT;
+#pragma unroll 1
+            for (int step = 0; step < 2 * C::PARTS; ++step) {
+              const int which = step / C::PARTS, half = step % C::PARTS;
+              if (half == 0 && !__all_sync(FULL_MASK, wait_for(&M.empty[stage], phase ^ 1, abort, err))) return;
+              if (!__all_sync(FULL_MASK, wait_for(&M.raw_full[place], place_phase, abort, err))) return;
+              const unsigned bad = M.bad[tile_no & 7];
+              const bool all = n0 >= w.b.lo && n0 + KT <= w.b.hi && !bad;
+              const unsigned char* from = smem + C::SM_RAW + place * C::RAW;
+              unsigned char* to = to0 + stage * C::STAGE + half * (C::RAW_ROWS * 128);
+              // of 4-bit rows: where the thread's codes and scales are in a unit
+              const int code_row = which ? 16 : D / 2, code0 = which ? part * 256 : part * 16;
+              const int scale_row = which ? 1 : D / 16, scale0 = 8 * D + (which ? part * 32 : part * 2), scale_step = which ? 16 : 1;
+#pragma unroll
+              for (int i = 0; i < N; ++i) {
+                const int q = r0 + i * STEP, n = n0 + half * C::RAW_ROWS + q;
+                // (rows that no token sees hold anything: they become 0)
+                const bool seen = all || (n >= w.b.lo && n < w.b.hi && !(bad >> ((n - n0) / 16) & 1));
+                auto put = [&](int k, uint4 v) {    // the k-th eight elements
+                  *reinterpret_cast<uint4*>(to + i * (STEP * 128) + (((piece0 + k) ^ sw) << 4)) = v;
+                };
+                if constexpr (!C::INT4) {
+                  const uint4 u = seen ? *reinterpret_cast<const uint4*>(from + q * D + part * 16) : make_uint4(0, 0, 0, 0);
+                  uint4 v;
+                  pa::e4m3x4_to_half2(u.x, v.x, v.y);
+                  pa::e4m3x4_to_half2(u.y, v.z, v.w);
+                  put(0, v);
+                  pa::e4m3x4_to_half2(u.z, v.x, v.y);
+                  pa::e4m3x4_to_half2(u.w, v.z, v.w);
+                  put(1, v);
+                } else {
+                  const unsigned char* unit = from + (q / 16) * (9 * D);
+                  const uint4 u = *reinterpret_cast<const uint4*>(unit + code0 + q % 16 * code_row);
+                  const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+                  const unsigned char* at = unit + scale0 + q % 16 * scale_row;
+                  const uint32_t two = pa::e4m3x2_to_half2((uint16_t)(seen ? at[0] | (unsigned)at[scale_step] << 8 : 0));
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    const pa::Int4Scale s4 = pa::int4_scale(__byte_perm(two, 0, h ? 0x3232 : 0x1010));
+#pragma unroll
+                    for (int k = 2 * h; k < 2 * h + 2; ++k) {
+                      uint32_t a[4];                // elements (0, 4), (1, 5), (2, 6), (3, 7) of eight: they stay so, as
+                      pa::int4x8_to_half2(x[k], s4, a);   // queries come, and outputs leave, in that order
+                      put(k, make_uint4(a[0], a[1], a[2], a[3]));
+                    }
+                  }
+                }
+              }
+              if (half == C::PARTS - 1) fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(&M.raw_empty[place]);
+                if (half == C::PARTS - 1) mbar_arrive(&M.full[stage]);
+              }
+              if (++place == C::RAWS) {
+                place = 0;
+                place_phase ^= 1;
+              }
+              if (half == C::PARTS - 1 && ++stage == C::STAGES) {
+                stage = 0;
+                phase ^= 1;
+              }
             }
-            const Raw values = load(g, j, 1);
-            if (j + 1 < w.to) g = pages_of(j + 1);
-            if (!store(keys)) return;
-            if (j + 1 < w.to) keys = load(g, j + 1, 0);
-            if (!store(values)) return;
           }
-        }
       };
       run();
     }
