@@ -1,12 +1,16 @@
 // Rows into 4-bit pages (hs_paged_append) and rows of any pages back as values
-// (hs_paged_read): a warp moves the rows of one token, head by head, 1/32 of a row a lane.
+// (hs_paged_read): a lane has eight elements of a row, a warp 256 / d rows of one token side by side.
 //
 // 4-bit rows.  x' = x / kv_scale (as a product with 1 / kv_scale, in 32 bits); 16 elements share
 // s = e4m3(max |x'| / 7); code = clamp(round(x' / s), -7, 7) + 8, so a row stands for
-// (code - 8) s kv_scale.  Both quotients are divisions rounded to nearest, so that the codes
-// are those of the formula.  A scale rounded down by up to 2^-4 leaves |x' / s| up to
-// 7.47: clamped, still within half a step.  7 / amax would waste the code 0 (-8), which rows
-// may hold but none is given: levels that are symmetric about zero keep signs fair.
+// (code - 8) s kv_scale.  Both quotients are rounded as divisions are, so that the codes are
+// those of the formula: q = a y with y the rounded reciprocal, then q + (a - q b) y, the
+// remainder exact in a fused multiply-add.  (No quotient that is not a half itself is within
+// 2^-24 of one: halves times s have 8 bits.)  A scale rounded down by up to 2^-4 leaves |x' / s|
+// up to 7.47: clamped, still within half a step.  7 / amax would waste the code 0 (-8), which
+// rows may hold but none is given: levels that are symmetric about zero keep signs fair.
+//
+// Bound: HBM in the end, instructions on the way.  Measured: FIGURES
 #include "hs_paged_place.cuh"
 
 namespace hs {
@@ -14,7 +18,10 @@ namespace {
 
 constexpr int ROWS_THREADS = 256;
 constexpr int ROWS_WARPS = ROWS_THREADS / 32;
-constexpr int ROWS_AHEAD = 8;      // rows of a warp on their way at once
+constexpr int VW = 8;              // elements of a lane
+constexpr int AHEAD = 4;           // rows of a lane on their way at once
+template <int D>
+constexpr int SIDE = 32 * VW / D;  // rows side by side in a warp
 
 template <typename T>
 struct Two;
@@ -35,43 +42,37 @@ struct Two<__half> {
   }
 };
 
-// VW 16-bit elements as words
-template <int VW>
-struct Words {
-  uint32_t w[VW / 2];
-};
-template <int VW>
-__device__ __forceinline__ Words<VW> load_words(const uint16_t* p, bool wide) {
-  Words<VW> x;
-  if (wide) {
-    if constexpr (VW == 2) x.w[0] = *reinterpret_cast<const uint32_t*>(p);
-    if constexpr (VW == 4) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      x.w[0] = v.x; x.w[1] = v.y;
-    }
-    if constexpr (VW == 8) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      x.w[0] = v.x; x.w[1] = v.y; x.w[2] = v.z; x.w[3] = v.w;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < VW / 2; ++e) x.w[e] = (uint32_t)p[2 * e] | ((uint32_t)p[2 * e + 1] << 16);
-  }
-  return x;
+// eight 16-bit elements as words
+__device__ __forceinline__ uint4 load8(const uint16_t* p, bool wide) {
+  if (wide) return *reinterpret_cast<const uint4*>(p);
+  auto w = [&](int i) { return (uint32_t)p[i] | ((uint32_t)p[i + 1] << 16); };
+  return make_uint4(w(0), w(2), w(4), w(6));
 }
-template <int VW>
-__device__ __forceinline__ void store_words(uint16_t* p, const Words<VW>& x, bool wide) {
+__device__ __forceinline__ void store8(uint16_t* p, uint4 x, bool wide) {
   if (wide) {
-    if constexpr (VW == 2) *reinterpret_cast<uint32_t*>(p) = x.w[0];
-    if constexpr (VW == 4) *reinterpret_cast<uint2*>(p) = make_uint2(x.w[0], x.w[1]);
-    if constexpr (VW == 8) *reinterpret_cast<uint4*>(p) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+    *reinterpret_cast<uint4*>(p) = x;
   } else {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int e = 0; e < VW / 2; ++e) {
-      p[2 * e] = (uint16_t)x.w[e];
-      p[2 * e + 1] = (uint16_t)(x.w[e] >> 16);
+    for (int e = 0; e < 4; ++e) {
+      p[2 * e] = (uint16_t)w[e];
+      p[2 * e + 1] = (uint16_t)(w[e] >> 16);
     }
   }
+}
+template <typename T>
+__device__ __forceinline__ void up8(uint4 x, float (&y)[VW]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 v = Two<T>::up(w[e]);
+    y[2 * e] = v.x;
+    y[2 * e + 1] = v.y;
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 down8(const float (&x)[VW]) {
+  return make_uint4(Two<T>::down(x[0], x[1]), Two<T>::down(x[2], x[3]), Two<T>::down(x[4], x[5]), Two<T>::down(x[6], x[7]));
 }
 
 __device__ __forceinline__ float e4m3_up(unsigned char b) {
@@ -86,11 +87,9 @@ __device__ __forceinline__ int scale_at(int d, bool values, int slot, int block)
   return 8 * d + (values ? block * 16 + slot : slot * (d >> 4) + block);
 }
 
-// VW elements of a lane -> 4-bit codes and its block's scale in the unit at `unit`
-template <int VW>
-__device__ __forceinline__ void store4(unsigned char* unit, bool values, int slot, const float (&x)[VW], float inv_scale) {
-  constexpr int D = 32 * VW, PER = 16 / VW;              // lanes of a block
-  const int lane = threadIdx.x & 31, e0 = lane * VW;
+// a lane's elements -> 4-bit codes, and its block's scale (of two lanes), in the unit at `unit`
+template <int D>
+__device__ __forceinline__ void store4(unsigned char* unit, bool values, int slot, int e0, const float (&x)[VW], float inv_scale, bool on) {
   float y[VW];
   unsigned top = 0;                                      // as whole numbers, so that a NaN is the largest
 #pragma unroll
@@ -98,44 +97,50 @@ __device__ __forceinline__ void store4(unsigned char* unit, bool values, int slo
     y[e] = x[e] * inv_scale;
     top = max(top, __float_as_uint(fabsf(y[e])));
   }
-#pragma unroll
-  for (int o = 1; o < PER; o <<= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
-  const unsigned char sb = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(top), 7.f), __NV_SATFINITE, __NV_E4M3);
-  const float s = e4m3_up(sb);
+  top = max(top, __shfl_xor_sync(FULL_MASK, top, 1));
+  constexpr float SEVENTH = 1.f / 7.f;
+  const float a = fminf(__uint_as_float(top), 3e38f), q7 = a * SEVENTH;
+  const unsigned char sb = top > 0x7f800000u
+                               ? (unsigned char)0x7f
+                               : __nv_cvt_float_to_fp8(fmaf(fmaf(-q7, 7.f, a), SEVENTH, q7), __NV_SATFINITE, __NV_E4M3);
+  const float s = e4m3_up(sb), most = 7.f * s, r = s == 0.f ? 0.f : __frcp_rn(s);
   unsigned codes = 0;
 #pragma unroll
   for (int e = 0; e < VW; ++e) {
-    const float q = s == 0.f ? 0.f : fminf(fmaxf(rintf(__fdiv_rn(y[e], s)), -7.f), 7.f);
-    codes |= (unsigned)((int)q + 8) << (4 * e);
+    const float z = fminf(fmaxf(y[e], -most), most), q = z * r;
+    // the whole number in the low bits of a sum with 1.5 * 2^23 (rounded to nearest, ties to even), and 8
+    const float n = fmaf(fmaf(-q, s, z), r, q) + 12582920.f;
+    codes |= (__float_as_uint(n) & 15u) << (4 * e);
   }
-  unsigned char* at = unit + code_at(D, values, slot, e0);
-  if constexpr (VW == 2) *at = (unsigned char)codes;
-  if constexpr (VW == 4) *reinterpret_cast<uint16_t*>(at) = (uint16_t)codes;
-  if constexpr (VW == 8) *reinterpret_cast<uint32_t*>(at) = codes;
-  if (lane % PER == 0) unit[scale_at(D, values, slot, e0 >> 4)] = sb;
+  if (top > 0x7f800000u) codes = 0x11111111u;            // (any: the scale makes them NaN)
+  if (!on) return;
+  *reinterpret_cast<uint32_t*>(unit + code_at(D, values, slot, e0)) = codes;
+  if ((e0 & 8) == 0) unit[scale_at(D, values, slot, e0 >> 4)] = sb;
 }
 
-template <typename T, int VW>
+template <typename T, int D>
 __global__ void __launch_bounds__(ROWS_THREADS) append4_kernel(const __grid_constant__ RotateParams p, bool interleaved, bool wide) {
-  constexpr int D = 32 * VW;
-  __shared__ float s_row[ROWS_WARPS][D];
+  __shared__ float s_row[ROWS_WARPS][32 * VW];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int side = lane / (D / VW), e0 = lane % (D / VW) * VW;
   const int vi = blockIdx.x >= p.first_cta[2] ? 2 : blockIdx.x >= p.first_cta[1] ? 1 : 0;
   const RowView& view = p.v[vi];
   const unsigned unit = (blockIdx.x - p.first_cta[vi]) * ROWS_WARPS + warp;
   const unsigned tu = unit / view.chunks;                // the token
   const bool mine = tu < (unsigned)p.n_tok;
   const int t = mine ? (int)tu : 0;
-  const int h0 = (unit - tu * view.chunks) * view.chunk_heads;
-  const int n = mine ? min(view.heads - h0, view.chunk_heads) : 0;
-  const int e0 = lane * VW;
+  const int h0 = (unit - tu * view.chunks) * view.chunk_heads + side;
+  const int h1 = mine ? min(view.heads, h0 - side + view.chunk_heads) : 0;
+  const int steps = mine ? (h1 - (h0 - side) + SIDE<D> - 1) / SIDE<D> : 0;    // of the warp
   griddep_wait();
   griddep_launch_dependents();
   const uint16_t* in = static_cast<const uint16_t*>(view.in) + t * view.in_ts + h0 * view.in_hs + e0;
-  Words<VW> raw[ROWS_AHEAD];
+  uint4 raw[AHEAD];
 #pragma unroll
-  for (int i = 0; i < ROWS_AHEAD; ++i)
-    if (i < n) raw[i] = load_words<VW>(in + i * view.in_hs, wide);
+  for (int i = 0; i < AHEAD; ++i) {
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (h0 + i * SIDE<D> < h1) raw[i] = load8(in + i * SIDE<D> * view.in_hs, wide);
+  }
 
   write_next_lengths(p);
   if (p.n_tok == 0) return;
@@ -163,19 +168,15 @@ __global__ void __launch_bounds__(ROWS_THREADS) append4_kernel(const __grid_cons
       }
     }
   }
-  float* row = s_row[warp];
+  float* row = s_row[warp] + side * D;
   const int slot = tok.slot & (PG_UNIT - 1);
 #pragma unroll
-  for (int i = 0; i < ROWS_AHEAD; ++i) {
-    if (i >= n) break;
-    const int h = h0 + i;
+  for (int i = 0; i < AHEAD; ++i) {
+    if (i >= steps) break;
+    const int h = h0 + i * SIDE<D>;
+    const bool on = h < h1;
     float x[VW];
-#pragma unroll
-    for (int e = 0; e < VW; e += 2) {
-      const float2 v = Two<T>::up(raw[i].w[e / 2]);
-      x[e] = v.x;
-      x[e + 1] = v.y;
-    }
+    up8<T>(raw[i], x);
     if (turn) {
       float z[VW];                                       // the partners
       if (interleaved) {
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) append4_kernel(const __grid_cons
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < VW; ++e) row[e0 + e] = x[e];
+        for (int e = 0; e < VW; e += 4) *reinterpret_cast<float4*>(row + e0 + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
         __syncwarp();
 #pragma unroll
         for (int e = 0; e < VW; ++e) {
@@ -205,73 +206,83 @@ __global__ void __launch_bounds__(ROWS_THREADS) append4_kernel(const __grid_cons
       }
     }
     if (view.kind == VIEW_ROTATE) {
-      Words<VW> y;
-#pragma unroll
-      for (int e = 0; e < VW; e += 2) y.w[e / 2] = Two<T>::down(x[e], x[e + 1]);
-      store_words<VW>(static_cast<uint16_t*>(view.out) + t * view.out_ts + h * view.out_hs + e0, y, wide);
+      if (on) store8(static_cast<uint16_t*>(view.out) + t * view.out_ts + h * view.out_hs + e0, down8<T>(x), wide);
     } else {
       const bool values = view.kind == VIEW_VALUES;
       const long long u = ((((long long)tok.page * 2 + values) * p.h_kv + h) << (p.page_shift - 4)) + (tok.slot >> 4);
-      store4<VW>(p.pages + u * (9 * D), values, slot, x, 1.0f / p.kv_scale[values * p.h_kv + h]);
+      store4<D>(p.pages + u * (9 * D), values, slot, e0, x, on ? 1.0f / p.kv_scale[values * p.h_kv + h] : 0.f, on);
     }
   }
 }
 
 // A token's keys and values, [2][h_kv][d] of its output row.
-template <typename T, int VW, int PAGES>
+template <typename T, int D, int PAGES>
 __global__ void __launch_bounds__(ROWS_THREADS) read_kernel(const __grid_constant__ RotateParams p) {
-  constexpr int D = 32 * VW;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * VW;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int side = lane / (D / VW), e0 = lane % (D / VW) * VW;
   const RowView& view = p.v[0];
   const unsigned unit = blockIdx.x * ROWS_WARPS + warp;
   const unsigned tu = unit / view.chunks;
   const bool mine = tu < (unsigned)p.n_tok;
   const int t = mine ? (int)tu : 0;
-  const int r0 = (unit - tu * view.chunks) * view.chunk_heads;
-  const int n = mine ? min(view.heads - r0, view.chunk_heads) : 0;   // of 2 h_kv rows
+  const int r0 = (unit - tu * view.chunks) * view.chunk_heads + side;     // of 2 h_kv rows
+  const int r1 = mine ? min(view.heads, r0 - side + view.chunk_heads) : 0;
   griddep_wait();
   griddep_launch_dependents();
   const Token tok = locate(p, t, mine);
   if (!mine || !tok.row) return;
-  uint16_t* out = static_cast<uint16_t*>(view.out) + (long long)t * view.out_ts + (long long)r0 * D + e0;
+  uint16_t* out = static_cast<uint16_t*>(view.out) + (long long)t * view.out_ts + e0;
   const bool held = tok.ok && tok.page >= 0;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    Words<VW> y = {};
-    if (held) {
-      const int which = r0 + i >= p.h_kv, h = r0 + i - which * p.h_kv;
-      const long long row = ((((long long)tok.page * 2 + which) * p.h_kv + h) << p.page_shift) + tok.slot;
-      if constexpr (PAGES == PAGES_SAME) {
-        y = load_words<VW>(reinterpret_cast<const uint16_t*>(p.pages) + row * D + e0, true);
-      } else {
-        float x[VW];
-        const float scale = p.kv_scale[which * p.h_kv + h];
-        if constexpr (PAGES == PAGES_E4M3) {
-          const unsigned char* b = p.pages + row * D + e0;
+  // every row's bytes on their way before the first is turned
+  uint4 raw[AHEAD];
+  float s[AHEAD], scale[AHEAD];
 #pragma unroll
-          for (int e = 0; e < VW; e += 2) {
-            const __half2_raw two = __nv_cvt_fp8x2_to_halfraw2(*reinterpret_cast<const uint16_t*>(b + e), __NV_E4M3);
-            const float2 v = __half22float2(__half2(two));
-            x[e] = v.x * scale;
-            x[e + 1] = v.y * scale;
-          }
-        } else {
-          const unsigned char* u = p.pages + (row >> 4) * (9 * D);
-          const int slot = tok.slot & 15;
-          const unsigned char* c = u + code_at(D, which, slot, e0);
-          unsigned codes;
-          if constexpr (VW == 2) codes = *c;
-          if constexpr (VW == 4) codes = *reinterpret_cast<const uint16_t*>(c);
-          if constexpr (VW == 8) codes = *reinterpret_cast<const uint32_t*>(c);
-          const float s = e4m3_up(u[scale_at(D, which, slot, e0 >> 4)]);
-#pragma unroll
-          for (int e = 0; e < VW; ++e) x[e] = (float)((int)((codes >> (4 * e)) & 15) - 8) * s * scale;
-        }
-#pragma unroll
-        for (int e = 0; e < VW; e += 2) y.w[e / 2] = Two<T>::down(x[e], x[e + 1]);
-      }
+  for (int i = 0; i < AHEAD; ++i) {
+    const int r = r0 + i * SIDE<D>;
+    raw[i] = make_uint4(0, 0, 0, 0);
+    s[i] = scale[i] = 0.f;
+    if (!held || r >= r1) continue;
+    const int which = r >= p.h_kv, h = r - which * p.h_kv;
+    const long long row = ((((long long)tok.page * 2 + which) * p.h_kv + h) << p.page_shift) + tok.slot;
+    if constexpr (PAGES != PAGES_SAME) scale[i] = p.kv_scale[r];
+    if constexpr (PAGES == PAGES_SAME) raw[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.pages) + row * D + e0);
+    if constexpr (PAGES == PAGES_E4M3) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p.pages + row * D + e0);
+      raw[i].x = v.x;
+      raw[i].y = v.y;
     }
-    store_words<VW>(out + (long long)i * D, y, true);
+    if constexpr (PAGES == PAGES_INT4) {
+      const unsigned char* u = p.pages + (row >> 4) * (9 * D);
+      raw[i].x = *reinterpret_cast<const uint32_t*>(u + code_at(D, which, tok.slot & 15, e0));
+      s[i] = e4m3_up(u[scale_at(D, which, tok.slot & 15, e0 >> 4)]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) {
+    const int r = r0 + i * SIDE<D>;
+    if (r >= r1) break;
+    uint4 y = raw[i];
+    if constexpr (PAGES != PAGES_SAME) {
+      float x[VW];
+#pragma unroll
+      for (int e = 0; e < VW; e += 2) {
+        if constexpr (PAGES == PAGES_E4M3) {
+          const uint32_t w = e < 4 ? raw[i].x : raw[i].y;
+          const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (e & 2 ? 16 : 0)), __NV_E4M3)));
+          x[e] = v.x * scale[i];
+          x[e + 1] = v.y * scale[i];
+        } else {
+#pragma unroll
+          for (int k = e; k < e + 2; ++k) {
+            // 2^23 + code, less 2^23 + 8: exact; times the block's scale: exact too
+            const float c = __uint_as_float(0x4b000000u | (raw[i].x >> (4 * k) & 15u)) - 8388616.f;
+            x[k] = c * s[i] * scale[i];
+          }
+        }
+      }
+      y = held ? down8<T>(x) : make_uint4(0, 0, 0, 0);
+    }
+    *reinterpret_cast<uint4*>(out + (long long)r * D) = y;
   }
 }
 
@@ -279,14 +290,15 @@ __global__ void __launch_bounds__(ROWS_THREADS) read_kernel(const __grid_constan
 template <template <typename, int> class F, typename... A>
 cudaError_t by_row(int type, int d, A... a) {
   if (type == HS_BF16)
-    return d == 64 ? F<__nv_bfloat16, 2>::go(a...) : d == 128 ? F<__nv_bfloat16, 4>::go(a...) : F<__nv_bfloat16, 8>::go(a...);
-  return d == 64 ? F<__half, 2>::go(a...) : d == 128 ? F<__half, 4>::go(a...) : F<__half, 8>::go(a...);
+    return d == 64 ? F<__nv_bfloat16, 64>::go(a...) : d == 128 ? F<__nv_bfloat16, 128>::go(a...) : F<__nv_bfloat16, 256>::go(a...);
+  return d == 64 ? F<__half, 64>::go(a...) : d == 128 ? F<__half, 128>::go(a...) : F<__half, 256>::go(a...);
 }
 
 // Rows of a warp: as many as it has places for, fewer while the call has not 32 warps for each of 152 SMs.
-bool split(RotateParams& p, int v, long long* cta) {
+bool split(RotateParams& p, int v, int side, long long* cta) {
   const long long rows = (long long)p.n_tok * p.v[v].heads;
-  p.v[v].chunk_heads = (int)std::min<long long>(std::min<int>(ROWS_AHEAD, p.v[v].heads), std::max<long long>(1, rows / (152 * 32)));
+  const long long each = std::max<long long>(1, rows / (152 * 32 * side));
+  p.v[v].chunk_heads = (int)std::min<long long>(p.v[v].heads, std::min<long long>(AHEAD, each) * side);
   p.v[v].chunks = (p.v[v].heads + p.v[v].chunk_heads - 1) / p.v[v].chunk_heads;
   const long long units = (long long)p.n_tok * p.v[v].chunks;
   p.first_cta[v] = (unsigned)*cta;
@@ -294,39 +306,39 @@ bool split(RotateParams& p, int v, long long* cta) {
   return units <= 0xf0000000LL && *cta <= 0x7fffffffLL;    // counted with 32 bits
 }
 
-template <typename T, int VW>
+template <typename T, int D>
 struct Append4 {
   static cudaError_t go(RotateParams p, bool interleaved, bool wide, cudaStream_t st) {
     long long cta = 0;
     if (p.n_views == 0) p.v[0].heads = p.v[0].chunks = p.v[0].chunk_heads = 1;   // no tokens: next_lengths only
     for (int v = 0; v < 3; ++v) {
       p.first_cta[v] = v ? 0xffffffffu : 0u;
-      if (v < p.n_views && !split(p, v, &cta)) return cudaErrorInvalidConfiguration;
+      if (v < p.n_views && !split(p, v, SIDE<D>, &cta)) return cudaErrorInvalidConfiguration;
     }
-    return launch_pdl(append4_kernel<T, VW>, dim3((unsigned)std::max(1LL, cta)), dim3(ROWS_THREADS), 0, st, p, interleaved, wide);
+    return launch_pdl(append4_kernel<T, D>, dim3((unsigned)std::max(1LL, cta)), dim3(ROWS_THREADS), 0, st, p, interleaved, wide);
   }
 };
-template <typename T, int VW>
+template <typename T, int D>
 struct Read {
   template <typename K>
   static cudaError_t pick(int page_type, K f) {
     const Pages k = pages_kind(page_type);
-    return k == PAGES_INT4 ? f(read_kernel<T, VW, PAGES_INT4>) : k == PAGES_E4M3 ? f(read_kernel<T, VW, PAGES_E4M3>) : f(read_kernel<T, VW, PAGES_SAME>);
+    return k == PAGES_INT4 ? f(read_kernel<T, D, PAGES_INT4>) : k == PAGES_E4M3 ? f(read_kernel<T, D, PAGES_E4M3>) : f(read_kernel<T, D, PAGES_SAME>);
   }
   static cudaError_t go(RotateParams p, int page_type, cudaStream_t st) {
     long long cta = 0;
-    if (!split(p, 0, &cta)) return cudaErrorInvalidConfiguration;
+    if (!split(p, 0, SIDE<D>, &cta)) return cudaErrorInvalidConfiguration;
     return pick(page_type, [&](auto kern) { return launch_pdl(kern, dim3((unsigned)cta), dim3(ROWS_THREADS), 0, st, p); });
   }
 };
-template <typename T, int VW>
+template <typename T, int D>
 struct Prepare {
   static cudaError_t go(int page_type) {
     cudaFuncAttributes fa;
     cudaError_t e = cudaSuccess;
-    if (page_type == HS_INT4) e = cudaFuncGetAttributes(&fa, append4_kernel<T, VW>);
+    if (page_type == HS_INT4) e = cudaFuncGetAttributes(&fa, append4_kernel<T, D>);
     if (e != cudaSuccess) return e;
-    return Read<T, VW>::pick(page_type, [&](auto kern) { return cudaFuncGetAttributes(&fa, kern); });
+    return Read<T, D>::pick(page_type, [&](auto kern) { return cudaFuncGetAttributes(&fa, kern); });
   }
 };
 
