@@ -518,6 +518,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int rr = w.blk * C::ROWS + min(slot * 128 + row, w.b.rows - 1);    // (rows behind the last: as the last)
         const int tok = rr / p.group, g = rr - tok * p.group, h = w.head * p.group + g;
         const int pos = w.r.len + tok;
+        const int ahead = __reduce_min_sync(FULL_MASK, pos);       // the first position of the warp's rows
         const int hi = max(pos + 1, w.r.all), lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
         const bool shaped = p.cap_in != 0.f || p.slopes;
         const float slope = p.slopes ? p.slopes[h] * LOG2_E : 0.f;   // to powers of two
@@ -555,14 +556,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const unsigned off = bad >> (c0 / 16);
             auto unseen = [&](int c) { return c < from || c >= to || (off >> (c / 16) & 1); };
             if constexpr (decltype(capped)::value) {
-              if constexpr (decltype(masked)::value) {     // (what hidden columns hold decides nothing)
-#pragma unroll
-                for (int c = 0; c < 64; ++c)
-                  if (unseen(c)) s[c] = 0;
-              }
               float most[2] = {0.f, 0.f};
 #pragma unroll
-              for (int c = 0; c < 64; c += 2) most[c >> 1 & 1] = max3(most[c >> 1 & 1], fabsf(S(c)), fabsf(S(c + 1)));
+              for (int c = 0; c < 64; c += 2) {
+                if constexpr (decltype(masked)::value)     // (what hidden columns hold decides nothing)
+                  most[c >> 1 & 1] = max3(most[c >> 1 & 1], unseen(c) ? 0.f : fabsf(S(c)), unseen(c + 1) ? 0.f : fabsf(S(c + 1)));
+                else
+                  most[c >> 1 & 1] = max3(most[c >> 1 & 1], fabsf(S(c)), fabsf(S(c + 1)));
+              }
               // (votes of their own: a lane must not pass one over)
               const float far = fmaxf(most[0], most[1]) * fabsf(mul);
               const bool over_half = __any_sync(FULL_MASK, mine_row && !(far <= 0.5f));
@@ -599,6 +600,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if constexpr (decltype(biased)::value) {
               const float far = (float)(n0 + c0 - pos), by = decltype(capped)::value ? 1.f : mul;
               const F2 by2 = two(by, by);
+              if (n0 + c0 + 63 <= ahead) {                 // nobody's position lies within: the distance has one sign
+                const float from = slope * far;
+#pragma unroll
+                for (int c = 0; c < 64; c += 2) {
+                  const F2 b = two(fmaf(slope, (float)c, from), fmaf(slope, (float)(c + 1), from)), x = two(S(c), S(c + 1));
+                  const float2 z = apart(decltype(capped)::value ? add2(x, b) : fma2(x, by2, b));
+                  s[c] = __float_as_uint(z.x);
+                  s[c + 1] = __float_as_uint(z.y);
+                }
+              } else
 #pragma unroll
               for (int c = 0; c < 64; c += 2) {
                 const float2 z = decltype(capped)::value ? make_float2(S(c), S(c + 1)) : apart(mul2(two(S(c), S(c + 1)), by2));
@@ -1180,49 +1191,51 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_attend_join_kernel(cons
   if ((int)blockIdx.y * 32 >= b.rows) return;
   const bool in = row < b.rows;
   const int n = ch.last - cta + 1, c0 = blockIdx.z * 8;
-  float m = -INFINITY, l = 0.f;
+  // all pieces' references first, so that the sums behind them wait for nothing but their own reads
+  auto piece = [&](int j) { return p.ws + ws_piece<C>(cta + j, j == 0); };
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int j = warp; j < n; j += JOIN_WARPS) m = fmaxf(m, in ? piece(j)[C::ROWS * C::D + row] : -INFINITY);
+  s_m[warp][lane] = m;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < JOIN_WARPS; ++k) m = fmaxf(m, s_m[k][lane]);
+  const float mm = m, base = mm == -INFINITY ? 0.f : mm;
+  float l = 0.f;
   float4 acc[8];
 #pragma unroll
   for (int c = 0; c < 8; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
   for (int j = warp; j < n; j += JOIN_WARPS) {
-    const float* at = p.ws + ws_piece<C>(cta + j, j == 0);
+    const float* at = piece(j);
     float4 x[8];
-    const float pm = in ? at[C::ROWS * C::D + row] : -INFINITY, pl = in ? at[C::ROWS * C::D + C::ROWS + row] : 0.f;
 #pragma unroll
     for (int c = 0; c < 8; ++c)
       x[c] = in ? *reinterpret_cast<const float4*>(at + ((size_t)(c0 + c) * C::ROWS + row) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float mm = fmaxf(m, pm), base = mm == -INFINITY ? 0.f : mm;
-    const float keep = exp2f(m - base), w = exp2f(pm - base);
-    m = mm;
-    l = l * keep + pl * w;
+    const float w = in ? exp2f(at[C::ROWS * C::D + row] - base) : 0.f;
+    l += in ? w * at[C::ROWS * C::D + C::ROWS + row] : 0.f;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      acc[c].x = acc[c].x * keep + x[c].x * w;
-      acc[c].y = acc[c].y * keep + x[c].y * w;
-      acc[c].z = acc[c].z * keep + x[c].z * w;
-      acc[c].w = acc[c].w * keep + x[c].w * w;
+      acc[c].x += x[c].x * w;
+      acc[c].y += x[c].y * w;
+      acc[c].z += x[c].z * w;
+      acc[c].w += x[c].w * w;
     }
   }
-  s_m[warp][lane] = m;
   s_l[warp][lane] = l;
 #pragma unroll
   for (int c = 0; c < 8; ++c) s_o[warp][c][lane] = acc[c];
   __syncthreads();
-  float mm = -INFINITY, ll = 0.f;
-#pragma unroll
-  for (int k = 0; k < JOIN_WARPS; ++k) mm = fmaxf(mm, s_m[k][lane]);
-  const float base = mm == -INFINITY ? 0.f : mm;
+  float ll = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < JOIN_WARPS; ++k) {
-    const float w = exp2f(s_m[k][lane] - base);
     const float4 x = s_o[k][warp][lane];
-    ll += w * s_l[k][lane];
-    o.x += w * x.x;
-    o.y += w * x.y;
-    o.z += w * x.z;
-    o.w += w * x.w;
+    ll += s_l[k][lane];
+    o.x += x.x;
+    o.y += x.y;
+    o.z += x.z;
+    o.w += x.w;
   }
   if (!in) return;
   const int rr = ch.blk * C::ROWS + row, tok = rr / p.group, h = ch.head * p.group + rr - tok * p.group;
@@ -1244,7 +1257,8 @@ struct Kernels {
   static cudaError_t launch(const PagedAttendParams& p, const CUtensorMap& map, cudaStream_t st) {
     const cudaError_t e = launch_pdl(paged_attend_kernel<C>, dim3(p.grid), dim3(C::THREADS), C::SMEM, st, p, map);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_attend_join_kernel<C>, dim3(p.grid, C::ROWS / 32, C::D / 32), dim3(32 * JOIN_WARPS), 0, st, p);
+    const int rows = (int)std::min<long long>(C::ROWS, (long long)p.n_tok * p.group);    // of a block, at most
+    return launch_pdl(paged_attend_join_kernel<C>, dim3(p.grid, (rows + 31) / 32, C::D / 32), dim3(32 * JOIN_WARPS), 0, st, p);
   }
 };
 
