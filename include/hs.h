@@ -399,8 +399,9 @@ int hs_indexer_topk_static_error(int32_t device, uint32_t* out);
  * The two-tier cache above takes queries and rows whose positions are already
  * rotated in: hs_rotary_apply rotates them.  Layers that attend to every
  * position, and requests short enough to stay in HBM, use the paged cache:
- * hs_paged_append rotates and stores new keys and values, hs_paged_decode
- * attends one new token per request over them.  None of these calls keeps
+ * hs_paged_append rotates and stores new keys and values, hs_paged_attend attends
+ * the new tokens of prompts over them, hs_paged_decode one new token per request, and
+ * hs_paged_read gives rows back as values.  None of these calls keeps
  * anything from one call for the next but what it writes to the caller's
  * buffers.  Messages of failed
  * calls: hs_last_error(NULL), of the calling thread.
@@ -544,7 +545,7 @@ void hs_paged_destroy(hs_paged_t* h);
  * hs_paged_set_scores — how hs_paged_decode and hs_paged_attend make a query's scores, from the
  * handle's next call on (host memory only; not while another thread uses the handle).  Without it,
  * and with 0 and NULL, a score is s = softmax_scale * q_h . K_n; else
- *   softcap : 0 (none), or in [1e-4, 1e6]:  s becomes softcap * tanh(s / softcap)
+ *   softcap : 0 (none), or in [1e-4, 1e6]:  s becomes softcap * tanh(s / softcap), to 2^-19 of itself
  *   slopes  : NULL, or dev float [h_q], finite, the caller's until the handle is destroyed or given
  *             others:  s then loses slopes[h] * |p - n|, p the query's position
  */
@@ -588,7 +589,8 @@ int hs_paged_append(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
 /*
  * hs_paged_decode — attention of one token per request over its cached positions
  * (stream-ordered, capturable): with N = lengths[r] and the last min(N, window) positions,
- *   o_h = sum_n softmax_n(softmax_scale * q_h . K_n) V_n,   kv head floor(h * h_kv / h_q).
+ *   o_h = sum_n softmax_n(softmax_scale * q_h . K_n) V_n,   kv head floor(h * h_kv / h_q)
+ * (scores with a cap or a bias: hs_paged_set_scores, p = N - 1).
  *   req_ids  : dev int32 [n_req] request ids (the same one may come twice), or NULL for
  *              0 .. n_req-1;  n_req is at most max_requests
  *   lengths  : dev int32 [max_requests], the new token's own position counted
@@ -604,7 +606,7 @@ int hs_paged_append(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
  * (HS_DEVERR_CAPACITY).  Positions on a page whose id is out of range are left out
  * (HS_DEVERR_PAGE).  Rows of a page at and behind the length are never used, whatever
  * they hold.  Scores, the softmax and the sums are in 32 bits; the weights that multiply
- * values are held as two numbers of 16 bits (8-bit pages: as one, off by up to 2^-11 of
+ * values are held as two numbers of 16 bits (8- and 4-bit pages: as one, off by up to 2^-11 of
  * itself).  Weights are at most 2^8 before the division by their sum: values of HS_BF16
  * pages up to 2^97 in magnitude cannot overflow the sums, larger ones may, up to 2^120 only
  * where several positions add up.
@@ -637,6 +639,12 @@ int hs_paged_decode(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
  * page whose id is out of range are left out (HS_DEVERR_PAGE).  Offsets that decrease or leave
  * [0, n_tok] (HS_DEVERR_OFFSETS) give their request no tokens.  n_tok * h_q / h_kv is below
  * 2^31 - 2^16.
+ * Scores, the softmax and the sums are in 32 bits; the weights that multiply values are rounded to 16
+ * bits once (fp16 for HS_E4M3 and HS_INT4 pages).  Rows of a page at and behind N are never used, nor
+ * those before the first position that one of the call's tokens sees, whatever they hold; a key that a
+ * token does not see never reaches it, whatever it holds, but a value that is not finite and is seen by
+ * other tokens of the request may make it NaN.  Large values: as for hs_paged_decode.  The result does
+ * not depend on which page ids hold a request, and is the same bits from call to call.
  */
 int64_t hs_paged_attend_workspace_bytes(const hs_paged_t* h);
 int hs_paged_attend(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* req_ids, int32_t n_tok,

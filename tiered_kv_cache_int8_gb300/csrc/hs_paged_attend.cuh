@@ -1,4 +1,49 @@
-// Attention of many new tokens per request over its paged cache (hs_paged_attend).
+// Attention of many new tokens per request over its paged cache (hs_paged_attend):
+//
+//   s_n = scale q_h . K_n;  s_n <- cap tanh(s_n / cap);  s_n <- s_n - slope_h |p - n|
+//   o_h = sum_n softmax_n(s_n) V_n,  lse_h = ln sum_n exp(s_n)
+//
+// over the positions n that the token at p sees, in one pass with a running maximum m and sum l.
+//
+// Bound: the tensor cores for prompts (4 d flops for a query, a head and a position it sees), HBM for
+// a few tokens over long contexts.  Rows of a block are (token, query head) pairs of one kv head, token
+// by token, whatever the group's size, so that every head of the group shares the rows of keys and
+// values that are read and short prompts fill blocks.
+//
+// Measured (GB300; bf16 products at 1940 TFLOP/s, copies at 6.8 TB/s).  32/8 heads of 128, bf16: 8192
+// tokens on 24576 positions 2.45 ms, 1570 TFLOP/s (81 % of measured); a prompt of 8192 450 us, 1220
+// TFLOP/s, with capped scores 700 us, with a distance bias 602 us; 512 tokens on 30 K positions of 4-bit
+// pages 497 us, 1020 TFLOP/s; 64 requests of 5 tokens on 4 K positions 210 us, 5.1 TB/s; one of them 22
+// us.  (The first kernel, a warp per token and head, took 489 ms for the capped prompt.)
+//
+// A CTA per SM, its warps in roles.  Scores: tcgen05 S = Q K^T, 128 x 128 x d, queries and keys in shared
+// memory, sums in TMEM; weights go back to TMEM as 16-bit numbers and are the first operand of O += P V.
+// Two tiles of 128 rows take turns, so that one's softmax runs while the other's products do; at d = 256,
+// where TMEM holds one tile's sums only, tiles of 64 positions and two buffers of scores do the same.
+//   softmax   a warp per 32 rows, a thread per row: no exchange between threads; the sums are rescaled
+//             only where a score is far above the reference (pa::SLACK), which is rare
+//   products  one warp issues everything, as one, so that descriptors stay in uniform registers: issued
+//             by a lone thread they took longer than the products (8192 tokens: 852 -> 703 us)
+//   copies    a warp: pages by TMA into a ring of stages (keys, values, keys ...), 128-byte swizzled
+//   a look    a warp: values that no row of the block sees become 0 (a weight of 0 would leave a NaN)
+//   queries   a warp: rows of any strides by 16-byte copies into the swizzled tile, for the next piece
+//             while this one ends
+//   8/4 bits  four warps turn rows of those pages into fp16 between two rings (exactly: their scales are
+//             folded into the scores and the output, or, of 4-bit rows, have 4 bits); bf16 queries come
+//             as fp16 under a power of two per row
+// Code size is what the inner loops were made short for: unrolled over a tile's 128 columns, the softmax's
+// and the turning's code (13 KB each) left warps waiting for instructions (4-bit chunks 774 -> 484 us when
+// the turning became a loop, 8192 tokens 703 -> 582 us with the softmax's).
+//
+// Weights are rounded to 16 bits once (bf16 2^-8, fp16 and 8- and 4-bit pages 2^-11 of themselves): the
+// relative error of bf16 outputs is 0.0022 where 32-bit weights give 0.0017; a second part, as one-token
+// attention has, would cost half as much again of the tensor time.  Sums and the softmax are in 32 bits.
+//
+// Work.  Segments (block of rows, kv head) have as many tiles as their last row sees; all tiles of the
+// call, and for each segment the cost of its start, form one sequence, and every CTA takes an equal share
+// of it.  What lies wholly in a share is written out; a segment cut by shares goes to the workspace in
+// pieces (at most two per CTA) that a second kernel joins.  So one request of 5 tokens on 4 K positions
+// and a batch of ragged prompts are spread the same way.  Nothing is kept between calls.
 #ifndef HS_PAGED_ATTEND_CUH_
 #define HS_PAGED_ATTEND_CUH_
 
@@ -396,9 +441,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     M.abort = 0;
     M.begin[4] = 0;
   }
-  if (warp == 0) tmem_alloc(&M.tmem, C::TCOLS);
   griddep_wait();
   griddep_launch_dependents();
+  // (behind the wait: a kernel before this one may still want its columns)
+  if (warp == 0) tmem_alloc(&M.tmem, C::TCOLS);
 
   // ---- the share: blocks before each request, then the cost of a thread's blocks, then the place of its begin
   long long share, mine;

@@ -40,6 +40,15 @@
 // needs no shuffling: queries are loaded in the order in which key bytes come, and
 // output rows leave in that of the value bytes.
 //
+// 4-bit pages come by two plain copies a unit (its keys lie together, and its values).  A lane's keys are 16
+// consecutive bytes of a row; values come by ldmatrix, four elements of two positions in a word, which
+// is the operand's order already.  A code becomes fp16 by one mask and one fused multiply-add, exactly.  16 x 32 K
+// positions over 4-bit pages: 178 us (bf16: 320), 3.4 TB/s; the ALU pipe is 64 % busy, 65 % of the issue slots
+// are used: 500 instructions a unit of 16 positions, half of them for turning codes.
+//
+// Scores with a cap or a bias are kernels of their own (SCORES): the cap by tanh32, the bias from the
+// positions; 16 x 32 K with a cap takes as long as without.
+//
 // Short contexts.  Where no request of the call can have more than a few dozen units (by
 // the table's width or the window), CTAs take whole segments: nothing crosses CTAs, and
 // the second kernel, 3 us on the GPU and 4 of a call through the API, is not launched.

