@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   // ---- the share: blocks before each request, then the cost of a thread's blocks, then the place of its begin
   long long share, mine;
-  int seg;
+  int seg, unsound;
   {
     int* pre = reinterpret_cast<int*>(smem + C::SM_RING);               // n_req + 1
     long long* part = reinterpret_cast<long long*>(smem);               // a sum per warp
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     if (tid == 0) pre[p.n_req] = all;
     if (err && blockIdx.x == 0) set_error(p.dev_error, err);
-    __syncthreads();
+    unsound = __syncthreads_or(err != 0);
     const int chunk = (all + C::THREADS - 1) / C::THREADS;
     const int b0 = min(all, tid * chunk), b1 = min(all, b0 + chunk);
     auto request_at = [&](int b) {               // the last request with pre <= b that has blocks
@@ -1201,7 +1201,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   }
 
   // ---- rows of bad requests
-  for (int i = blockIdx.x; i < p.n_req; i += gridDim.x) {
+  for (int i = unsound ? blockIdx.x : p.n_req; i < p.n_req; i += gridDim.x) {
     unsigned e = 0;
     const Request r = request_of(p, i, &e);
     if (r.req >= 0 || r.n == 0) continue;

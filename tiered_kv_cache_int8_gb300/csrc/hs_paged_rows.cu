@@ -13,6 +13,7 @@
 // Bound: instructions (70 to 75 % of the issue slots).  Measured (GB300): 23.6 K ragged tokens of 8 + 8
 // heads of 128, fp16, stored in 57 us (a copy of the bytes: 19 us; 86 us with four elements a lane and
 // divisions) and read back in 34 us (19 us); 16 tokens 2.8 us each way.
+#include "hs_paged_attention.cuh"
 #include "hs_paged_place.cuh"
 
 namespace hs {
@@ -105,11 +106,17 @@ __device__ __forceinline__ void store4(unsigned char* unit, bool values, int slo
   const unsigned char sb = top > 0x7f800000u
                                ? (unsigned char)0x7f
                                : __nv_cvt_float_to_fp8(fmaf(fmaf(-q7, 7.f, a), SEVENTH, q7), __NV_SATFINITE, __NV_E4M3);
-  const float s = e4m3_up(sb), most = 7.f * s, r = s == 0.f ? 0.f : __frcp_rn(s);
+  const float s = e4m3_up(sb), r = s == 0.f ? 0.f : __frcp_rn(s);
+  // up to 464 * 7 the scale keeps quotients below 7.5; beyond, it stays at 448 and values are clamped
+  if (__any_sync(FULL_MASK, __uint_as_float(top) > 3248.f)) {
+    const float most = 7.f * s;
+#pragma unroll
+    for (int e = 0; e < VW; ++e) y[e] = fminf(fmaxf(y[e], -most), most);
+  }
   unsigned codes = 0;
 #pragma unroll
   for (int e = 0; e < VW; ++e) {
-    const float z = fminf(fmaxf(y[e], -most), most), q = z * r;
+    const float z = y[e], q = z * r;
     // the whole number in the low bits of a sum with 1.5 * 2^23 (rounded to nearest, ties to even), and 8
     const float n = fmaf(fmaf(-q, s, z), r, q) + 12582920.f;
     codes |= (__float_as_uint(n) & 15u) << (4 * e);
@@ -237,12 +244,14 @@ __global__ void __launch_bounds__(ROWS_THREADS) read_kernel(const __grid_constan
   const bool held = tok.ok && tok.page >= 0;
   // every row's bytes on their way before the first is turned
   uint4 raw[AHEAD];
-  float s[AHEAD], scale[AHEAD];
+  uint32_t s[AHEAD];               // of a 4-bit row: the block's scale, twice
+  float scale[AHEAD];
 #pragma unroll
   for (int i = 0; i < AHEAD; ++i) {
     const int r = r0 + i * SIDE<D>;
     raw[i] = make_uint4(0, 0, 0, 0);
-    s[i] = scale[i] = 0.f;
+    s[i] = 0;
+    scale[i] = 0.f;
     if (!held || r >= r1) continue;
     const int which = r >= p.h_kv, h = r - which * p.h_kv;
     const long long row = ((((long long)tok.page * 2 + which) * p.h_kv + h) << p.page_shift) + tok.slot;
@@ -256,7 +265,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) read_kernel(const __grid_constan
     if constexpr (PAGES == PAGES_INT4) {
       const unsigned char* u = p.pages + (row >> 4) * (9 * D);
       raw[i].x = *reinterpret_cast<const uint32_t*>(u + code_at(D, which, tok.slot & 15, e0));
-      s[i] = e4m3_up(u[scale_at(D, which, tok.slot & 15, e0 >> 4)]);
+      s[i] = 0x101u * u[scale_at(D, which, tok.slot & 15, e0 >> 4)];
     }
   }
 #pragma unroll
@@ -266,20 +275,24 @@ __global__ void __launch_bounds__(ROWS_THREADS) read_kernel(const __grid_constan
     uint4 y = raw[i];
     if constexpr (PAGES != PAGES_SAME) {
       float x[VW];
+      if constexpr (PAGES == PAGES_E4M3) {
 #pragma unroll
-      for (int e = 0; e < VW; e += 2) {
-        if constexpr (PAGES == PAGES_E4M3) {
+        for (int e = 0; e < VW; e += 2) {
           const uint32_t w = e < 4 ? raw[i].x : raw[i].y;
           const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (e & 2 ? 16 : 0)), __NV_E4M3)));
           x[e] = v.x * scale[i];
           x[e + 1] = v.y * scale[i];
-        } else {
+        }
+      } else {
+        // code times the block's scale as fp16, 2^-6 as large: exact; then one product in 32 bits
+        uint32_t a[4];               // elements (0, 4), (1, 5), (2, 6), (3, 7)
+        pa::int4x8_to_half2(raw[i].x, pa::int4_scale(pa::e4m3x2_to_half2((uint16_t)s[i])), a);
+        const float by = scale[i] * pa::INT4_SHIFT;
 #pragma unroll
-          for (int k = e; k < e + 2; ++k) {
-            // 2^23 + code, less 2^23 + 8: exact; times the block's scale: exact too
-            const float c = __uint_as_float(0x4b000000u | (raw[i].x >> (4 * k) & 15u)) - 8388616.f;
-            x[k] = c * s[i] * scale[i];
-          }
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&a[e]));
+          x[e] = v.x * by;
+          x[e + 4] = v.y * by;
         }
       }
       y = held ? down8<T>(x) : make_uint4(0, 0, 0, 0);
