@@ -94,9 +94,10 @@ struct Cfg {
   static constexpr int SM_META = (SM_RAW + RAWS * RAW + 1023) / 1024 * 1024;
   static constexpr size_t SMEM = 1024 + SM_META + sizeof(int) * 256;
   static constexpr int PIECE = ROWS * D + 2 * ROWS;            // floats of a piece: o [d / 4][row][4], m, l
-  // of a segment on top of its tiles, in tiles: queries, the first scores, output (6 us; a tile takes 1.6 us
-  // at d = 128, 1 us at 64 and, of 64 positions, at 256)
-  static constexpr int SEGMENT_COST = D == 128 ? 4 : 6;
+  // of a segment on top of its tiles, in tiles: queries, the first scores, output: some 6 us (where rows are
+  // turned, 10), of tiles of 1.6 us at d = 128 and 1 us, of 64 positions, at 256; with 4 and 7 a prompt of
+  // 8192 over 4-bit pages takes 815 and 680 us, with 3 and 5 one over 16-bit pages 494 and 456
+  static constexpr int SEGMENT_COST = D == 64 ? 4 : D == 128 && !CONV ? 5 : 7;
 };
 
 struct Meta {
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int rr = w.blk * C::ROWS + min(slot * 128 + row, w.b.rows - 1);    // (rows behind the last: as the last)
         const int tok = rr / p.group, g = rr - tok * p.group, h = w.head * p.group + g;
         const int pos = w.r.len + tok;
-        const int ahead = __reduce_min_sync(FULL_MASK, pos);       // the first position of the warp's rows
+        const int ahead = __reduce_min_sync(FULL_MASK, pos), behind = __reduce_max_sync(FULL_MASK, pos);   // of the warp's rows
         const int hi = max(pos + 1, w.r.all), lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
         const bool shaped = p.cap_in != 0.f || p.slopes;
         const float slope = p.slopes ? p.slopes[h] * LOG2_E : 0.f;   // to powers of two
@@ -646,11 +647,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if constexpr (decltype(biased)::value) {
               const float far = (float)(n0 + c0 - pos), by = decltype(capped)::value ? 1.f : mul;
               const F2 by2 = two(by, by);
-              if (n0 + c0 + 63 <= ahead) {                 // nobody's position lies within: the distance has one sign
-                const float from = slope * far;
+              // where nobody's position lies within, the distance has one sign
+              const bool past = n0 + c0 + 63 <= ahead;
+              if (past || n0 + c0 >= behind) {
+                const float slope_n = past ? slope : -slope, from = slope_n * far;
 #pragma unroll
                 for (int c = 0; c < 64; c += 2) {
-                  const F2 b = two(fmaf(slope, (float)c, from), fmaf(slope, (float)(c + 1), from)), x = two(S(c), S(c + 1));
+                  const F2 b = two(fmaf(slope_n, (float)c, from), fmaf(slope_n, (float)(c + 1), from)), x = two(S(c), S(c + 1));
                   const float2 z = apart(decltype(capped)::value ? add2(x, b) : fma2(x, by2, b));
                   s[c] = __float_as_uint(z.x);
                   s[c + 1] = __float_as_uint(z.y);
