@@ -11,10 +11,10 @@
 // values that are read and short prompts fill blocks.
 //
 // Measured (GB300; bf16 products at 1940 TFLOP/s, copies at 6.8 TB/s).  32/8 heads of 128, bf16: 8192
-// tokens on 24576 positions 2.45 ms, 1570 TFLOP/s (81 % of measured); a prompt of 8192 450 us, 1220
-// TFLOP/s, with capped scores 700 us, with a distance bias 602 us; 512 tokens on 30 K positions of 4-bit
-// pages 497 us, 1020 TFLOP/s; 64 requests of 5 tokens on 4 K positions 210 us, 5.1 TB/s; one of them 22
-// us.  (The first kernel, a warp per token and head, took 489 ms for the capped prompt.)
+// tokens on 24576 positions 2.48 ms, 1550 TFLOP/s (80 % of measured); a prompt of 8192 453 us, 1215
+// TFLOP/s, with capped scores 705 us, with a distance bias 610 us, over 8-bit pages 645 us, 4-bit ones 675;
+// 512 tokens on 30 K positions of 4-bit pages 500 us, 1015 TFLOP/s; 64 requests of 5 tokens on 4 K
+// positions 205 us, 5.3 TB/s; one of them 22 us.  (The first kernel, a warp per token and head, took 489 ms for the capped prompt.)
 //
 // A CTA per SM, its warps in roles.  Scores: tcgen05 S = Q K^T, 128 x 128 x d, queries and keys in shared
 // memory, sums in TMEM; weights go back to TMEM as 16-bit numbers and are the first operand of O += P V.
@@ -96,7 +96,7 @@ struct Cfg {
   static constexpr int PIECE = ROWS * D + 2 * ROWS;            // floats of a piece: o [d / 4][row][4], m, l
   // of a segment on top of its tiles, in tiles: queries, the first scores, output: some 6 us (where rows are
   // turned, 10), of tiles of 1.6 us at d = 128 and 1 us, of 64 positions, at 256; with 4 and 7 a prompt of
-  // 8192 over 4-bit pages takes 815 and 680 us, with 3 and 5 one over 16-bit pages 494 and 456
+  // 8192 over 4-bit pages takes 815 and 675 us, with 3 and 5 one over 16-bit pages 494 and 456
   static constexpr int SEGMENT_COST = D == 64 ? 4 : D == 128 && !CONV ? 5 : 7;
 };
 
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int rr = w.blk * C::ROWS + min(slot * 128 + row, w.b.rows - 1);    // (rows behind the last: as the last)
         const int tok = rr / p.group, g = rr - tok * p.group, h = w.head * p.group + g;
         const int pos = w.r.len + tok;
-        const int ahead = __reduce_min_sync(FULL_MASK, pos), behind = __reduce_max_sync(FULL_MASK, pos);   // of the warp's rows
+        const int ahead = __reduce_min_sync(FULL_MASK, pos);       // the first position of the warp's rows
         const int hi = max(pos + 1, w.r.all), lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
         const bool shaped = p.cap_in != 0.f || p.slopes;
         const float slope = p.slopes ? p.slopes[h] * LOG2_E : 0.f;   // to powers of two
@@ -647,13 +647,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if constexpr (decltype(biased)::value) {
               const float far = (float)(n0 + c0 - pos), by = decltype(capped)::value ? 1.f : mul;
               const F2 by2 = two(by, by);
-              // where nobody's position lies within, the distance has one sign
-              const bool past = n0 + c0 + 63 <= ahead;
-              if (past || n0 + c0 >= behind) {
-                const float slope_n = past ? slope : -slope, from = slope_n * far;
+              if (n0 + c0 + 63 <= ahead) {                 // nobody's position lies within: the distance has one sign
+                const float from = slope * far;
 #pragma unroll
                 for (int c = 0; c < 64; c += 2) {
-                  const F2 b = two(fmaf(slope_n, (float)c, from), fmaf(slope_n, (float)(c + 1), from)), x = two(S(c), S(c + 1));
+                  const F2 b = two(fmaf(slope, (float)c, from), fmaf(slope, (float)(c + 1), from)), x = two(S(c), S(c + 1));
                   const float2 z = apart(decltype(capped)::value ? add2(x, b) : fma2(x, by2, b));
                   s[c] = __float_as_uint(z.x);
                   s[c + 1] = __float_as_uint(z.y);
