@@ -11,8 +11,8 @@
 // rows may hold but none is given: levels that are symmetric about zero keep signs fair.
 //
 // Bound: instructions (70 to 75 % of the issue slots).  Measured (GB300): 23.6 K ragged tokens of 8 + 8
-// heads of 128, fp16, stored in 57 us (a copy of the bytes: 19 us; 86 us with four elements a lane and
-// divisions) and read back in 34 us (19 us); 16 tokens 2.8 us each way.
+// heads of 128, fp16, stored in 54 us (a copy of the bytes: 19 us; 86 us with four elements a lane and
+// divisions) and read back in 33 us (19 us); 16 tokens 2.8 us each way.
 #include "hs_paged_attention.cuh"
 #include "hs_paged_place.cuh"
 
