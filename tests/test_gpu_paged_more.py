@@ -569,6 +569,80 @@ def test_a_request_moves_to_the_two_tier_cache():
     two.close()
 
 
+# ---- offsets of more than 32 bits -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3", "int4"])
+def test_pages_behind_32_bits(kv):
+    # a pool of more than 2^32 bytes (of 16-bit pages: elements), a request on its last pages and one on its first
+    torch, pm = T(), M()
+    from tiered_kv_cache_int8_gb300 import PagedKVCache
+    hq, hk, d, page, n_pages = 16, 8, 128, 64, 66000
+    ks = None if kv == "bf16" else torch.full((1, 2, hk), 0.01 if kv == "e4m3" else 0.5, device="cuda")
+    c = PagedKVCache(n_layers=1, n_pages=n_pages, page_size=page, max_requests=2, max_pages=16, h_q=hq, h_kv=hk, d=d,
+                     kv_dtype=pm.DT.get(kv, kv), kv_scale=ks)
+    assert c.pages.numel() > 1 << 32
+    held, new = [700, 90], [70, 40]
+    c.page_table[0, :14] = torch.arange(n_pages - 1, n_pages - 15, -1, device="cuda", dtype=torch.int32)
+    c.page_table[1, :4] = torch.arange(4, device="cuda", dtype=torch.int32)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    for r in range(2):
+        pm.fill(c, 0, r, 0, held[r], g)
+    c.set_lengths(ints(held))
+    k, v = (torch.randn(110, hk, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    c.append(0, k, v, tok_offsets=offsets(new))
+    check_attend(c, queries(110, hq, d, "bf16"), held, new)
+    c.commit()
+    check_decode(c, queries(2, hq, d, "bf16", 1), [770, 130])
+    rows = c.read(0, 70, req_ids=ints([0]), starts=ints([700, 0]))
+    want, _ = pm.rows_of(c, 0, 0, 770)
+    pm.within(rows, want[700:], pm.HALF_STEP[torch.bfloat16] * want[700:].abs() * (1 + 2.0 ** -12), "rows")
+    # what was stored is what was given: to its own type, to e4m3's half a step (and the type's), to half of a 4-bit one
+    x = torch.stack([k[:70], v[:70]], 1).double()
+    amax = x.unflatten(-1, (-1, 16)).abs().amax(-1, keepdim=True).expand(-1, -1, -1, -1, 16).flatten(-2)
+    tol = {"bf16": 0 * x, "e4m3": x.abs() * 2.0 ** -4 + 0.01 * 2.0 ** -10, "int4": amax * (0.5 / 7) * 1.0625 + 1e-6}[kv]
+    pm.within(want[700:], x, tol * (1 + 2.0 ** -10), "stored rows")
+    assert c.device_error() == 0
+
+
+def test_rows_of_a_call_behind_31_bits():
+    # more than 2^31 elements of queries, outputs and rows read: 4096 requests that share their pages
+    torch, pm = T(), M()
+    from tiered_kv_cache_int8_gb300 import PagedKVCache
+    R, n, hq, hk, d, page = 4096, 130, 64, 16, 64, 64
+    c = PagedKVCache(n_layers=1, n_pages=8, page_size=page, max_requests=R, max_pages=4, h_q=hq, h_kv=hk, d=d)
+    c.page_table.copy_(torch.arange(4, device="cuda", dtype=torch.int32).expand(R, 4))
+    pm.fill(c, 0, 0, 0, 170, torch.Generator(device="cuda").manual_seed(3))
+    c.set_lengths(torch.full((R,), 40, dtype=torch.int32, device="cuda"))
+    q = queries(n, hq, d, "bf16").repeat(R, 1, 1)
+    assert q.numel() > 1 << 31
+    ends = torch.arange(R + 1, dtype=torch.int32, device="cuda") * n
+    out, lse = c.attend(0, q, tok_offsets=ends, return_lse=True)
+    pos = torch.arange(40, 40 + n, device="cuda")
+    for r in (0, R // 2, R - 1):
+        rows = slice(r * n, (r + 1) * n)
+        want, wl, tol, tl = pm.attend(c, 0, r, q[rows], pos, 40 + n)
+        pm.within(lse[rows], wl, tl, f"lse of request {r}")
+        pm.within(out[rows], want, tol, f"out of request {r}")
+    del q, out, lse
+    rows = c.read(0, R * 170 * 2, tok_offsets=torch.arange(R, 2 * R + 1, dtype=torch.int32, device="cuda") * 170,
+                  starts=torch.zeros(R, dtype=torch.int32, device="cuda"))
+    want, _ = pm.rows_of(c, 0, 0, 170)
+    assert rows.numel() > 1 << 31
+    for r in (R, 2 * R - 1):                       # (rows before the first offset are nobody's)
+        assert torch.equal(rows[r * 170:(r + 1) * 170].double(), want)
+    del rows
+    # rows far apart
+    big = torch.empty(10, 1 << 28, dtype=torch.bfloat16, device="cuda")
+    few = c.read(0, 10, req_ids=ints([R - 1]), starts=torch.zeros(R, dtype=torch.int32, device="cuda"),
+                 out=big[:, :2 * hk * d].unflatten(1, (2, hk, d)))
+    assert torch.equal(few.double(), want[:10])
+    q = big[:, 4096:4096 + hq * d].unflatten(1, (hq, d))
+    q.copy_(queries(10, hq, d, "bf16", 7))
+    got = c.attend(0, q, req_ids=ints([R - 1]), return_lse=True)
+    check_attend(c, q, [40] * R, [10], ids=[R - 1], got=got)
+    assert c.device_error() == 0
+
+
 # ---- together -------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("typ, kv, d", [("bf16", "bf16", 128), ("fp16", "int4", 64), ("bf16", "int4", 128), ("bf16", "e4m3", 256)])
