@@ -643,6 +643,28 @@ def test_rows_of_a_call_behind_31_bits():
     assert c.device_error() == 0
 
 
+@pytest.mark.parametrize("kv", ["bf16", "int4"])
+@pytest.mark.parametrize("window", [0, 1000])
+def test_the_last_positions_of_the_longest_request(kv, window):
+    # 2^22 positions, most of them on one page that they share
+    torch, pm = T(), M()
+    from tiered_kv_cache_int8_gb300 import PagedKVCache
+    N, page, hq, d = 1 << 22, 256, 4, 64
+    c = PagedKVCache(n_layers=1, n_pages=12, page_size=page, max_requests=1, max_pages=N // page, h_q=hq, h_kv=1, d=d, window=window,
+                     kv_dtype=pm.DT.get(kv, kv), kv_scale=None if kv == "bf16" else torch.full((1, 2, 1), 0.5, device="cuda"),
+                     softcap=20.0, slopes=pm.slopes_of(hq))
+    c.page_table.zero_()
+    c.page_table[0, -10:] = torch.arange(1, 11, device="cuda", dtype=torch.int32)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    pm.fill(c, 0, 0, 0, page, g)
+    pm.fill(c, 0, 0, N - 10 * page, N, g)
+    c.set_lengths(ints([N - 40]))
+    check_attend(c, queries(40, hq, d, "bf16"), [N - 40], [40])
+    c.set_lengths(ints([N]))
+    check_decode(c, queries(1, hq, d, "bf16", 1), [N])
+    assert c.device_error() == 0
+
+
 # ---- together -------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("typ, kv, d", [("bf16", "bf16", 128), ("fp16", "int4", 64), ("bf16", "int4", 128), ("bf16", "e4m3", 256)])
