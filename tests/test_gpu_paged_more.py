@@ -445,6 +445,84 @@ def test_append_4bit_nan_infinity_and_border_values():
     assert torch.equal(c.pages, want)
 
 
+def quiet_rows(n, hk, d, typ, ks, seed):
+    """Rows [n, 2, hk, d] whose blocks' largest |x / kv_scale| lies between 2^-12 and 2^-2: near every border of the
+    subnormal scales k 2^-9 and of the first normal ones, and anywhere between; ks a power of two."""
+    torch, pm = T(), M()
+    g = torch.Generator(device="cuda").manual_seed(seed + 41)
+    blocks = n * 2 * hk * (d // 16)
+    # s changes at amax / 7 = (k + 1/2) 2^-9, codes of the largest element at |x| = 7.5 s: there, one step of the type up and down
+    k = torch.arange(0, 16, device="cuda", dtype=torch.float64)
+    edges = torch.cat([7 * (2 * k + 1) * 2.0 ** -10, 7.5 * k[1:] * 2.0 ** -9, 7 * k[1:] * 2.0 ** -9])
+    step = 1 + 2 * pm.HALF_STEP[pm.DT[typ]]
+    edges = torch.cat([edges, edges * step, edges / step])
+    top = torch.exp2(torch.rand(blocks, generator=g, device="cuda", dtype=torch.float64) * 10 - 12)
+    near = torch.randint(0, 2 * len(edges), (blocks,), generator=g, device="cuda")
+    top = torch.where(near < len(edges), edges[near.clamp(max=len(edges) - 1)], top)
+    x = torch.rand(blocks, 16, generator=g, device="cuda", dtype=torch.float64) * 2 - 1
+    x[:, 0], x[:, 1] = 1, -1
+    x = x.gather(1, torch.rand(blocks, 16, generator=g, device="cuda").argsort(1))
+    x[::2] *= torch.randint(0, 2, (len(x[::2]), 1), generator=g, device="cuda") * 2 - 1
+    return ((x * top[:, None]).view(n, 2, hk, d) * ks.double()[None, :, :, None]).to(pm.DT[typ])
+
+
+@pytest.mark.parametrize("typ, d, hk, page", [("bf16", 64, 3, 16), ("bf16", 128, 8, 64), ("bf16", 256, 2, 32), ("fp16", 64, 1, 256),
+                                              ("fp16", 128, 2, 16), ("fp16", 256, 3, 128)])
+def test_append_4bit_codes_of_quiet_rows(typ, d, hk, page):
+    # below 2^-6 the scales of blocks are multiples of 2^-9, whose rounding leaves quotients of up to 10.5: codes stay in +-7
+    torch, pm = T(), M()
+    held, new = [0, 17, 5], [40, 333, 64]
+    c = pm.make(3, hk, hk, d, page, typ, "int4", held, extra_pages=25, power_of_two=True)
+    c.set_lengths(ints(held))
+    n = sum(new)
+    rows = quiet_rows(n, hk, d, typ, c.kv_scale[0], d + hk)
+    pos = torch.cat([torch.arange(a, a + b, device="cuda") for a, b in zip(held, new)])
+    req = torch.cat([torch.full((b,), r, device="cuda") for r, b in enumerate(new)])
+    want = c.pages.clone()
+    code, scale = pm.quantise(rows, c.kv_scale[0])
+    assert len(scale.unique()) > 15 and int(scale.min()) == 0 and int(code.min()) == 1 and int(code.max()) == 15
+    pm.put4(want[0], c.page_table[req, pos // page], pos % page, code, scale)
+    c.append(0, rows[:, 0], rows[:, 1], tok_offsets=offsets(new))
+    assert torch.equal(c.pages, want)
+    # and what a reader gets: a code of 4 bits, scales of 4 and a power of two, exact in either type
+    value = (code.double() - 8) * scale.contiguous().view(torch.float8_e4m3fn).double() * c.kv_scale[0].double()[None, :, :, None]
+    assert torch.equal(c.read(0, n, tok_offsets=offsets(new)).double(), value)
+    assert c.device_error() == 0
+
+
+@pytest.mark.parametrize("sigma", [0.005, 0.01, 0.02, 0.03, 0.05, 0.2])
+@pytest.mark.parametrize("d, rot, inter", [(64, 64, False), (128, 128, True), (256, 64, False)])
+def test_append_4bit_quiet_rows_rotated(sigma, d, rot, inter):
+    # normal rows under kv_scale 1: every element within half a step of its block's scale, or, where a scale rounded down
+    # leaves the largest above 7 of it, within what is cut off there
+    torch, pm = T(), M()
+    from tiered_kv_cache_int8_gb300 import PagedKVCache, Rotary
+    hk, n = 4, 300
+    R = Rotary(rot, interleaved=inter)
+    c = PagedKVCache(n_layers=1, n_pages=20, page_size=16, max_requests=1, max_pages=20, h_q=hk, h_kv=hk, d=d, kv_dtype="int4",
+                     kv_scale=torch.ones(1, 2, hk, device="cuda"), rotary=R)
+    c.reserve(0, n)
+    g = torch.Generator(device="cuda").manual_seed(d)
+    q, k, v = ((torch.randn(n, hk, d, generator=g, device="cuda") * sigma).bfloat16() for _ in range(3))
+    offs, pos = ints([0, n]), torch.arange(n, device="cuda")
+    c.append(0, k, v, q=q, tok_offsets=offs)
+    kr, tol = plain.rotate(k, pos.int(), plain.frequencies(rot), 1.0, inter)
+    got, _ = pm.rows_of(c, 0, 0, n)
+    units = c.pages[0][c.page_table[0, pos // 16].long(), :, :, 0]
+    for w, (x, t) in enumerate(((kr, tol), (v.double(), torch.zeros_like(tol)))):
+        _, at = (p[w].to(x.device) for p in pm.places(d))
+        s = units[:, w].gather(-1, at[pos % 16][:, None, :].expand(n, hk, d)).contiguous().view(torch.float8_e4m3fn).double()
+        wide = lambda y: y.unflatten(-1, (-1, 16)).amax(-1, keepdim=True).expand(n, hk, d // 16, 16).flatten(-2)   # noqa: E731
+        top, slack = wide(x.abs()), wide(t + 2.0 ** -22 * x.abs())
+        # the scale: half a step of e4m3, relative where it is normal, of 2^-9 below
+        assert ((s - top / 7).abs() <= (top / 7 * 2.0 ** -4).clamp(min=2.0 ** -10) * (1 + 2.0 ** -20) + slack).all()
+        off = (got[:, w] - x).abs()
+        assert (off <= torch.maximum(s * (0.5 + 2.0 ** -20), top - 7 * s) + 2 * slack).all()
+        assert (got[:, w] * x >= -(slack * s)).all()                  # no element's sign turns
+    assert torch.equal(c.read(0, n, tok_offsets=offs, starts=ints([0])).double(), got)
+    assert c.device_error() == 0
+
+
 @pytest.mark.parametrize("d, rot, inter, shift", [(128, 128, False, 0), (64, 32, True, 0), (256, 64, False, 0), (128, 128, True, 1),
                                                   (64, 6, False, 1), (256, 250, False, 0)])
 def test_append_4bit_rotated(d, rot, inter, shift):

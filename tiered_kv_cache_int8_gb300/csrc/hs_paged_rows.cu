@@ -6,9 +6,11 @@
 // (code - 8) s kv_scale.  Both quotients are rounded as divisions are, so that the codes are
 // those of the formula: q = a y with y the rounded reciprocal, then q + (a - q b) y, the
 // remainder exact in a fused multiply-add.  (No quotient that is not a half itself is within
-// 2^-24 of one: halves times s have 8 bits.)  A scale rounded down by up to 2^-4 leaves |x' / s|
-// up to 7.47: clamped, still within half a step.  7 / amax would waste the code 0 (-8), which
-// rows may hold but none is given: levels that are symmetric about zero keep signs fair.
+// 2^-24 of one: halves times s have 8 bits.)  A normal scale is rounded down by 2^-4 of itself at most,
+// which leaves |x' / s| below 7.5 and every element within half a step; one below 2^-6 is a multiple
+// k 2^-9, rounded by up to half of 2^-9, which leaves up to 7 (1 + 1 / 2k), 10.5 at k = 1: clamped to 7,
+// up to 3.5 steps off.  7 / amax would waste the code 0 (-8), which rows may hold but none is given:
+// levels that are symmetric about zero keep signs fair.
 //
 // Bound: instructions (70 to 75 % of the issue slots).  Measured (GB300): 23.6 K ragged tokens of 8 + 8
 // heads of 128, fp16, stored in 54 us (a copy of the bytes: 19 us; 86 us with four elements a lane and
@@ -107,8 +109,9 @@ __device__ __forceinline__ void store4(unsigned char* unit, bool values, int slo
                                ? (unsigned char)0x7f
                                : __nv_cvt_float_to_fp8(fmaf(fmaf(-q7, 7.f, a), SEVENTH, q7), __NV_SATFINITE, __NV_E4M3);
   const float s = e4m3_up(sb), r = s == 0.f ? 0.f : __frcp_rn(s);
-  // up to 464 * 7 the scale keeps quotients below 7.5; beyond, it stays at 448 and values are clamped
-  if (__any_sync(FULL_MASK, __uint_as_float(top) > 3248.f)) {
+  // a normal scale keeps quotients below 7.5 up to 464 * 7; beyond, it stays at 448, and below 2^-6 (bytes 1 to
+  // 7) it may be a third too small: there values are clamped (code 16 would be stored as 0, the other sign)
+  if (__any_sync(FULL_MASK, __uint_as_float(top) > 3248.f || (unsigned)(sb - 1) < 7u)) {
     const float most = 7.f * s;
 #pragma unroll
     for (int e = 0; e < VW; ++e) y[e] = fminf(fmaxf(y[e], -most), most);
