@@ -637,8 +637,8 @@ int hs_paged_decode(hs_paged_t* h, int32_t layer, int32_t n_req, const int32_t* 
  * their lse is written.  A request with a bad id (HS_DEVERR_REQ_RANGE), or with a length below 0 or
  * tokens past max_pages * page_size (HS_DEVERR_CAPACITY), gives out = 0, lse = -inf.  Positions on a
  * page whose id is out of range are left out (HS_DEVERR_PAGE).  Offsets that decrease or leave
- * [0, n_tok] (HS_DEVERR_OFFSETS) give their request no tokens.  n_tok * h_q / h_kv is below
- * 2^31 - 2^16.
+ * [0, n_tok] (HS_DEVERR_OFFSETS) give their request no tokens; where the others still claim more than
+ * n_tok rows between them, no request gets any.  n_tok * h_q / h_kv is below 2^31 - 2^16.
  * Scores, the softmax and the sums are in 32 bits; the weights that multiply values are rounded to 16
  * bits once (fp16 for HS_E4M3 and HS_INT4 pages).  Rows of a page at and behind N are never used, nor
  * those before the first position that one of the call's tokens sees, whatever they hold; a key that a

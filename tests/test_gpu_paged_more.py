@@ -184,6 +184,33 @@ def test_attend_skips_bad_requests_pages_and_offsets():
         assert (out[54:] == 7).all()
 
 
+def test_attend_offsets_that_claim_rows_twice():
+    # decreasing offsets may give many requests the same rows: refused as a whole (the work would have no bound)
+    torch, pm = T(), M()
+    from tiered_kv_cache_int8_gb300 import hs
+    for d, kv in ((64, "bf16"), (128, "int4"), (256, "bf16")):
+        R, n = 9, 150
+        c = pm.make(R, 4, 2, d, 32, "bf16", kv, [n] * R)
+        c.set_lengths(ints([0] * R))
+        q = queries(n, 4, d, "bf16")
+        out = torch.full((n, 4, d), 7.0, device="cuda").bfloat16()
+        twice = ints([0, n] * 5)
+        ids = ints([0, 1, 2, 3, 77, 5, 6, 7, 8])                  # (a bad request's rows are not cleared either)
+        c.attend(0, q, req_ids=ids, tok_offsets=twice, out=out)
+        assert c.device_error() == hs.HS_DEVERR_OFFSETS | hs.HS_DEVERR_REQ_RANGE
+        assert (out == 7).all()
+        # where the rows suffice, requests with sound offsets keep theirs
+        c._error.zero_()
+        some = [0, 20, 999, 30, 60, 60, 140, 140, 140, 140]
+        got, lse = c.attend(0, q, tok_offsets=ints(some), out=out, return_lse=True)
+        assert c.device_error() == hs.HS_DEVERR_OFFSETS
+        assert (out[20:30] == 7).all() and (out[140:] == 7).all()
+        for r in (0, 3, 5):
+            rows = slice(some[r], some[r + 1])
+            check_attend(c, q[rows], [0] * R, [some[r + 1] - some[r]], ids=[r], got=(out[rows], lse[rows]))
+        check_attend(c, q, [0] * R, [n], ids=[4])
+
+
 def test_attend_where_nothing_is_seen():
     # every page of a request out of range: rows of zeros
     torch, pm = T(), M()

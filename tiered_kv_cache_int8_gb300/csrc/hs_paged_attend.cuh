@@ -467,6 +467,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (tid == 0) pre[p.n_req] = all;
     if (err && blockIdx.x == 0) set_error(p.dev_error, err);
     unsound = __syncthreads_or(err != 0);
+    if (unsound) {                               // offsets that decrease may let requests claim rows twice, without a bound
+      long long rows = 0;
+      for (int i = i0; i < i1; ++i) rows += request_of(p, i, &err).n;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) rows += __shfl_xor_sync(FULL_MASK, rows, o);
+      if (lane == 0) part[warp] = rows;
+      __syncthreads();
+      rows = 0;
+      for (int t = 0; t < C::WARPS; ++t) rows += part[t];
+      if (rows > p.n_tok) all = unsound = 0;     // nobody gets any (blocks may have left 32 bits)
+      __syncthreads();
+    }
     const int chunk = (all + C::THREADS - 1) / C::THREADS;
     const int b0 = min(all, tid * chunk), b1 = min(all, b0 + chunk);
     auto request_at = [&](int b) {               // the last request with pre <= b that has blocks
