@@ -504,7 +504,8 @@ int hs_rotary_apply(const hs_rotary_t* rot, int32_t type, int32_t d, int32_t n_t
  * element's code is round(x / s) + 8 (ties to even, the rounded quotient in [-7, 7]; 8 where s
  * is 0), so that a row stands for (code - 8) * s * kv_scale.  A NaN makes its 16 elements NaN;
  * infinities saturate, as s does beyond 448 * 7 * kv_scale; 16 elements all below 2^-10 * 7 *
- * kv_scale become 0.  A layer's pages are bytes [n_pages][2][h_kv][page_size / 16][9 d], the 9 d
+ * kv_scale become 0.  Below 2^-6, s is a multiple of 2^-9: rows whose largest of 16 elements is under 0.11 *
+ * kv_scale are held less exactly, so kv_scale is best small enough to keep them above.  A layer's pages are bytes [n_pages][2][h_kv][page_size / 16][9 d], the 9 d
  * of 16 positions i of a head being
  *   keys  : codes [i][d / 2], then scales [i][d / 16]
  *   values: codes [d / 32][i][16], then scales [d / 16][i]
@@ -546,8 +547,9 @@ void hs_paged_destroy(hs_paged_t* h);
  * handle's next call on (host memory only; not while another thread uses the handle).  Without it,
  * and with 0 and NULL, a score is s = softmax_scale * q_h . K_n; else
  *   softcap : 0 (none), or in [1e-4, 1e6]:  s becomes softcap * tanh(s / softcap), to 2^-19 of itself
- *   slopes  : NULL, or dev float [h_q], finite, the caller's until the handle is destroyed or given
- *             others:  s then loses slopes[h] * |p - n|, p the query's position
+ *   slopes  : NULL, or dev float [h_q], at most 1e30 in magnitude, the caller's until the handle is
+ *             destroyed or given others:  s then loses slopes[h] * |p - n|, p the query's position (to
+ *             2^-22 of the product and, for many tokens, 2^-18 of slopes[h])
  */
 int hs_paged_set_scores(hs_paged_t* h, float softcap, const float* slopes);
 

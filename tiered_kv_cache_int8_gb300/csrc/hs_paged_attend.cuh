@@ -223,7 +223,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // tanh(x) / x as a polynomial of x^2, the one with the least relative error on its range (found by
-// exchange): 5.4e-7 for |x| <= 1/2, 5.9e-7 for |x| <= 1.  Six or eight products a score, where e^2x and its
+// exchange): 5.5e-7 for |x| <= 1/2, 6.2e-7 for |x| <= 1, and 7.6e-7 with the roundings of 32 bits.  Six or eight products a score, where e^2x and its
 // reciprocal would cost two special functions and as many (a tile of 128 scores a thread: 8000 cycles).
 template <int N>
 __device__ __forceinline__ F2 capped2(F2 s, F2 mul, float cap) {

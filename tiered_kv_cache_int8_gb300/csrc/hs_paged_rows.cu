@@ -12,9 +12,12 @@
 // up to 3.5 steps off.  7 / amax would waste the code 0 (-8), which rows may hold but none is given:
 // levels that are symmetric about zero keep signs fair.
 //
-// Bound: instructions (70 to 75 % of the issue slots).  Measured (GB300): 23.6 K ragged tokens of 8 + 8
-// heads of 128, fp16, stored in 54 us (a copy of the bytes: 19 us; 86 us with four elements a lane and
-// divisions) and read back in 33 us (19 us); 16 tokens 2.8 us each way.
+// Bound: instructions (70 to 77 % of the issue slots).  Measured (GB300): 24.1 K ragged tokens of 8 + 8
+// heads of 128, fp16, stored in 60 us (a copy of the bytes: 19 us; 86 us with four elements a lane and
+// divisions; 63 us where blocks are quiet enough to be clamped) and read back in 32 us (19 us), from 8-bit
+// pages in 31 us (22 us), from 16-bit ones in 33 us (29 us).  With a rotation and 32 heads of queries: 243 us
+// (77 us; into 8-bit pages, by their own kernel, 85 us); the sines of a lane's eight elements are worked out
+// anew for every four of its rows.  16 tokens 2.8 us each way.
 #include "hs_paged_attention.cuh"
 #include "hs_paged_place.cuh"
 

@@ -206,7 +206,8 @@ class PagedKVCache:
     tokens and of one token, and its rows as values.
 
     kv_dtype   : of the pages: dtype, torch.float8_e4m3fn or "int4"; the last two with kv_scale,
-                 float32 [n_layers, 2 (keys, values), h_kv]: what a stored 1 stands for
+                 float32 [n_layers, 2 (keys, values), h_kv]: what a stored 1 stands for ("int4": best
+                 where the largest of 16 neighbours in a row is from 0.11 to 3136 of it)
     pages      : [n_layers, n_pages, 2, h_kv, page_size, d] (given, or allocated here); "int4":
                  bytes [n_layers, n_pages, 2, h_kv, page_size // 16, 9 * d] (include/hs.h has their order)
     softcap    : scores become softcap * tanh(score / softcap); 0: they stay
